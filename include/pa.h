@@ -99,6 +99,8 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT4 = 2 } pa_kv_dtype;
 #define PA_DEVERR_SLOT         4   /* slot_mapping entry >= nblocks * block_size    */
 #define PA_DEVERR_FP8_CONFLICT 8   /* two tokens of one FP8/4-bit write, one slot    */
 #define PA_DEVERR_TIMEOUT      16  /* an internal pipeline wait gave up             */
+#define PA_DEVERR_QUERY        32  /* query_offsets falls, or leaves [0, total_queries] */
+#define PA_DEVERR_POSITION     64  /* a token's position outside the rotation table */
 
 typedef struct {
     int32_t B;            /* sequences (decode) or tokens to write (cache write) */
@@ -433,6 +435,99 @@ pa_status pa_quest_select(const pa_shape *shape, const void *q, const void *key_
                           const int32_t *block_tables, const int32_t *seq_lens, int32_t topk,
                           float *page_scores, int32_t *selected_pages, int32_t *err_flag,
                           pa_stream_t stream);
+
+/*
+ * Calls with several new tokens per sequence: the rotation and the write of a call's tokens,
+ * and their attention.  A prompt, a chunk of one, or a few speculated tokens go through
+ * pa_rope_and_cache and then pa_extend; a decoder's cross-attention layers read an encoder's
+ * cached states through pa_cross_attend.  (A single token per sequence: pa_decode.)
+ */
+
+/* How pa_rope_and_cache turns a head, and how its inputs lie in memory. */
+typedef struct {
+    int32_t rotary_dim;       /* channels [0, rotary_dim) turn: a multiple of 16, <= D  */
+    int32_t interleaved;      /* 0: pair j is channels (j, j + rotary_dim / 2);
+                                 1: channels (2j, 2j + 1)                               */
+    int32_t num_positions;    /* rows of cos_sin                                        */
+    int64_t q_stride;         /* elements from one token to the next in q, k_new and    */
+    int64_t k_stride;         /*   v_new, multiples of 8 (slices of one projection's    */
+    int64_t v_stride;         /*   output, say); 0: dense                               */
+} pa_rope;
+
+/*
+ * pa_rope_and_cache -- rotate the queries and keys of a call's tokens by their positions and
+ * write the rotated keys and the values to the cache.  For every token t < shape->B with
+ * s = slot_mapping[t] >= 0, every head and every pair j < rotary_dim / 2 of its channels (a, b):
+ *     a' = a c - b s,  b' = b c + a s,   c, s = cos_sin[positions[t]][j], [rotary_dim / 2 + j]
+ * in fp32 (each product and sum rounded), rounded once to bf16; the other channels are copied.
+ * q_out holds the rotated queries; the rotated keys and the values are written as by
+ * pa_reshape_and_cache with k_new = the rotated keys (bf16, E4M3 and 4-bit pools: the same
+ * bytes and scales).
+ *   cos_sin [num_positions, rotary_dim] fp32: cosines, then sines, of each position's angles
+ *     (any frequencies and scaling the caller puts in);
+ *   positions [B] int32; slot_mapping [B] int64;
+ *   q [B, Hq, D], k_new and v_new [B, Hkv, D] bf16, heads dense, tokens `*_stride` apart;
+ *   q_out [B, Hq, D] bf16, dense.  q_out may be q (dense) and must not overlap it otherwise.
+ *     Both NULL: keys and values only.
+ * A token with a negative slot is padding: nothing of it is written, q_out neither.  A slot
+ * beyond the pool sets PA_DEVERR_SLOT, a position outside the table PA_DEVERR_POSITION; such a
+ * token is skipped like padding.
+ */
+pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const float *cos_sin,
+                            const int32_t *positions, void *q_out, const void *q,
+                            const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                            float *k_scale, float *v_scale, const int64_t *slot_mapping,
+                            int32_t *err_flag, pa_stream_t stream);
+
+/*
+ * pa_extend -- attention of the tokens that a call appends, over the paged cache that already
+ * holds them (pa_rope_and_cache first).  Sequence b's query tokens are rows
+ * query_offsets[b] .. query_offsets[b + 1) of q and out, n_b of them, and they are the last n_b
+ * of its seq_lens[b] cached tokens: row i of them sits at position p = seq_lens[b] - n_b + i and
+ * sees the positions j <= p (window > 0: p - window < j <= p).
+ *     out[row][h][:] = sum_j softmax_j(sm_scale * <q[row][h], K_b[j]>) V_b[j]
+ * with K_b, V_b gathered through the block table and restored as in pa_decode, KV head h / G.
+ *   q, out         [total_queries, Hq, D] bf16 (out must not overlap q)
+ *   query_offsets  [B + 1] int32, not falling, within [0, total_queries]; rows before the first
+ *                  and from the last offset on are left as they were.  n_b may be 0.
+ *   workspace      device memory of pa_attend_workspace_bytes bytes, 256-byte aligned; calls
+ *                  that may overlap on the GPU need one each
+ * Cached values must be finite at the positions [seq_lens[b] - n_b - window + 1, seq_lens[b])
+ * that some token of the call sees; other rows, and blocks wholly outside them, may hold
+ * anything.  Block-table entries of blocks before every token's window are not read.
+ * Errors found on the device: a block id outside the pool reads zeros (PA_DEVERR_BLOCK_ID); a
+ * length beyond the block table is clamped, and a sequence with more query than cached tokens
+ * gets zeros (PA_DEVERR_SEQ_LEN); a sequence whose offsets fall or leave the rows is skipped
+ * (PA_DEVERR_QUERY).
+ * Rounding: q K^T and the sums are fp32; the weights enter the second product as bf16.  The
+ * result is the same on every call, bit for bit.  Batches of more than 16384 sequences, and
+ * quantised pools, return PA_ERR_UNSUPPORTED.
+ */
+pa_status pa_extend(const pa_shape *shape, void *out, const void *q, const int32_t *query_offsets,
+                    int32_t total_queries, const void *k_pool, const void *v_pool,
+                    const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                    const int32_t *seq_lens, int32_t window, float sm_scale, void *workspace,
+                    size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream);
+
+/*
+ * pa_cross_attend -- the same attention without order: every query token of sequence b sees all
+ * seq_lens[b] cached tokens (an encoder's states, written by pa_reshape_and_cache; their number
+ * has nothing to do with n_b).  seq_lens[b] = 0 gives zeros.  Several sequences may name the
+ * same blocks.
+ */
+pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
+                          const int32_t *query_offsets, int32_t total_queries,
+                          const void *k_pool, const void *v_pool, const float *k_scale,
+                          const float *v_scale, const int32_t *block_tables,
+                          const int32_t *seq_lens, float sm_scale, void *workspace,
+                          size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream);
+
+/*
+ * Bytes of pa_extend's and pa_cross_attend's workspace for this shape and number of query rows
+ * on a GPU with sm_count SMs; 0 if the arguments are invalid.  It does not depend on the
+ * lengths.  Nothing in it needs initialising, and it keeps nothing for a later call.  Host only.
+ */
+size_t pa_attend_workspace_bytes(const pa_shape *shape, int32_t total_queries, int32_t sm_count);
 
 /* Human-readable name of a status. */
 const char *pa_status_string(pa_status status);

@@ -17,12 +17,14 @@ PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_DEVICE = rang
 PA_KV_BF16, PA_KV_FP8_E4M3, PA_KV_INT4 = 0, 1, 2
 PA_DEVERR_BLOCK_ID, PA_DEVERR_SEQ_LEN, PA_DEVERR_SLOT = 1, 2, 4
 PA_DEVERR_FP8_CONFLICT, PA_DEVERR_TIMEOUT = 8, 16
+PA_DEVERR_QUERY, PA_DEVERR_POSITION = 32, 64
 
 EXPORTED = ("pa_reshape_and_cache", "pa_decode", "pa_splitkv_workspace_bytes",
             "pa_default_num_splits", "pa_decode_splitkv", "pa_merge_lse", "pa_status_string",
             "pa_read_error_flag", "pa_decode_splitkv_noalloc", "pa_quest_summarize",
             "pa_quest_select", "pa_cascade_workspace_bytes", "pa_decode_workspace_bytes",
-            "pa_default_num_segments")
+            "pa_default_num_segments", "pa_rope_and_cache", "pa_extend", "pa_cross_attend",
+            "pa_attend_workspace_bytes")
 PA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -31,6 +33,12 @@ class pa_shape(ctypes.Structure):
                 ("D", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("nblocks", ctypes.c_int32), ("max_blocks", ctypes.c_int32),
                 ("kv_dtype", ctypes.c_int32)]
+
+
+class pa_rope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("num_positions", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
 
 
 class pa_decode_opts(ctypes.Structure):
@@ -104,6 +112,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
             "pa_quest_summarize": (I32, [S, P, P, P, P, P, P]),
             "pa_quest_select": (I32, [S, P, P, P, P, I32, P, P, P, P]),
             "pa_cascade_workspace_bytes": (ctypes.c_size_t, [S]),
+            "pa_rope_and_cache": (I32, [S, ctypes.POINTER(pa_rope)] + [P] * 13),
+            "pa_extend": (I32, [S, P, P, P, I32, P, P, P, P, P, P, I32, F, P, ctypes.c_size_t, P,
+                                P]),
+            "pa_cross_attend": (I32, [S, P, P, P, I32, P, P, P, P, P, P, F, P, ctypes.c_size_t, P,
+                                      P]),
+            "pa_attend_workspace_bytes": (ctypes.c_size_t, [S, I32, I32]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -132,6 +146,18 @@ def _ptr(t):
     if not t.is_contiguous():
         raise ValueError("libpa takes contiguous tensors only")
     return t.data_ptr()
+
+
+def _token_ptr(t):
+    """(device pointer, elements from one token to the next) of a [T, H, D] CUDA tensor whose
+    heads are dense, e.g. a slice of a fused projection's output (None -> NULL)."""
+    if t is None or isinstance(t, int):
+        return t, 0
+    if not t.is_cuda:
+        raise ValueError("libpa takes CUDA tensors only")
+    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        raise ValueError("libpa takes [tokens, heads, D] tensors with dense heads")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
 
 
 def _stream(stream):
@@ -262,3 +288,48 @@ def pa_quest_select(shape: pa_shape, q, key_summaries, block_tables, seq_lens, t
     _check("pa_quest_select", lib.pa_quest_select(
         ctypes.byref(shape), _ptr(q), _ptr(key_summaries), _ptr(block_tables), _ptr(seq_lens),
         int(topk), _ptr(page_scores), _ptr(selected_pages), _ptr(err_flag), _stream(stream)))
+
+
+def pa_rope_and_cache(shape: pa_shape, cos_sin, positions, q_out, q, k_new, v_new, k_pool, v_pool,
+                      k_scale, v_scale, slot_mapping, err_flag=None, stream=None,
+                      interleaved: bool = False) -> None:
+    """cos_sin: [positions, rotary_dim] fp32 (see device.rope_table); q, k_new and v_new may be
+    slices of one [T, heads, D] tensor.  q = q_out = None: keys and values only."""
+    lib = load()
+    (qp, qs), (kp, ks), (vp, vs) = _token_ptr(q), _token_ptr(k_new), _token_ptr(v_new)
+    rows, width = cos_sin.shape
+    rope = pa_rope(int(width), int(bool(interleaved)), int(rows), qs, ks, vs)
+    _check("pa_rope_and_cache", lib.pa_rope_and_cache(
+        ctypes.byref(shape), ctypes.byref(rope), _ptr(cos_sin), _ptr(positions), _ptr(q_out), qp,
+        kp, vp, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
+        _ptr(err_flag), _stream(stream)))
+
+
+def pa_attend_workspace_bytes(shape: pa_shape, total_queries: int, sm_count: int) -> int:
+    return int(load().pa_attend_workspace_bytes(ctypes.byref(shape), int(total_queries),
+                                                int(sm_count)))
+
+
+def pa_extend(shape: pa_shape, out, q, query_offsets, k_pool, v_pool, k_scale, v_scale,
+              block_tables, seq_lens, sm_scale: float, workspace, err_flag=None, stream=None,
+              window: int = 0) -> None:
+    """q, out: [total_queries, Hq, D] bf16; query_offsets: [B + 1] int32; workspace: uint8 tensor
+    of pa_attend_workspace_bytes."""
+    lib = load()
+    _check("pa_extend", lib.pa_extend(
+        ctypes.byref(shape), _ptr(out), _ptr(q), _ptr(query_offsets), int(q.shape[0]),
+        _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        _ptr(seq_lens), int(window), float(sm_scale), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+
+
+def pa_cross_attend(shape: pa_shape, out, q, query_offsets, k_pool, v_pool, k_scale, v_scale,
+                    block_tables, seq_lens, sm_scale: float, workspace, err_flag=None,
+                    stream=None) -> None:
+    """As pa_extend, every query token seeing all of its sequence's cached tokens."""
+    lib = load()
+    _check("pa_cross_attend", lib.pa_cross_attend(
+        ctypes.byref(shape), _ptr(out), _ptr(q), _ptr(query_offsets), int(q.shape[0]),
+        _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        _ptr(seq_lens), float(sm_scale), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))

@@ -102,6 +102,40 @@ pa_status current_sm_count(int *sms) {
   return PA_OK;
 }
 
+pa_status check_attend_shape(const pa_shape *s, int32_t total_queries) {
+  const pa_status st = check_shape(s, true);
+  if (st != PA_OK) return st;
+  if (total_queries < 0 || static_cast<int64_t>(total_queries) * s->Hq >= (int64_t(1) << 31))
+    return PA_ERR_INVALID_ARG;
+  // key positions are counted in int32
+  if (static_cast<int64_t>(s->max_blocks) * s->block_size >= (int64_t(1) << 30))
+    return PA_ERR_INVALID_ARG;
+  return s->B > pa::kMaxSplitBatch ? PA_ERR_UNSUPPORTED : PA_OK;
+}
+
+// pa_extend (causal) and pa_cross_attend.
+pa_status attend(const pa_shape *shape, void *out, const void *q, const int32_t *query_offsets,
+                 int32_t total_queries, const void *k_pool, const void *v_pool,
+                 const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                 const int32_t *seq_lens, bool causal, int32_t window, float sm_scale,
+                 void *workspace, size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream) {
+  pa_status st = check_attend_shape(shape, total_queries);
+  if (st != PA_OK) return st;
+  if (window < 0) return PA_ERR_INVALID_ARG;
+  if (shape->B == 0 || total_queries == 0) return PA_OK;
+  st = check_ptrs({out, q, query_offsets, k_pool, v_pool, block_tables, seq_lens, workspace});
+  if (st != PA_OK) return st;
+  if (shape->kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
+  int sms = 0;
+  if (current_sm_count(&sms) != PA_OK) return PA_ERR_CUDA;
+  if (workspace_bytes < pa::attend_workspace_bytes(*shape, total_queries, sms))
+    return PA_ERR_INVALID_ARG;
+  return pa::run_attend(*shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale,
+                        v_scale, block_tables, seq_lens, causal, window, sm_scale, workspace, sms,
+                        err_flag, reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -252,6 +286,63 @@ pa_status pa_quest_select(const pa_shape *shape, const void *q, const void *key_
   return pa::run_quest_select(*shape, q, key_summaries, block_tables, seq_lens, topk,
                               page_scores, selected_pages, err_flag,
                               reinterpret_cast<cudaStream_t>(stream));
+}
+
+pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const float *cos_sin,
+                            const int32_t *positions, void *q_out, const void *q,
+                            const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                            float *k_scale, float *v_scale, const int64_t *slot_mapping,
+                            int32_t *err_flag, pa_stream_t stream) {
+  pa_status st = check_shape(shape, true);
+  if (st != PA_OK) return st;
+  if (!rope || rope->rotary_dim <= 0 || rope->rotary_dim > shape->D || rope->num_positions <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (rope->rotary_dim % 16) return PA_ERR_UNSUPPORTED;
+  auto bad_stride = [&](int64_t stride, int heads) {
+    return stride != 0 && (stride < static_cast<int64_t>(heads) * shape->D || stride % 8);
+  };
+  if (bad_stride(rope->q_stride, shape->Hq) || bad_stride(rope->k_stride, shape->Hkv) ||
+      bad_stride(rope->v_stride, shape->Hkv))
+    return PA_ERR_INVALID_ARG;
+  if (shape->B == 0) return PA_OK;
+  st = check_ptrs({cos_sin, positions, k_new, v_new, k_pool, v_pool, slot_mapping});
+  if (st != PA_OK) return st;
+  if ((q != nullptr) != (q_out != nullptr) || !aligned16(q) || !aligned16(q_out))
+    return PA_ERR_INVALID_ARG;
+  if (q && q == q_out && rope->q_stride != 0 &&
+      rope->q_stride != static_cast<int64_t>(shape->Hq) * shape->D)
+    return PA_ERR_INVALID_ARG;
+  if (shape->kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  return pa::run_rope_and_cache(*shape, *rope, cos_sin, positions, q_out, q, k_new, v_new, k_pool,
+                                v_pool, k_scale, v_scale, slot_mapping, err_flag,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t pa_attend_workspace_bytes(const pa_shape *shape, int32_t total_queries, int32_t sm_count) {
+  if (check_attend_shape(shape, total_queries) != PA_OK || sm_count < 1 || sm_count > kMaxSplits)
+    return 0;
+  return pa::attend_workspace_bytes(*shape, total_queries, sm_count);
+}
+
+pa_status pa_extend(const pa_shape *shape, void *out, const void *q, const int32_t *query_offsets,
+                    int32_t total_queries, const void *k_pool, const void *v_pool,
+                    const float *k_scale, const float *v_scale, const int32_t *block_tables,
+                    const int32_t *seq_lens, int32_t window, float sm_scale, void *workspace,
+                    size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream) {
+  return attend(shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale, v_scale,
+                block_tables, seq_lens, true, window, sm_scale, workspace, workspace_bytes,
+                err_flag, stream);
+}
+
+pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
+                          const int32_t *query_offsets, int32_t total_queries,
+                          const void *k_pool, const void *v_pool, const float *k_scale,
+                          const float *v_scale, const int32_t *block_tables,
+                          const int32_t *seq_lens, float sm_scale, void *workspace,
+                          size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream) {
+  return attend(shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale, v_scale,
+                block_tables, seq_lens, false, 0, sm_scale, workspace, workspace_bytes, err_flag,
+                stream);
 }
 
 const char *pa_status_string(pa_status status) {

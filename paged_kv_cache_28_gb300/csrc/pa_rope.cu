@@ -1,0 +1,346 @@
+// pa_rope.cu -- the position rotation of a call's queries and keys, and the slot-mapped write
+// of the rotated keys and the values (pa_rope_and_cache), in one pass.
+//
+// Pair j of a head's first `rotary_dim` channels turns by the angle whose cosine and sine the
+// caller's table holds for the token's position:
+//     a' = a cos - b sin,   b' = b cos + a sin
+// in fp32 with each product and sum rounded (no fused multiply-add, so that the bits are those
+// of the written formula), rounded once to bf16.  The rotated keys and the values then go to
+// the cache exactly as pa_reshape_and_cache would write them.
+//
+// Nothing here is reused but the table row of a token, so the kernels are bound by HBM: each
+// vector is read once and written once.
+#include "pa_codec.cuh"
+#include "pa_common.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+struct RopeParams {
+  const float *cos_sin;
+  const int32_t *positions;
+  const int64_t *slots;
+  uint16_t *q_out;
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  uint8_t *k_pool, *v_pool;
+  float *k_scale, *v_scale;
+  int32_t *err;
+  int T, Hq, Hkv, r, num_positions, bs, nblocks;
+};
+
+// (a, b) turned by (c, s)
+__device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
+  return make_float2(__fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)),
+                     __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
+}
+
+// Whether token t is written: a slot in the pool and a position in the table.
+__device__ __forceinline__ bool token_ok(const RopeParams &p, int t, int64_t slot, bool report) {
+  if (slot < 0) return false;                            // padding
+  int bits = 0;
+  if (slot >= static_cast<int64_t>(p.nblocks) * p.bs) bits |= PA_DEVERR_SLOT;
+  const int pos = p.positions[t];
+  if (pos < 0 || pos >= p.num_positions) bits |= PA_DEVERR_POSITION;
+  if (bits && report) set_err(p.err, bits);
+  return bits == 0;
+}
+
+// One thread's share of a head: 16 channels as two 16-byte chunks that hold eight whole pairs.
+struct Item {
+  int c0, c1;            // first channels of the chunks
+  bool rotates;
+  float cos[8], sin[8];
+};
+
+template <bool kInterleaved>
+__device__ __forceinline__ void load_item(const RopeParams &p, int item, int pos, Item &x) {
+  x.rotates = item < p.r / 16;
+  const bool split = x.rotates && !kInterleaved;         // pairs (j, j + r / 2)
+  x.c0 = split ? 8 * item : 16 * item;
+  x.c1 = split ? p.r / 2 + 8 * item : 16 * item + 8;
+  if (!x.rotates) return;
+  const float4 *row =
+      reinterpret_cast<const float4 *>(p.cos_sin + static_cast<int64_t>(pos) * p.r + 8 * item);
+  const float4 *sin_row = row + p.r / 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    *reinterpret_cast<float4 *>(x.cos + 4 * i) = __ldg(row + i);
+    *reinterpret_cast<float4 *>(x.sin + 4 * i) = __ldg(sin_row + i);
+  }
+}
+
+template <bool kInterleaved>
+__device__ __forceinline__ void rotate_item(const Item &x, uint4 &a, uint4 &b) {
+  uint32_t *u = reinterpret_cast<uint32_t *>(&a), *w = reinterpret_cast<uint32_t *>(&b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kInterleaved) {
+      const float2 y = turn(bf16_lo(u[i]), bf16_hi(u[i]), x.cos[i], x.sin[i]);
+      const float2 z = turn(bf16_lo(w[i]), bf16_hi(w[i]), x.cos[4 + i], x.sin[4 + i]);
+      u[i] = pack_bf16(y.x, y.y);
+      w[i] = pack_bf16(z.x, z.y);
+    } else {
+      const float2 y = turn(bf16_lo(u[i]), bf16_lo(w[i]), x.cos[2 * i], x.sin[2 * i]);
+      const float2 z = turn(bf16_hi(u[i]), bf16_hi(w[i]), x.cos[2 * i + 1], x.sin[2 * i + 1]);
+      u[i] = pack_bf16(y.x, z.x);
+      w[i] = pack_bf16(y.y, z.y);
+    }
+  }
+}
+
+// Heads first, first + step, ... < last of token t, counted through the queries, then (bf16
+// pools) the keys and the values; this thread's item of each.  Four heads' loads are in flight
+// at once.
+template <int D, bool kInterleaved>
+__device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int64_t slot, const Item &x,
+                                           int first, int step, int last) {
+  constexpr int U = 4;
+  for (int h0 = first; h0 < last; h0 += step * U) {
+    uint4 a[U], b[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * step;
+      if (h >= last) break;
+      const uint16_t *src = h < p.Hq ? p.q + t * p.q_stride + h * D
+                            : h < p.Hq + p.Hkv ? p.k + t * p.k_stride + (h - p.Hq) * D
+                                               : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * D;
+      a[i] = *reinterpret_cast<const uint4 *>(src + x.c0);
+      b[i] = *reinterpret_cast<const uint4 *>(src + x.c1);
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * step;
+      if (h >= last) break;
+      if (x.rotates && h < p.Hq + p.Hkv) rotate_item<kInterleaved>(x, a[i], b[i]);
+      uint16_t *dst =
+          h < p.Hq ? p.q_out + (static_cast<int64_t>(t) * p.Hq + h) * D
+          : h < p.Hq + p.Hkv
+              ? reinterpret_cast<uint16_t *>(p.k_pool) + (slot * p.Hkv + h - p.Hq) * D
+              : reinterpret_cast<uint16_t *>(p.v_pool) + (slot * p.Hkv + h - p.Hq - p.Hkv) * D;
+      *reinterpret_cast<uint4 *>(dst + x.c0) = a[i];
+      *reinterpret_cast<uint4 *>(dst + x.c1) = b[i];
+    }
+  }
+}
+
+// BF16 pools: blockIdx.x is the token; blockIdx.y a share of its heads.
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kItems = D / 16, kHeads = 128 / kItems;
+  const int t = blockIdx.x;
+  const int64_t slot = p.slots[t];
+  if (!token_ok(p, t, slot, threadIdx.x == 0 && blockIdx.y == 0)) return;
+  Item x;
+  load_item<kInterleaved>(p, threadIdx.x % kItems, p.positions[t], x);
+  rope_heads<D, kInterleaved>(p, t, slot, x, (p.q ? 0 : p.Hq) + blockIdx.y * kHeads + threadIdx.x / kItems,
+                              gridDim.y * kHeads, p.Hq + 2 * p.Hkv);
+}
+
+// Quantised pools (D = 128).  CTAs [0, T) write the cache: as in pa_reshape_and_cache, the
+// first token of the call in a block (its leader) applies every token of the call in that
+// block, in token order; the others leave.  A warp takes (KV head, K or V) jobs, a lane four
+// consecutive channels.  The codes of a job's rows stay in shared memory while its tokens are
+// applied, so a token that raises the scale costs no trip to the pool, and each row is written
+// once.  CTAs [T, 2 T) rotate the queries.
+template <class Codec, bool kInterleaved>
+__global__ void __launch_bounds__(256) rope_quant_kernel(const RopeParams p) {
+  using Word = typename Codec::Word;
+  constexpr int D = 128, kWarps = 8, kBatch = 8;
+  __shared__ int members[256];      // this chunk's tokens of the block, in token order
+  __shared__ int member_off[256];
+  __shared__ int warp_count[kWarps];
+  __shared__ uint32_t offsets_seen;
+  __shared__ Word codes[kWarps][32][32];                 // a job's rows: one word per lane
+  pdl_trigger();
+  pdl_wait();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x >= p.T) {
+    const int t = blockIdx.x - p.T;
+    if (!token_ok(p, t, p.slots[t], false)) return;
+    Item x;
+    load_item<kInterleaved>(p, tid % 8, p.positions[t], x);
+    rope_heads<D, kInterleaved>(p, t, 0, x, tid / 8, 32, p.Hq);
+    return;
+  }
+  const int t = blockIdx.x;
+  const int64_t slot = p.slots[t];
+  if (!token_ok(p, t, slot, tid == 0)) return;
+  const int64_t nslots = static_cast<int64_t>(p.nblocks) * p.bs;
+  const int64_t blk = slot / p.bs, blk0 = blk * p.bs;
+  auto in_block = [&](int u, int64_t o) {
+    return o >= blk0 && o < blk0 + p.bs && o < nslots && token_ok(p, u, o, false);
+  };
+  // A token right after another of its block (a prompt's tokens fill their blocks in order)
+  // leaves at once; the others look through the call: an earlier token of the block leads it,
+  // and without a later one past the first 256 tokens one look is enough.
+  if (t > 0 && in_block(t - 1, p.slots[t - 1])) return;
+  int earlier = 0, later = 0;
+#pragma unroll 4
+  for (int u = tid; u < t - 1; u += 256) earlier |= in_block(u, p.slots[u]);
+  if (__syncthreads_or(earlier)) return;
+#pragma unroll 4
+  for (int u = t + 256 + tid; u < p.T; u += 256) later |= in_block(u, p.slots[u]);
+  const int end = __syncthreads_or(later) ? p.T : min(p.T, t + 256);
+  if (tid == 0) offsets_seen = 0u;
+  for (int c0 = t; c0 < end; c0 += 256) {
+    // the chunk's tokens of this block, in token order (ballot compaction)
+    const int u = c0 + tid;
+    const int64_t o = u < p.T ? p.slots[u] : -1;
+    const bool mine = u < p.T && in_block(u, o);
+    const uint32_t ballot = __ballot_sync(0xffffffffu, mine);
+    if (lane == 0) warp_count[warp] = __popc(ballot);
+    __syncthreads();
+    int before = 0, n = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      before += w < warp ? warp_count[w] : 0;
+      n += warp_count[w];
+    }
+    if (mine) {
+      const int i = before + __popc(ballot & ((1u << lane) - 1u));
+      const int off = static_cast<int>(o - blk0);
+      members[i] = u;
+      member_off[i] = off;
+      // a second token for one slot: applied after the first, and reported
+      if (atomicOr(&offsets_seen, 1u << off) & (1u << off)) set_err(p.err, PA_DEVERR_FP8_CONFLICT);
+    }
+    __syncthreads();
+    for (int job = warp; job < 2 * p.Hkv; job += kWarps) {
+      const int h = job >> 1;
+      const bool is_v = job & 1;
+      uint8_t *pool = is_v ? p.v_pool : p.k_pool;
+      float *scale = (is_v ? p.v_scale : p.k_scale) + blk * p.Hkv + h;
+      const uint16_t *src = (is_v ? p.v : p.k) + h * D + lane * 4;
+      const int64_t stride = is_v ? p.v_stride : p.k_stride;
+      auto word = [&](int r) {
+        return reinterpret_cast<Word *>(pool + ((blk0 + r) * p.Hkv + h) * int64_t(Codec::kRowBytes) +
+                                        lane * sizeof(Word));
+      };
+      float s = *scale;
+      uint32_t held = 0;                                 // rows whose codes are in shared memory
+      for (int i0 = 0; i0 < n; i0 += kBatch) {
+        uint2 raw[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (i0 + i < n) raw[i] = *reinterpret_cast<const uint2 *>(src + members[i0 + i] * stride);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          if (i0 + i >= n) break;
+          const int off = member_off[i0 + i];
+          float v[4] = {bf16_lo(raw[i].x), bf16_hi(raw[i].x), bf16_lo(raw[i].y), bf16_hi(raw[i].y)};
+          if (!is_v) {
+            // the lane's own angles: four pairs half a rotation apart (the partner channels are
+            // r / 8 lanes away), or two neighbouring pairs
+            const bool turns = lane * 4 < p.r;
+            const bool upper = !kInterleaved && lane * 4 >= p.r / 2;
+            const float *row = p.cos_sin + static_cast<int64_t>(p.positions[members[i0 + i]]) * p.r;
+            if constexpr (kInterleaved) {
+              if (turns) {
+                const float2 c = __ldg(reinterpret_cast<const float2 *>(row) + lane);
+                const float2 sn = __ldg(reinterpret_cast<const float2 *>(row + p.r / 2) + lane);
+                const float2 y = turn(v[0], v[1], c.x, sn.x), z = turn(v[2], v[3], c.y, sn.y);
+                v[0] = y.x, v[1] = y.y, v[2] = z.x, v[3] = z.y;
+              }
+            } else {
+              const int peer = (upper ? lane - p.r / 8 : lane + p.r / 8) & 31;
+              float w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[e] = __shfl_sync(0xffffffffu, v[e], peer);
+              if (turns) {
+                const int j = lane * 4 - (upper ? p.r / 2 : 0);
+                const float4 c = __ldg(reinterpret_cast<const float4 *>(row + j));
+                const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2 + j));
+                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  v[e] = upper ? turn(w[e], v[e], cc[e], ss[e]).y : turn(v[e], w[e], cc[e], ss[e]).x;
+              }
+            }
+            if (turns) {                                 // the cache takes the bf16 key
+              const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
+              v[0] = bf16_lo(lo), v[1] = bf16_hi(lo), v[2] = bf16_lo(hi), v[3] = bf16_hi(hi);
+            }
+          }
+          float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+          for (int sh = 16; sh > 0; sh >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, sh));
+          const float cand = __fdiv_rn(amax, Codec::kMaxCode);
+          const float s_new = (off == 0 || cand > s) ? cand : s;
+          if (off > 0 && s_new > s) {
+            for (int r = 0; r < off; ++r) {
+              const Word c = held >> r & 1 ? codes[warp][r][lane] : *word(r);
+              codes[warp][r][lane] = Codec::reencode(c, s, s_new);
+            }
+            held |= (1u << off) - 1u;
+          }
+          codes[warp][off][lane] = Codec::encode(v, s_new);
+          held |= 1u << off;
+          s = s_new;
+        }
+      }
+      for (int r = 0; r < p.bs; ++r)
+        if (held >> r & 1) *word(r) = codes[warp][r][lane];
+      if (lane == 0) *scale = s;
+    }
+    __syncthreads();   // the member lists and the scales are reused by the next chunk
+  }
+}
+
+template <int D, bool I>
+cudaError_t launch_bf16(const RopeParams &p, cudaStream_t stream) {
+  return launch_pdl(rope_bf16_kernel<D, I>, dim3(p.T), dim3(128), 0, stream, p);
+}
+
+template <class Codec, bool I>
+cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
+  return launch_pdl(rope_quant_kernel<Codec, I>, dim3(p.q ? 2 * p.T : p.T), dim3(256), 0, stream, p);
+}
+
+}  // namespace
+
+pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const float *cos_sin,
+                             const int32_t *positions, void *q_out, const void *q,
+                             const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                             float *k_scale, float *v_scale, const int64_t *slot_mapping,
+                             int32_t *err, cudaStream_t stream) {
+  RopeParams p{};
+  p.cos_sin = cos_sin;
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.q_out = static_cast<uint16_t *>(q_out);
+  p.q = static_cast<const uint16_t *>(q);
+  p.k = static_cast<const uint16_t *>(k_new);
+  p.v = static_cast<const uint16_t *>(v_new);
+  p.q_stride = rope.q_stride ? rope.q_stride : static_cast<int64_t>(s.Hq) * s.D;
+  p.k_stride = rope.k_stride ? rope.k_stride : static_cast<int64_t>(s.Hkv) * s.D;
+  p.v_stride = rope.v_stride ? rope.v_stride : static_cast<int64_t>(s.Hkv) * s.D;
+  p.k_pool = static_cast<uint8_t *>(k_pool);
+  p.v_pool = static_cast<uint8_t *>(v_pool);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.err = err;
+  p.T = s.B;
+  p.Hq = s.Hq;
+  p.Hkv = s.Hkv;
+  p.r = rope.rotary_dim;
+  p.num_positions = rope.num_positions;
+  p.bs = s.block_size;
+  p.nblocks = s.nblocks;
+  const bool i = rope.interleaved;
+  cudaError_t e;
+  if (s.kv_dtype == PA_KV_FP8_E4M3)
+    e = i ? launch_quant<Fp8Codec, true>(p, stream) : launch_quant<Fp8Codec, false>(p, stream);
+  else if (s.kv_dtype == PA_KV_INT4)
+    e = i ? launch_quant<Int4Codec, true>(p, stream) : launch_quant<Int4Codec, false>(p, stream);
+  else if (s.D == 128)
+    e = i ? launch_bf16<128, true>(p, stream) : launch_bf16<128, false>(p, stream);
+  else
+    e = i ? launch_bf16<64, true>(p, stream) : launch_bf16<64, false>(p, stream);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace pa

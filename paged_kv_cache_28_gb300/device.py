@@ -18,6 +18,16 @@ def to_device_bf16(bits: np.ndarray, device) -> torch.Tensor:
         torch.bfloat16)
 
 
+def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0,
+               device="cuda") -> torch.Tensor:
+    """The rotation table of pa_rope_and_cache, [num_positions, rotary_dim] fp32: position p's
+    angles p base^(-2 j / rotary_dim), computed in 64 bits (in 32 a far position's angle is off
+    by 2^-24 of itself, thousandths of a radian), as cosines, then sines."""
+    f = torch.arange(0, rotary_dim, 2, device=device, dtype=torch.float64) / rotary_dim
+    angle = torch.arange(num_positions, device=device, dtype=torch.float64)[:, None] * base ** -f
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
 class DeviceBatch:
     def __init__(self, batch: Batch, device="cuda", pools=None):
         """pools: optional (k_pool, v_pool, k_scale, v_scale) device tensors to use
@@ -143,6 +153,45 @@ class DeviceBatch:
                                self.shared_prefix_lens if hints else None)
         if merge:
             _lib.pa_merge_lse(self.shape, self.out, self.o_part, self.lse, num_splits, stream)
+
+    # -- several tokens per sequence ---------------------------------------------
+
+    def rope_and_cache(self, q, k_new, v_new, positions, slot_mapping, cos_sin, q_out=None,
+                       stream=None, interleaved: bool = False) -> torch.Tensor:
+        """Rotate q [T, Hq, D] and k_new [T, Hkv, D] and append k_new, v_new to the pools;
+        returns the rotated queries."""
+        b = self.batch
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+        shape = _lib.make_shape(q.shape[0], b.Hq, b.Hkv, b.D, b.block_size, b.nblocks,
+                                b.max_blocks, self.shape.kv_dtype)
+        _lib.pa_rope_and_cache(shape, cos_sin, positions, q_out, q, k_new, v_new, self.k_pool,
+                               self.v_pool, self.k_scale, self.v_scale, slot_mapping, self.err,
+                               stream, interleaved)
+        return q_out
+
+    def attend_workspace(self, total_queries: int) -> torch.Tensor:
+        nbytes = _lib.pa_attend_workspace_bytes(self.shape, total_queries, _sm_count(self.device))
+        if getattr(self, "_attend_ws", None) is None or self._attend_ws.numel() < nbytes:
+            self._attend_ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return self._attend_ws
+
+    def extend(self, q, query_offsets, out=None, stream=None, window: int = 0) -> torch.Tensor:
+        """pa_extend of ragged query rows q [T, Hq, D] over the batch's cache."""
+        out = torch.zeros_like(q) if out is None else out
+        _lib.pa_extend(self.shape, out, q, query_offsets, self.k_pool, self.v_pool, self.k_scale,
+                       self.v_scale, self.block_tables, self.seq_lens, self.batch.sm_scale,
+                       self.attend_workspace(q.shape[0]), self.err, stream, window)
+        return out
+
+    def cross_attend(self, q, query_offsets, out=None, stream=None) -> torch.Tensor:
+        """pa_cross_attend of ragged query rows q [T, Hq, D] over the batch's cache."""
+        out = torch.zeros_like(q) if out is None else out
+        _lib.pa_cross_attend(self.shape, out, q, query_offsets, self.k_pool, self.v_pool,
+                             self.k_scale, self.v_scale, self.block_tables, self.seq_lens,
+                             self.batch.sm_scale, self.attend_workspace(q.shape[0]), self.err,
+                             stream)
+        return out
 
     # -- Quest page selection ------------------------------------------------------
 

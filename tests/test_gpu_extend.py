@@ -1,0 +1,563 @@
+"""pa_rope_and_cache, pa_extend and pa_cross_attend on a GPU against plain 64-bit forms.
+
+Tolerances.  A rounding to bf16 is off by at most u = 2^-8 of the value (half a step).  The
+attention rounds each weight to bf16 before the second product (error <= u sum_j w_j |V_j| / sum_j
+w_j = u A) and its result once (<= u |out|).  What 32 bits add: a score is a sum of D <= 128
+products and its rounding, off by <= D 2^-24 s with s = scale sum |q k|, which is the relative
+error of its weight, above and below the fraction; sums over N keys add N 2^-24 of A on each side:
+    |out - ref| <= u |ref| + (u + 2 (D s + N + 16) 2^-24) A
+(16: the exponential's own error and the scale factors).  Where every weight is exactly 1 (q = 0)
+only the sums and the last rounding are left.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_28_gb300 as pa
+from paged_kv_cache_28_gb300.device import rope_table
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -8
+KINDS = {"bf16": pa.PA_KV_BF16, "fp8": pa.PA_KV_FP8_E4M3, "int4": pa.PA_KV_INT4}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+
+
+def restore(pool, scale, kind):
+    """The values of a pool [nblocks, bs, Hkv, D] in 64 bits."""
+    if kind == "bf16":
+        return pool.double()
+    if kind == "fp8":
+        x = pool.view(torch.float8_e4m3fn).double()
+    else:
+        x = torch.stack([(pool & 15).double() - 8, (pool >> 4).double() - 8], -1).flatten(-2)
+    return x * scale.double()[:, None, :, None]
+
+
+class Batch:
+    """Ragged sequences over a pool whose every row that no token sees is NaN (bf16 and E4M3)."""
+
+    def __init__(self, n, L, Hkv, G, D=128, bs=16, kind="bf16", window=0, causal=True, seed=0, qmul=1.0,
+                 extra_rows=3, max_blocks=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.n, self.L, self.Hkv, self.G, self.D, self.bs = n, L, Hkv, G, D, bs
+        self.kind, self.window, self.causal = kind, window, causal
+        self.Hq, self.B = Hkv * G, len(n)
+        need = [-(-x // bs) for x in L]
+        self.nblocks = sum(need) + 4
+        self.max_blocks = max_blocks or max(need + [1]) + 2
+        order = torch.randperm(self.nblocks, generator=g, device="cuda").int()
+        bt = torch.full((self.B, self.max_blocks), -7, dtype=torch.int32, device="cuda")
+        at = 0
+        for b, k in enumerate(need):
+            bt[b, :k] = order[at:at + k]
+            at += k
+        self.block_tables = bt
+        shape = (self.nblocks, bs, Hkv, D)
+        self.k_scale = self.v_scale = None
+        if kind == "bf16":
+            self.k = torch.randn(shape, generator=g, device="cuda").bfloat16()
+            self.v = torch.randn(shape, generator=g, device="cuda").bfloat16()
+        elif kind == "fp8":
+            self.k = (torch.randn(shape, generator=g, device="cuda") * 100).clamp(-448, 448).to(
+                torch.float8_e4m3fn).view(torch.uint8)
+            self.v = (torch.randn(shape, generator=g, device="cuda") * 100).clamp(-448, 448).to(
+                torch.float8_e4m3fn).view(torch.uint8)
+        else:
+            self.k, self.v = (torch.randint(0, 256, (*shape[:3], D // 2), generator=g, device="cuda",
+                                            dtype=torch.uint8) for _ in range(2))
+            for x in (self.k, self.v):           # nibbles 1..15
+                x |= ((x & 15) == 0).to(torch.uint8) | (((x >> 4) == 0).to(torch.uint8) << 4)
+        if kind != "bf16":
+            unit = 0.01 if kind == "fp8" else 0.25
+            self.k_scale, self.v_scale = (unit * (0.5 + torch.rand(self.nblocks, Hkv, generator=g,
+                                                                   device="cuda")) for _ in range(2))
+        # rows that some token sees
+        seen = torch.zeros(self.nblocks * bs, dtype=torch.bool, device="cuda")
+        for b in range(self.B):
+            lo = max(0, L[b] - n[b] - window + 1) if causal and window else 0
+            pos = torch.arange(lo, L[b], device="cuda")
+            seen[bt[b, pos // bs].long() * bs + pos % bs] = True
+        self.seen = seen
+        if kind != "int4":
+            for x in (self.k, self.v):
+                x.view(-1, Hkv, D)[~seen] = float("nan") if kind == "bf16" else 0x7F
+        self.offsets = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+        self.seq_lens = torch.tensor(L, dtype=torch.int32, device="cuda")
+        self.T = sum(n) + extra_rows
+        self.q = (torch.randn(self.T, self.Hq, D, generator=g, device="cuda") * qmul).bfloat16()
+        self.scale = D ** -0.5
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.shape = pa.make_shape(self.B, self.Hq, Hkv, D, bs, self.nblocks, self.max_blocks, KINDS[kind])
+        self.ws = workspace(self.shape, self.T)
+
+    def run(self, out=None, stream=None):
+        out = torch.full((self.T, self.Hq, self.D), -3.0, dtype=torch.bfloat16, device="cuda") if out is None else out
+        args = (self.shape, out, self.q, self.offsets, self.k, self.v, self.k_scale, self.v_scale,
+                self.block_tables, self.seq_lens, self.scale, self.ws, self.err, stream)
+        if self.causal:
+            pa.pa_extend(*args, window=self.window)
+        else:
+            pa.pa_cross_attend(*args)
+        return out
+
+    def reference(self):
+        """The result in 64 bits, and the bound's second term."""
+        ref = torch.full((self.T, self.Hq, self.D), -3.0, dtype=torch.float64, device="cuda")
+        size = torch.zeros_like(ref)
+        kd, vd = restore(self.k, self.k_scale, self.kind), restore(self.v, self.v_scale, self.kind)
+        at = 0
+        for b in range(self.B):
+            n, L = self.n[b], self.L[b]
+            pos = torch.arange(L, device="cuda")
+            rows = self.block_tables[b, pos // self.bs].long() * self.bs + pos % self.bs
+            ok = self.seen[rows][:, None, None]
+            zero = torch.zeros((), dtype=torch.float64, device="cuda")
+            k = torch.where(ok, kd.view(-1, self.Hkv, self.D)[rows], zero)
+            v = torch.where(ok, vd.view(-1, self.Hkv, self.D)[rows], zero)
+            q = self.q[at:at + n].double().view(n, self.Hkv, self.G, self.D)
+            s = torch.einsum("ihgd,jhd->hgij", q, k) * self.scale
+            slack = 0.0
+            if n and L:
+                top = float(torch.einsum("ihgd,jhd->hgij", q.abs(), k.abs()).max()) * abs(self.scale)
+                slack = 2 * (self.D * top + L + 16) * 2.0 ** -24
+            if self.causal:
+                me = torch.arange(n, device="cuda")[:, None] + (L - n)
+                hide = pos > me
+                if self.window:
+                    hide |= pos <= me - self.window
+                s = s.masked_fill(hide, -math.inf)
+            if L:
+                w = s.softmax(-1)
+                ref[at:at + n] = torch.einsum("hgij,jhd->ihgd", w, v).reshape(n, self.Hq, self.D)
+                size[at:at + n] = (U + slack) * torch.einsum("hgij,jhd->ihgd", w, v.abs()).reshape(
+                    n, self.Hq, self.D)
+            else:
+                ref[at:at + n] = 0
+            at += n
+        return ref, size
+
+    def check(self, out=None):
+        out = self.run() if out is None else out
+        torch.cuda.synchronize()
+        assert pa.pa_read_error_flag(self.err) == 0
+        ref, size = self.reference()
+        bad = ~((out.double() - ref).abs() <= U * ref.abs() + size)
+        assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off; first {bad.nonzero()[0].tolist()}"
+
+
+def workspace(shape, T):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return torch.full((pa.pa_attend_workspace_bytes(shape, T, sms),), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+HEADS = [(2, 4, 64, 16), (1, 8, 128, 16), (3, 1, 128, 32), (2, 3, 64, 32), (1, 5, 128, 16), (2, 16, 128, 32)]
+LENGTHS = {
+    "one": ([1], [1]),
+    "one of many": ([1], [700]),
+    "few": ([4], [100]),
+    "tile edges": ([127, 1, 16], [128, 129, 127]),
+    "prompt": ([300], [300]),
+    "ragged": ([5, 0, 33, 1, 130], [5, 40, 1000, 257, 131]),
+    "page ends": ([17, 31, 1], [17, 47, 33]),
+    "many short": ([1, 2, 3, 1, 2, 3] * 30, [1, 2, 30, 17, 60, 129] * 30),
+}
+
+
+def kinds_of(D):
+    return ["bf16"]
+
+
+CASES = [(h, name, kind) for h in HEADS for name in LENGTHS for kind in kinds_of(h[2])]
+
+
+@pytest.mark.parametrize("heads,name,kind", CASES)
+def test_extend(heads, name, kind):
+    Hkv, G, D, bs = heads
+    n, L = LENGTHS[name]
+    Batch(n, L, Hkv, G, D, bs, kind, seed=3).check()
+
+
+@pytest.mark.parametrize("heads,name,kind", CASES)
+def test_cross_attend(heads, name, kind):
+    Hkv, G, D, bs = heads
+    n, L = LENGTHS[name]
+    L = L[::-1]
+    L[0] = 0 if len(L) > 2 else L[0]             # a sequence without states gives zeros
+    Batch(n, L, Hkv, G, D, bs, kind, causal=False, seed=4).check()
+
+
+@pytest.mark.parametrize("window", [1, 16, 100, 128, 129, 1000])
+@pytest.mark.parametrize("G,kind", [(8, "bf16"), (3, "bf16")])
+def test_extend_window(window, G, kind):
+    Batch([200, 3, 1, 140], [900, 600, 513, 140], 2, G, 128, 16, kind, window=window, seed=5).check()
+
+
+def counting(b):
+    """q = 0 makes every weight 1 and V[j] the unit vector of j mod D: channel d of a row times the
+    number of keys it sees is the number of them that are d mod D, which shows every key."""
+    b.q.zero_()
+    for s in range(b.B):
+        pos = torch.arange(b.L[s], device="cuda")
+        rows = b.block_tables[s, pos // b.bs].long() * b.bs + pos % b.bs
+        keep = b.seen[rows]
+        one = torch.nn.functional.one_hot(pos % b.D, b.D)[:, None].expand(-1, b.Hkv, -1).bfloat16()
+        b.v.view(-1, b.Hkv, b.D)[rows[keep]] = one[keep]
+    out = b.run().double()
+    assert pa.pa_read_error_flag(b.err) == 0
+    at = 0
+    for s in range(b.B):
+        n, L = b.n[s], b.L[s]
+        i = torch.arange(n, device="cuda")[:, None]
+        d = torch.arange(b.D, device="cuda")[None]
+        hi = (L - n + i + 1) if b.causal else torch.full_like(i, L)
+        lo = (hi - b.window).clamp(min=0) if b.causal and b.window else torch.zeros_like(i)
+        upto = lambda x: (x - d + b.D - 1).div(b.D, rounding_mode="floor").clamp(min=0)  # noqa: E731
+        want = upto(hi) - upto(lo)
+        got = out[at:at + n] * (hi - lo)[:, None].double()
+        if n and L:
+            assert float(want.max()) * U < 0.49  # a count is told from its neighbours
+            assert torch.equal(got.round(), want[:, None].expand_as(got).double()), s
+        at += n
+    assert (out[at:] == -3.0).all()
+
+
+@pytest.mark.parametrize("n,L,G,bs,window", [
+    ([1], [9000], 8, 16, 0), ([3], [12001], 5, 32, 0), ([700], [8000], 8, 16, 0),
+    ([260, 1, 77], [4001, 15999, 300], 8, 32, 0), ([2000], [5003], 1, 16, 0),
+    ([513, 9], [6000, 7000], 7, 16, 2500), ([2048], [2048], 16, 16, 300),
+    ([40, 300, 0, 1, 5], [10000, 300, 7, 1, 6001], 2, 16, 0),
+])
+def test_extend_sees_every_key(n, L, G, bs, window):
+    counting(Batch(n, L, 2, G, 128, bs, window=window, seed=6))
+
+
+@pytest.mark.parametrize("n,L,G,D", [([1] * 40, list(range(1, 1600, 40)), 1, 64),
+                                     ([448, 60, 3], [1500, 700, 7000], 1, 64),
+                                     ([300, 5], [0, 12345], 4, 128)])
+def test_cross_attend_sees_every_key(n, L, G, D):
+    counting(Batch(n, L, 4, G, D, 16, causal=False, seed=7))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("qmul", [0.0, 8.0, 64.0, -64.0])
+def test_large_and_equal_scores(qmul, causal):
+    """The reference maximum moves between tiles; a negative sm_scale turns the order around."""
+    b = Batch([70, 3], [900, 1300], 2, 8, qmul=abs(qmul), causal=causal, seed=8)
+    if qmul < 0:
+        b.scale = -b.scale
+    b.check()
+
+
+def test_zero_scale_is_the_mean():
+    b = Batch([20], [300], 1, 4, seed=9)
+    b.scale = 0.0
+    b.check()
+
+
+def test_rows_outside_the_batch_stay():
+    b = Batch([5, 0, 3], [50, 10, 3], 2, 4, seed=10, extra_rows=0)
+    b.offsets += 2                               # two rows before the first sequence
+    b.T += 4
+    b.q = torch.randn(b.T, b.Hq, b.D, device="cuda").bfloat16()
+    b.ws = workspace(b.shape, b.T)
+    out = b.run()
+    assert (out[:2] == -3).all() and (out[10:] == -3).all()
+    inner = b.q
+    b.q, b.offsets, b.T = inner[2:10].contiguous(), b.offsets - 2, 8
+    b.check(out[2:10])
+
+
+def test_same_bits_on_every_call_and_with_any_workspace_contents():
+    b = Batch([40, 1, 7, 300], [3000, 9000, 100, 300], 2, 8, seed=11)
+    first = b.run().clone()
+    for fill in (0, 0x7F, 0xFF):
+        b.ws.fill_(fill)
+        assert torch.equal(b.run(), first)
+
+
+def test_capture_and_replay_with_new_lengths():
+    b = Batch([16, 8], [2000, 500], 2, 8, seed=12)
+    out = b.run()
+    want = out.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        b.run(out, stream=torch.cuda.current_stream())
+    out.fill_(-3.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    b.L = [300, 444]                             # other lengths in the same buffers
+    b.seq_lens.copy_(torch.tensor(b.L, dtype=torch.int32))
+    b.k.nan_to_num_()
+    b.v.nan_to_num_()
+    b.seen[:] = True
+    out.fill_(-3.0)
+    g.replay()
+    b.check(out)
+
+
+def test_two_streams_at_once():
+    bs = [Batch([200], [2000], 2, 8, seed=13), Batch([3] * 20, [700] * 20, 2, 8, seed=14, causal=False)]
+    want = [b.run().clone() for b in bs]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for b, o, s in zip(bs, outs, streams):
+            b.run(o, stream=s)
+    torch.cuda.synchronize()
+    for b, o, w in zip(bs, outs, want):
+        k = sum(b.n)
+        assert torch.equal(o[:k], w[:k])
+
+
+def test_device_errors():
+    # a block id outside the pool reads zeros: its keys score 0 and its values add nothing
+    b = Batch([1], [40], 1, 2, seed=15)
+    b.block_tables[0, 1] = b.nblocks + 5
+    b.run()
+    assert pa.pa_read_error_flag(b.err) == pa.PA_DEVERR_BLOCK_ID
+    # more query tokens than cached tokens: zeros, and the other sequence as ever
+    b = Batch([4, 3], [20, 30], 1, 2, seed=16)
+    want = b.run().clone()
+    b.seq_lens[0] = 3
+    out = b.run()
+    assert pa.pa_read_error_flag(b.err) == pa.PA_DEVERR_SEQ_LEN
+    assert (out[:4] == 0).all() and torch.equal(out[4:], want[4:])
+    # negative length, length beyond the table
+    for bad in (-5, 10 ** 8):
+        b.err.zero_()
+        b.seq_lens[0] = bad
+        b.k.nan_to_num_()
+        b.block_tables[0] = b.block_tables[0, 0]
+        assert torch.equal(b.run()[4:], want[4:])
+        assert pa.pa_read_error_flag(b.err) == pa.PA_DEVERR_SEQ_LEN
+    # offsets that fall, or leave the rows: that sequence is skipped
+    for offsets in ([0, 7, 5], [0, 4, 4 + 3 + 4]):
+        b = Batch([4, 3], [20, 30], 1, 2, seed=16)
+        b.offsets.copy_(torch.tensor(offsets, dtype=torch.int32))
+        out = b.run()
+        assert pa.pa_read_error_flag(b.err) == pa.PA_DEVERR_QUERY
+        assert (out[7:] == -3).all()
+
+
+def test_refuses_a_short_workspace():
+    b = Batch([4], [20], 1, 2, seed=17)
+    b.ws = b.ws[:-256]
+    with pytest.raises(pa.PAError, match="PA_ERR_INVALID_ARG"):
+        b.run()
+
+
+def test_a_batch_without_tokens():
+    b = Batch([0, 0], [10, 0], 1, 2, seed=18)
+    assert (b.run() == -3).all()
+    b = Batch([0], [10], 1, 2, seed=18, extra_rows=0)
+    assert b.run().numel() == 0
+
+
+# ------------------------------------------------------------------ rotation and write
+
+def rotated(x, cos_sin, pos, interleaved):
+    """The written formula in the type of cos_sin, not rounded."""
+    r = cos_sin.shape[1]
+    c, s = cos_sin[pos][:, None, :r // 2], cos_sin[pos][:, None, r // 2:]
+    x = x.to(cos_sin.dtype)
+    y = x.clone()
+    a, b = (x[..., 0:r:2], x[..., 1:r:2]) if interleaved else (x[..., :r // 2], x[..., r // 2:r])
+    u, v = a * c - b * s, b * c + a * s
+    if interleaved:
+        y[..., 0:r:2], y[..., 1:r:2] = u, v
+    else:
+        y[..., :r // 2], y[..., r // 2:r] = u, v
+    return y
+
+
+class Append:
+    def __init__(self, T, Hq, Hkv, D=128, bs=16, kind="bf16", r=None, interleaved=False, fused=False, seed=0,
+                 order="runs", nblocks=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        self.T, self.Hq, self.Hkv, self.D, self.bs, self.kind = T, Hq, Hkv, D, bs, kind
+        self.interleaved, self.r = interleaved, r or D
+        self.nblocks = nblocks or T // 4 + 5
+        blocks = rng.permutation(self.nblocks)
+        if order == "runs":                      # runs of consecutive slots, starting inside blocks
+            slots, at = [], 0
+            while len(slots) < T:
+                start = int(rng.integers(0, bs))
+                k = min(int(rng.integers(1, 3 * bs)), T - len(slots), (len(blocks) - at) * bs - start)
+                for i in range(start, start + k):
+                    slots.append(int(blocks[at + i // bs]) * bs + i % bs)
+                at = at + (start + k - 1) // bs + 1
+                if at >= len(blocks):
+                    slots += [-1] * (T - len(slots))
+        else:                                    # every slot of some blocks, shuffled
+            k = -(-T // bs)
+            slots = rng.permutation(np.concatenate([b * bs + np.arange(bs) for b in blocks[:k]]))[:T].tolist()
+        self.slots = torch.tensor(slots, dtype=torch.int64, device="cuda")
+        self.npos = 5000
+        self.pos = torch.from_numpy(rng.integers(0, self.npos, T).astype(np.int32)).cuda()
+        self.cos_sin = rope_table(self.npos, self.r, 500000.0)
+        qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g, device="cuda").bfloat16()
+        parts = [qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]]
+        self.q, self.k, self.v = parts if fused else [x.contiguous() for x in parts]
+        shape = (self.nblocks, bs, Hkv, {"bf16": D, "fp8": D, "int4": D // 2}[kind])
+        if kind == "bf16":
+            self.pools = [torch.randn(shape, generator=g, device="cuda").bfloat16() for _ in range(2)]
+            self.scales = [None, None]
+        else:
+            self.pools = [torch.randint(0, 0x7F if kind == "fp8" else 256, shape, generator=g, device="cuda",
+                                        dtype=torch.uint8) for _ in range(2)]
+            self.scales = [torch.rand(self.nblocks, Hkv, generator=g, device="cuda") * 0.02 for _ in range(2)]
+        self.shape = pa.make_shape(T, Hq, Hkv, D, bs, self.nblocks, 1, KINDS[kind])
+        self.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        self.q_out = torch.full((T, Hq, D), -3.0, dtype=torch.bfloat16, device="cuda")
+
+    def run(self, q="own", q_out=None):
+        pa.pa_rope_and_cache(self.shape, self.cos_sin, self.pos, self.q_out if q_out is None else q_out,
+                             self.q if isinstance(q, str) else q, self.k, self.v, *self.pools, *self.scales,
+                             self.slots, self.err, interleaved=self.interleaved)
+
+    def check(self, keep=None):
+        """Queries against 64 bits; keys and values: the bytes of the separate calls."""
+        keep = self.slots >= 0 if keep is None else keep
+        pools = [x.clone() for x in self.pools]
+        scales = [None if x is None else x.clone() for x in self.scales]
+        self.run()
+        k = rotated(self.k, self.cos_sin, self.pos.long().clamp(0, self.npos - 1), self.interleaved).bfloat16()
+        slots = torch.where(keep, self.slots, -1)
+        pa.pa_reshape_and_cache(self.shape, k, self.v.contiguous(), *pools, *scales, slots, None)
+        torch.cuda.synchronize()
+        for x, y in zip(self.pools + self.scales, pools + scales):
+            assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+        q = self.q[keep]
+        pos = self.pos[keep].long()
+        ref = rotated(q, self.cos_sin.double(), pos, self.interleaved)
+        # products and their sum in 32 bits: three roundings of parts no larger than |a| + |b|
+        part = rotated(q.abs(), torch.ones_like(self.cos_sin).double(), pos, self.interleaved).abs() + 2 * q.abs().double()
+        assert ((self.q_out[keep].double() - ref).abs() <= U * ref.abs() + 3 * 2.0 ** -24 * part).all()
+        assert (self.q_out[~keep] == -3.0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("T,Hq,Hkv,bs,order", [(1, 8, 1, 16, "runs"), (37, 6, 2, 32, "runs"),
+                                               (300, 64, 8, 16, "runs"), (600, 10, 5, 32, "shuffled"),
+                                               (257, 16, 16, 16, "shuffled")])
+@pytest.mark.parametrize("interleaved,r,fused", [(False, 128, False), (True, 128, True), (False, 32, True),
+                                                 (True, 16, False), (False, 112, False)])
+def test_rope_and_cache(kind, T, Hq, Hkv, bs, order, interleaved, r, fused):
+    Append(T, Hq, Hkv, 128, bs, kind, r, interleaved, fused, seed=T + r, order=order).check()
+
+
+@pytest.mark.parametrize("interleaved,r", [(False, 64), (True, 64), (False, 48), (True, 16)])
+def test_rope_and_cache_small_heads(interleaved, r):
+    Append(77, 9, 3, 64, 16, "bf16", r, interleaved, True, seed=r).check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+def test_rope_skips_padding_and_bad_tokens(kind):
+    a = Append(120, 8, 2, kind=kind, seed=3, order="shuffled")
+    a.slots[::7] = -1
+    a.pos[::7] = -9                              # a padded token's position means nothing
+    a.slots[5] = a.nblocks * a.bs
+    a.pos[11] = a.npos
+    a.pos[24] = -1
+    keep = a.slots >= 0
+    keep[5] = keep[11] = keep[24] = False
+    a.check(keep)
+    assert pa.pa_read_error_flag(a.err) == pa.PA_DEVERR_SLOT | pa.PA_DEVERR_POSITION
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+def test_rope_in_place_and_without_queries(kind):
+    a = Append(50, 8, 2, kind=kind, seed=4)
+    a.run()
+    q = a.q.clone()
+    keep = a.slots >= 0
+    a.run(q, q)
+    assert torch.equal(q[keep], a.q_out[keep]) and torch.equal(q[~keep], a.q[~keep])
+    b = Append(50, 8, 2, kind=kind, seed=4)
+    pa.pa_rope_and_cache(b.shape, b.cos_sin, b.pos, None, None, b.k, b.v, *b.pools, *b.scales, b.slots, b.err)
+    c = Append(50, 8, 2, kind=kind, seed=4)
+    c.run()
+    for x, y in zip(b.pools, c.pools):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+def test_rope_two_tokens_in_one_slot(kind):
+    a = Append(700, 4, 2, kind=kind, seed=5, order="shuffled")
+    a.slots[650] = a.slots[3]
+    a.slots[4] = a.slots[3]
+    a.check()
+    assert pa.pa_read_error_flag(a.err) == pa.PA_DEVERR_FP8_CONFLICT
+
+
+def test_rope_far_positions():
+    """A table row of a far position holds the angle to 32 bits, and the kernel adds no error."""
+    a = Append(40, 4, 2, seed=6)
+    a.npos = 1 << 20
+    a.cos_sin = rope_table(a.npos, 128, 10000.0)
+    a.pos = torch.randint(a.npos - 1000, a.npos, (40,), dtype=torch.int32, device="cuda")
+    f = 10000.0 ** -(torch.arange(0, 128, 2, dtype=torch.float64, device="cuda") / 128)
+    angle = a.pos.double()[:, None] * f
+    row = a.cos_sin[a.pos.long()].double()
+    assert (row - torch.cat([angle.cos(), angle.sin()], 1)).abs().max() < 2.0 ** -24 + 2.0 ** -32
+    a.check()
+
+
+# ------------------------------------------------------------------ as they are used together
+
+@pytest.mark.parametrize("kind", ["bf16"])
+def test_prompt_in_chunks_then_decode(kind):
+    """Three sequences of different lengths: their prompts in two chunks through pa_rope_and_cache
+    and pa_extend, then a decode step through pa_rope_and_cache and pa_decode.  Every attention is
+    checked against 64 bits on the cache that it read."""
+    Hkv, G, D, bs, B = 2, 4, 128, 16, 3
+    b = Batch([40, 17, 90], [150, 33, 200], Hkv, G, D, bs, kind, seed=20, max_blocks=14)
+    spare = torch.arange(B * 14, device="cuda").view(B, 14).int()
+    b.block_tables = spare                       # every sequence has 14 blocks of its own
+    b.nblocks = B * 14
+    pools = [torch.zeros(b.nblocks, bs, Hkv, D if kind != "int4" else D // 2, device="cuda",
+                         dtype=torch.bfloat16 if kind == "bf16" else torch.uint8) for _ in range(2)]
+    b.k, b.v = pools
+    if kind != "bf16":
+        b.k_scale, b.v_scale = (torch.zeros(b.nblocks, Hkv, device="cuda") for _ in range(2))
+    b.shape = pa.make_shape(B, b.Hq, Hkv, D, bs, b.nblocks, 14, KINDS[kind])
+    b.seen = torch.ones(b.nblocks * bs, dtype=torch.bool, device="cuda")
+    cos_sin = rope_table(400, D)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    done = [0] * B
+    for chunk in ([110, 16, 110], [40, 17, 90], [1, 1, 1]):
+        T = sum(chunk)
+        qkv = torch.randn(T, b.Hq + 2 * Hkv, D, generator=g, device="cuda").bfloat16()
+        q, k, v = qkv[:, :b.Hq], qkv[:, b.Hq:b.Hq + Hkv], qkv[:, b.Hq + Hkv:]
+        pos = torch.cat([torch.arange(d, d + c, device="cuda") for d, c in zip(done, chunk)]).int()
+        seq = torch.repeat_interleave(torch.arange(B, device="cuda"), torch.tensor(chunk, device="cuda"))
+        slots = b.block_tables[seq, (pos // bs).long()].long() * bs + pos.long() % bs
+        q_out = torch.empty(T, b.Hq, D, dtype=torch.bfloat16, device="cuda")
+        pa.pa_rope_and_cache(pa.make_shape(T, b.Hq, Hkv, D, bs, b.nblocks, 14, KINDS[kind]), cos_sin, pos, q_out,
+                             q, k, v, b.k, b.v, b.k_scale, b.v_scale, slots, b.err)
+        done = [d + c for d, c in zip(done, chunk)]
+        b.n, b.L, b.T, b.q = chunk, list(done), T, q_out
+        b.offsets = torch.tensor(np.concatenate([[0], np.cumsum(chunk)]), dtype=torch.int32, device="cuda")
+        b.seq_lens = torch.tensor(done, dtype=torch.int32, device="cuda")
+        b.ws = workspace(b.shape, T)
+        b.check()
+        if kind == "bf16":                       # what went into the cache is the rotated key
+            want = rotated(k, cos_sin, pos.long(), False).bfloat16()
+            assert torch.equal(b.k.view(-1, Hkv, D)[slots], want)
+    out = torch.empty(B, b.Hq, D, device="cuda")
+    pa.pa_decode(b.shape, out, b.q, b.k, b.v, b.k_scale, b.v_scale, b.block_tables, b.seq_lens, b.scale, b.err)
+    ref, size = b.reference()
+    assert ((out.double() - ref).abs() <= (1e-3 if kind == "bf16" else 2e-2) * (1 + ref.abs())).all()
