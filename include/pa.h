@@ -500,8 +500,8 @@ pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const fl
  * gets zeros (PA_DEVERR_SEQ_LEN); a sequence whose offsets fall or leave the rows is skipped
  * (PA_DEVERR_QUERY).
  * Rounding: q K^T and the sums are fp32; the weights enter the second product as bf16.  The
- * result is the same on every call, bit for bit.  Batches of more than 16384 sequences, and
- * quantised pools, return PA_ERR_UNSUPPORTED.
+ * result is the same on every call, bit for bit.  Batches of more than 16384 sequences return
+ * PA_ERR_UNSUPPORTED.
  */
 pa_status pa_extend(const pa_shape *shape, void *out, const void *q, const int32_t *query_offsets,
                     int32_t total_queries, const void *k_pool, const void *v_pool,

@@ -365,25 +365,142 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+
+// ------------------------------------------------------------------ codes to bf16
+
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two E4M3 codes (bytes 2 i and 2 i + 1 of w), exact: exponent and mantissa moved to bf16's
+// places are the value times 2^-120 (the difference of the exponent biases, 127 - 7).
+__device__ __forceinline__ uint32_t e4m3_pair_bf16(uint32_t w, int i) {
+  const uint32_t x = __byte_perm(w, 0u, i == 0 ? 0x1404 : 0x3424);       // codes in the high bytes
+  return bf16x2_mul((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), 0x7B807B80u);
+}
+
+// The two 4-bit codes of byte i of w, given w and w >> 4, exact: 128 + u is a bf16 with u in its
+// lowest bits; less 136 it is the code u - 8.
+__device__ __forceinline__ uint32_t int4_pair_bf16(uint32_t w, uint32_t w4, int i) {
+  const uint32_t x = __byte_perm(w, w4, 0x4400 + i * 0x1111);
+  return bf16x2_sub((x & 0x000F000Fu) | 0x43004300u, 0x43084308u);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+
+// A tile's codes (as TMA swizzled them) to a bf16 tile (128-byte swizzle), by four warps.
+// Neighbouring lanes write both 64-column halves of a row at once; the order of a lane's stores
+// keeps the two halves off each other's banks.
+template <int KIND>
+__device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, int lane) {
+  constexpr int kBatch = 4;
+  if constexpr (KIND == PA_KV_FP8_E4M3) {
+    const int c = lane & 7;                              // 16 codes: columns [16 c, 16 c + 16)
+    for (int i0 = 0; i0 < 8; i0 += kBatch) {
+      uint4 v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = (i0 + i) * 16 + w * 4 + (lane >> 3);
+        v[i] = lds128(raw + r * 128 + ((c ^ (r & 7)) << 4));
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = (i0 + i) * 16 + w * 4 + (lane >> 3);
+        const uint4 lo = make_uint4(e4m3_pair_bf16(v[i].x, 0), e4m3_pair_bf16(v[i].x, 1),
+                                    e4m3_pair_bf16(v[i].y, 0), e4m3_pair_bf16(v[i].y, 1));
+        const uint4 hi = make_uint4(e4m3_pair_bf16(v[i].z, 0), e4m3_pair_bf16(v[i].z, 1),
+                                    e4m3_pair_bf16(v[i].w, 0), e4m3_pair_bf16(v[i].w, 1));
+        const uint32_t row = dst + (c >> 2) * (kKeys * 128) + r * 128;
+        const int c8 = 2 * (c & 3), odd = c >> 2;
+        sts128(row + (((c8 + odd) ^ (r & 7)) << 4), odd ? hi : lo);
+        sts128(row + (((c8 + 1 - odd) ^ (r & 7)) << 4), odd ? lo : hi);
+      }
+    }
+  } else {
+    const int c = lane & 3;                              // 32 codes: columns [32 c, 32 c + 32)
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 32 + w * 8 + (lane >> 2);
+      v[i] = lds128(raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = i * 32 + w * 8 + (lane >> 2);
+      const uint32_t row = dst + (c >> 1) * (kKeys * 128) + r * 128;
+      const bool swap = c >= 2;
+      if (swap) v[i] = make_uint4(v[i].z, v[i].w, v[i].x, v[i].y);
+      const uint32_t words[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {                      // chunk j, or j ^ 2 of the other half
+        const uint32_t x = words[j], x4 = x >> 4;
+        const int c8 = 4 * (c & 1) + (swap ? j ^ 2 : j);
+        sts128(row + ((c8 ^ (r & 7)) << 4),
+               make_uint4(int4_pair_bf16(x, x4, 0), int4_pair_bf16(x, x4, 1),
+                          int4_pair_bf16(x, x4, 2), int4_pair_bf16(x, x4, 3)));
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------------ the kernel
 
-template <int kD, bool kShared>
+// kKind: the pools' pa_kv_dtype.  Codes (D = 128) are restored to bf16 tiles, without their scale,
+// by four warps of their own: K's scale multiplies the scores of a page, V's its weights.
+template <int kD, int kKind, bool kShared>
 struct AttendCfg {
-  static constexpr int D = kD;
-  static constexpr bool SHARED = kShared;
-  static constexpr int HALVES = D / 64;                 // 128-byte column chunks of a row
+  static constexpr int D = kD, KIND = kKind;
+  static constexpr bool SHARED = kShared, QUANT = kKind != PA_KV_BF16;
+  static constexpr int HALVES = D / 64;                 // 128-byte column chunks of a bf16 row
   static constexpr int TILE = kKeys * D * 2;            // bytes of a Q, K or V tile
-  static constexpr int STAGES = D == 128 ? 5 : 12;      // K/V ring: 160 or 192 KB
+  static constexpr int CODE_ROW = KIND == PA_KV_INT4 ? 64 : 128;
+  static constexpr int RAW_TILE = kKeys * CODE_ROW;
+  // the ring of K and V tiles; code pools: as many code tiles wait before it (224 KB with Q)
+  static constexpr int STAGES = D == 64 ? 12 : KIND == PA_KV_BF16 ? 5 : KIND == PA_KV_FP8_E4M3 ? 3 : 4;
+  static constexpr int RAW = QUANT ? 4 : 1;
   static constexpr int RING = 2 * TILE;                 // after the two Q tiles
-  static constexpr int SMEM = RING + STAGES * TILE + 1024;
-  // Warps 0-7 softmax, 8 products, 9 loads, 10 and 11 the pieces of each stream.  Registers
-  // are dealt out by groups of four warps: 384 threads start with 168 registers, 64,512 in all, dealt anew as
-  // 256 x 208 + 128 x 88: a softmax thread holds its row's 128 scores.
-  static constexpr int THREADS = 384;
-  static constexpr int MMA_WARP = 8, LOAD_WARP = 9, PIECE_WARP = 10;
-  static constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
+  static constexpr int RAW_RING = RING + STAGES * TILE;
+  static constexpr int SMEM = RAW_RING + (QUANT ? RAW * RAW_TILE : 0) + 1024;
+  // Warps 0-7 softmax, then (code pools) four that restore codes, then one each for the
+  // products, the loads and the pieces of each stream.  Registers are dealt out by groups of four
+  // warps: 384 threads start with 168, 64,512 in all, dealt anew as 256 x 208 + 128 x 88 (512
+  // with 128: 256 x 184 + 256 x 72): a softmax thread holds its row's 128 scores.
+  static constexpr int THREADS = QUANT ? 512 : 384;
+  static constexpr int CODE_WARP = 8;
+  static constexpr int MMA_WARP = QUANT ? 12 : 8, LOAD_WARP = MMA_WARP + 1, PIECE_WARP = MMA_WARP + 2;
+  static constexpr int SOFTMAX_REGS = QUANT ? 184 : 208, OTHER_REGS = QUANT ? 72 : 88;
   static constexpr int STREAMS = SHARED ? 1 : 2;        // key streams of a CTA
   static constexpr int PIECES = 8;                      // pieces known ahead per stream
+  static constexpr int SCALES = 5;                      // tiles whose scales are held per stream
+  // the scales of tile j + SCALES are stored before its K is issued; by then the copies have
+  // come 2 (SCALES - 1) past V of tile j, which must be further than both rings hold
+  static_assert(!QUANT || 2 * (SCALES - 1) >= RAW + STAGES, "scales overwritten too early");
 };
 
 template <class C>
@@ -391,10 +508,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int kBars = 2 * C::STAGES + 9 + 2 * C::STREAMS * C::PIECES;
+  constexpr int kPieceBars = 2 * C::STAGES + 9, kRawBars = kPieceBars + 2 * C::STREAMS * C::PIECES;
+  constexpr int kBars = kRawBars + (C::QUANT ? 2 * C::RAW + C::STREAMS * C::SCALES : 0);
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ Piece pieces[C::STREAMS][C::PIECES];
   __shared__ uint32_t tmem_slot;
+  // scales of the tiles on their way: K's pages (16 tokens each), then V's
+  __shared__ float4 scales[C::STREAMS][C::QUANT ? C::SCALES : 1][4];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -408,18 +528,33 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t done_bar = bar0 + 8 * (2 * C::STAGES + 8);
   // piece k of a stream is known / no longer needed
   auto pc_full = [&](int st, uint32_t k) {
-    return bar0 + 8 * (2 * C::STAGES + 9 + st * C::PIECES + k % C::PIECES);
+    return bar0 + 8 * (kPieceBars + st * C::PIECES + k % C::PIECES);
   };
   auto pc_empty = [&](int st, uint32_t k) {
-    return bar0 + 8 * (2 * C::STAGES + 9 + (C::STREAMS + st) * C::PIECES + k % C::PIECES);
+    return bar0 + 8 * (kPieceBars + (C::STREAMS + st) * C::PIECES + k % C::PIECES);
   };
+  // code pools: code tiles landed / restored, scales of a stream's tile n stored
+  auto raw_full = [&](int i) { return bar0 + 8 * (kRawBars + i); };
+  auto raw_empty = [&](int i) { return bar0 + 8 * (kRawBars + C::RAW + i); };
+  auto sc_full = [&](int st, uint32_t n) {
+    return bar0 + 8 * (kRawBars + 2 * C::RAW + st * C::SCALES + n % C::SCALES);
+  };
+  auto sc_parity = [](uint32_t n) { return (n / C::SCALES) & 1; };
   auto pc_parity = [](uint32_t k) { return (k / C::PIECES) & 1; };
   const int S = C::SHARED ? 2 * p.tok : p.tok;
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(kv_full(i), 1);
+      mbar_init(kv_full(i), C::QUANT ? 4 : 1);           // the restoring warps, or the copies
       mbar_init(kv_empty(i), 1);
+    }
+    if constexpr (C::QUANT) {
+      for (int i = 0; i < C::RAW; ++i) {
+        mbar_init(raw_full(i), 1);
+        mbar_init(raw_empty(i), 4);
+      }
+      for (int st = 0; st < C::STREAMS; ++st)
+        for (int n = 0; n < C::SCALES; ++n) mbar_init(sc_full(st, n), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
@@ -431,7 +566,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int st = 0; st < C::STREAMS; ++st)
       for (int k = 0; k < C::PIECES; ++k) {
         mbar_init(pc_full(st, k), 1);
-        mbar_init(pc_empty(st, k), 2 + (C::SHARED ? 8 : 4));   // loads, products, softmax
+        mbar_init(pc_empty(st, k), 2 + (C::SHARED ? 8 : 4) + (C::QUANT ? 4 : 0));   // every reader
       }
     fence_mbar_init();
   }
@@ -473,6 +608,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int tok0 = C::SHARED ? t * p.tok : 0;          // first token of this row tile in a unit
     bool q_sent = false;                                 // Q of the next piece is on its way
     uint32_t q_loads = 0, q_used = 0, s_phase = 0, o_phase = 0;
+    uint32_t tiles = 0;                                  // key tiles of the stream so far
     auto load_q = [&](const Piece &x) {                  // by one thread
       mbar_arrive_expect_tx(q_full(t), C::HALVES * p.tok * p.G * 128);
 #pragma unroll
@@ -488,6 +624,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(pc_empty(st, k));
       if (x.n == 0) break;
+      const uint32_t tile0 = tiles;
+      tiles += x.n;
       const int ntok = min(p.tok, x.ntok - tok0);        // tokens of this tile
       if (ntok <= 0) continue;
       if (row == 0 && !q_sent) load_q(x);
@@ -528,6 +666,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < kKeys; j += 32) tc_ld32(s + j, tS + j);
           tc_wait_ld();
+          const float *sc = nullptr;                     // 8 K scales, 8 V scales
+          if constexpr (C::QUANT) {
+            const uint32_t n = tile0 + i;
+            ok = mbar_wait(sc_full(st, n), sc_parity(n));
+            sc = reinterpret_cast<const float *>(scales[st][n % C::SCALES]);
+#pragma unroll
+            for (int j = 0; j < kKeys; j += 2) {
+              const float f = sc[j / 16] * p.c;
+              const float2 y = mul2(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
+                                    make_float2(f, f));
+              s[j] = __float_as_uint(y.x);
+              s[j + 1] = __float_as_uint(y.y);
+            }
+          }
           if (key0 < all_lo || key0 + kKeys > all_hi) {
             const int a = lo - key0;
             const unsigned n = static_cast<unsigned>(max(0, hi - lo));
@@ -541,7 +693,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[j + e]), __uint_as_float(s[j + 4 + e])));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (C::QUANT ? 1.f : p.c);
           if (m == -INFINITY) m = top;                   // O and l are zero so far
           // the reference moves only past kMaxJump octaves: weights stay below 2^8, far
           // inside bf16 and fp32, and O is seldom rescaled
@@ -571,10 +723,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 y = make_float2(__uint_as_float(s[j + 2 * e]), __uint_as_float(s[j + 2 * e + 1]));
-              y = fma2(y, c2, n2);
+              y = C::QUANT ? add2(y, n2) : fma2(y, c2, n2);
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum[e & 1] = add2(sum[e & 1], y);
+              if constexpr (C::QUANT) {
+                const float f = sc[8 + (j + 2 * e) / 16];
+                y = mul2(y, make_float2(f, f));
+              }
               packed[e] = pack_bf16(y.x, y.y);
             }
             tc_st16(tS + j / 2, packed);
@@ -675,12 +831,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     } else if (warp == C::LOAD_WARP) {
       // ---------------------------------------------------------------- K and V tiles
-      // lane (half, page): one box of 16 tokens x 64 columns
-      const int page = lane & 7, half = lane >> 3;
-      const bool loads = lane < 8 * C::HALVES;
+      // lane (half, page): one box of 16 tokens x 64 columns; code pools: x a whole row, by lanes
+      // 0-7, while lanes 0-7 and 8-15 fetch the pages' K and V scales
+      const int page = lane & 7, half = C::QUANT ? 0 : lane >> 3;
+      const bool loads = lane < 8 * (C::QUANT ? 1 : C::HALVES);
+      constexpr int kRing = C::QUANT ? C::RAW : C::STAGES;
+      auto ring_full = [&](int i) { return C::QUANT ? raw_full(i) : kv_full(i); };
+      auto ring_empty = [&](int i) { return C::QUANT ? raw_empty(i) : kv_empty(i); };
       struct Tile {
         bool ok;
         int h, boxes, blk, g;                              // blk < 0: this lane loads nothing
+        float scale;
       };
       Piece pc[C::STREAMS] = {};
       int at[C::STREAMS] = {};
@@ -716,11 +877,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       };
       uint32_t count = 0;
       auto issue = [&](const CUtensorMap *map, const Tile &t) {
-        const int stage = count % C::STAGES;
-        ok = ok && mbar_wait(kv_empty(stage), ((count / C::STAGES) & 1) ^ 1);
+        const int stage = count % kRing;
+        ok = ok && mbar_wait(ring_empty(stage), ((count / kRing) & 1) ^ 1);
         if (!ok) return;
         ++count;
-        if (lane == 0) mbar_arrive_expect_tx(kv_full(stage), t.boxes * C::HALVES * 16 * 128);
+        constexpr int kBox = C::QUANT ? 16 * C::CODE_ROW : 16 * 128;
+        if (lane == 0)
+          mbar_arrive_expect_tx(ring_full(stage), t.boxes * kBox * (C::QUANT ? 1 : C::HALVES));
         __syncwarp();
         if (loads && t.blk >= 0) {
           int row = p.nblocks * p.bs;                      // outside the pool: reads zeros
@@ -728,29 +891,98 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             row = t.blk * p.bs + t.g % p.bs;
           else
             set_err(p.err, PA_DEVERR_BLOCK_ID);
-          tma_load_2d(sm + C::RING + stage * C::TILE + half * (kKeys * 128) + page * (16 * 128), map,
-                      t.h * C::D + half * 64, row, kv_full(stage));
+          if constexpr (C::QUANT)
+            tma_load_2d(sm + C::RAW_RING + stage * C::RAW_TILE + page * kBox, map, t.h * C::CODE_ROW,
+                        row, ring_full(stage));
+          else
+            tma_load_2d(sm + C::RING + stage * C::TILE + half * (kKeys * 128) + page * kBox, map,
+                        t.h * C::D + half * 64, row, ring_full(stage));
         }
       };
-  #pragma unroll
-      for (int st = 0; st < C::STREAMS; ++st) cur[st] = fetch(st);
+      // A tile's block ids are fetched two tiles ahead of its copy and its scales one ahead.
+      uint32_t tiles[C::STREAMS] = {};
+      Tile nxt[C::STREAMS] = {};
+      auto fetch_scale = [&](Tile &t) {
+        t.scale = 0.f;
+        if (C::QUANT && t.ok && lane < 16 && t.blk >= 0 && t.blk < p.nblocks)
+          t.scale = (lane < 8 ? p.k_scale : p.v_scale)[static_cast<int64_t>(t.blk) * p.Hkv + t.h];
+      };
+#pragma unroll
+      for (int st = 0; st < C::STREAMS; ++st) {
+        cur[st] = fetch(st);
+        fetch_scale(cur[st]);
+        if (cur[st].ok) nxt[st] = fetch(st);
+      }
       for (bool more = true; more && ok;) {
         more = false;
-  #pragma unroll
+#pragma unroll
         for (int st = 0; st < C::STREAMS; ++st) {
           if (!ok || !(prev[st].ok || cur[st].ok)) continue;
           more = true;
-          const Tile nxt = cur[st].ok ? fetch(st) : Tile{};
+          fetch_scale(nxt[st]);
+          const Tile far = nxt[st].ok ? fetch(st) : Tile{};
           if (prev[st].ok) issue(&tmV, prev[st]);
-          if (cur[st].ok) issue(&tmK, cur[st]);
+          if (cur[st].ok) {
+            if constexpr (C::QUANT) {
+              const uint32_t n = tiles[st]++;
+              if (lane < 16) reinterpret_cast<float *>(scales[st][n % C::SCALES])[lane] = cur[st].scale;
+              __syncwarp();
+              if (lane == 0) mbar_arrive(sc_full(st, n));
+            }
+            issue(&tmK, cur[st]);
+          }
           prev[st] = cur[st];
-          cur[st] = nxt;
+          cur[st] = nxt[st];
+          nxt[st] = far;
         }
       }
       if (!ok) {
         // the copies in flight land in this CTA's memory: wait for them before leaving
-        for (uint32_t k = count > C::STAGES ? count - C::STAGES : 0; k < count; ++k)
-          mbar_wait(kv_full(k % C::STAGES), (k / C::STAGES) & 1);
+        for (uint32_t k = count > kRing ? count - kRing : 0; k < count; ++k)
+          mbar_wait(ring_full(k % kRing), (k / kRing) & 1);
+      }
+    } else if (C::QUANT && warp < C::MMA_WARP) {
+      // ---------------------------------------------------------------- codes to bf16 tiles
+      // in the order of the ring, until the pieces' tiles are all done
+      uint32_t todo[C::STREAMS] = {}, next_piece[C::STREAMS] = {}, count = 0;
+      bool over[C::STREAMS] = {};
+      bool v_due[C::STREAMS] = {};
+      auto one = [&] {
+        const int from = count % C::RAW, to = count % C::STAGES;
+        ok = ok && mbar_wait(raw_full(from), (count / C::RAW) & 1) &&
+             mbar_wait(kv_empty(to), ((count / C::STAGES) & 1) ^ 1);
+        if (!ok) return;
+        ++count;
+        restore_tile<C::KIND>(sm + C::RAW_RING + from * C::RAW_TILE, sm + C::RING + to * C::TILE,
+                              warp - C::CODE_WARP, lane);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(raw_empty(from));
+          mbar_arrive(kv_full(to));
+        }
+      };
+      for (bool more = true; more && ok;) {
+        more = false;
+#pragma unroll
+        for (int st = 0; st < C::STREAMS; ++st) {
+          if (todo[st] == 0 && !over[st]) {
+            const uint32_t k = next_piece[st]++;
+            ok = ok && mbar_wait(pc_full(st, k), pc_parity(k));
+            if (!ok) break;
+            todo[st] = pieces[st][k % C::PIECES].n;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pc_empty(st, k));
+            over[st] = todo[st] == 0;
+          }
+          if (v_due[st]) one();                          // V of the tile before
+          v_due[st] = todo[st] > 0;
+          if (v_due[st]) {
+            --todo[st];
+            one();                                       // K
+            more = true;
+          }
+        }
       }
     } else if (warp == C::MMA_WARP) {
       // ---------------------------------------------------------------- matrix products
@@ -996,7 +1228,6 @@ pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t 
                      const float *v_scale, const int32_t *bt, const int32_t *sl, bool causal,
                      int window, float sm_scale, void *workspace, int sms, int32_t *err,
                      cudaStream_t stream) {
-  if (s.kv_dtype != PA_KV_BF16) return PA_ERR_UNSUPPORTED;
   const Plan plan = make_plan(s, T, sms);
   AttendParams p{};
   p.out = static_cast<uint16_t *>(out);
@@ -1031,11 +1262,13 @@ pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t 
   if (!make_query_map(&mq, q, s, T, plan.tok) || !make_pool_map(&mk, k_pool, s, 1) ||
       !make_pool_map(&mv, v_pool, s, 1))
     return PA_ERR_CUDA;
-  if (s.D == 128)
-    return plan.shared ? launch<AttendCfg<128, true>>(p, mq, mk, mv, stream)
-                       : launch<AttendCfg<128, false>>(p, mq, mk, mv, stream);
-  return plan.shared ? launch<AttendCfg<64, true>>(p, mq, mk, mv, stream)
-                     : launch<AttendCfg<64, false>>(p, mq, mk, mv, stream);
+#define PA_ATTEND(D, KIND)                                                      \
+  (plan.shared ? launch<AttendCfg<D, KIND, true>>(p, mq, mk, mv, stream)        \
+               : launch<AttendCfg<D, KIND, false>>(p, mq, mk, mv, stream))
+  if (s.kv_dtype == PA_KV_FP8_E4M3) return PA_ATTEND(128, PA_KV_FP8_E4M3);
+  if (s.kv_dtype == PA_KV_INT4) return PA_ATTEND(128, PA_KV_INT4);
+  return s.D == 128 ? PA_ATTEND(128, PA_KV_BF16) : PA_ATTEND(64, PA_KV_BF16);
+#undef PA_ATTEND
 }
 
 }  // namespace pa

@@ -172,7 +172,7 @@ LENGTHS = {
 
 
 def kinds_of(D):
-    return ["bf16"]
+    return ["bf16"] if D == 64 else ["bf16", "fp8", "int4"]
 
 
 CASES = [(h, name, kind) for h in HEADS for name in LENGTHS for kind in kinds_of(h[2])]
@@ -195,7 +195,7 @@ def test_cross_attend(heads, name, kind):
 
 
 @pytest.mark.parametrize("window", [1, 16, 100, 128, 129, 1000])
-@pytest.mark.parametrize("G,kind", [(8, "bf16"), (3, "bf16")])
+@pytest.mark.parametrize("G,kind", [(8, "bf16"), (3, "bf16"), (4, "fp8"), (8, "int4")])
 def test_extend_window(window, G, kind):
     Batch([200, 3, 1, 140], [900, 600, 513, 140], 2, G, 128, 16, kind, window=window, seed=5).check()
 
@@ -518,7 +518,7 @@ def test_rope_far_positions():
 
 # ------------------------------------------------------------------ as they are used together
 
-@pytest.mark.parametrize("kind", ["bf16"])
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
 def test_prompt_in_chunks_then_decode(kind):
     """Three sequences of different lengths: their prompts in two chunks through pa_rope_and_cache
     and pa_extend, then a decode step through pa_rope_and_cache and pa_decode.  Every attention is
