@@ -22,8 +22,7 @@
 //
 // One CTA per SM: Q, K and V tiles in 128-byte-swizzled shared memory (TMA, one box per 16
 // tokens of a page), S and O in TMEM (128 + D columns per row tile), P written over S as
-// bf16 and read from TMEM by the second product.  Warps 0-3 and 4-7: the softmax of row
-// tiles 0 and 1, one thread per row; one warp issues the products, one the loads.
+// bf16 and read from TMEM by the second product.
 #include <algorithm>
 
 #include "pa_common.cuh"
@@ -34,6 +33,7 @@ namespace {
 
 constexpr int kKeys = 128;              // keys per tile
 constexpr int kRows = 128;              // rows per tile
+constexpr int kEarly = 96;              // keys whose weights are announced ahead of the rest
 constexpr float kMaxJump = 8.f;         // the reference maximum moves only past this many octaves
 
 struct AttendParams {
@@ -45,8 +45,10 @@ struct AttendParams {
   float2 *part_ml;                      // [2 workers][rows]: (reference maximum times c, l)
   int4 *cut;                            // [workers]: the unit a worker leaves unfinished
   int B, Hq, Hkv, G, T, bs, max_blocks, nblocks, window, causal, tok, workers, rows;
+  uint64_t over_workers;                // 2^64 / workers, rounded up
   float c;                              // |sm_scale| log2(e)
   uint32_t negate;                      // sm_scale < 0: the products take -Q
+  bool wide;                            // `out` is 32-byte aligned
 };
 
 // ------------------------------------------------------------------ units of work
@@ -135,25 +137,6 @@ __device__ __forceinline__ int64_t scan64(int64_t v, int lane) {   // inclusive
   return v;
 }
 
-// ceil(a / w), w < 2^15, by digits of 16 bits (a 64-bit division is a call, which would
-// spill the softmax warps' registers)
-__device__ __forceinline__ int64_t div_up(int64_t a, int w) {
-  a += w - 1;
-  int64_t q = 0;
-  uint32_t r = 0;
-#pragma unroll
-  for (int sh = 48; sh >= 0; sh -= 16) {
-    const uint32_t d = (r << 16) | (static_cast<uint32_t>(a >> sh) & 0xFFFFu);
-    q = (q << 16) | (d / w);
-    r = d % w;
-  }
-  return q;
-}
-
-__device__ __forceinline__ int64_t seq_tiles_total(const AttendParams &p, const Seq &s, int S) {
-  return s.n > 0 ? p.Hkv * tiles_before(p, s, (s.n + S - 1) / S, S) : 0;
-}
-
 // A piece of a unit: key tiles [tile, tile + n) of unit tokens [row, row + ntok).
 struct Piece {
   int seq, h, row, ntok, pos;  // pos: position of the first token (causal)
@@ -162,60 +145,84 @@ struct Piece {
   int starts, ends;            // holds the unit's first / last key tile
 };
 
+// The tiles of the sequences before each point of the batch, as one warp sees them: lane i
+// holds sequence i of a group of 32.
+struct Group {
+  int g;                       // -1: none
+  Seq s;
+  int64_t per_head, upto;      // tiles of one KV head; of the group through this sequence
+
+  __device__ __forceinline__ void load(const AttendParams &p, int group, int S, int lane,
+                                       int32_t *err) {
+    g = group;
+    const int b = group * 32 + lane;
+    s = Seq{};
+    per_head = 0;
+    if (b < p.B) {
+      s = load_seq(p, b, err);
+      per_head = tiles_before(p, s, (s.n + S - 1) / S, S);
+    }
+    upto = scan64(p.Hkv * per_head, lane);
+  }
+};
+
 // The pieces of one worker, in order.
 struct Walker {
   int b, h, u, off, U;
   int remaining;
   Seq s;
 
-  // [start, end) of the tile stream; sums: tiles of each group of 32 sequences
-  __device__ void init(const AttendParams &p, const int64_t *sums, int64_t start, int64_t end,
-                       int S, int lane) {
-    remaining = static_cast<int>(max(static_cast<int64_t>(0), end - start));
+  // tiles [start, end) of the stream; sums: tiles of each group of 32 sequences (more than 32)
+  __device__ __forceinline__ void init(const AttendParams &p, Group &group, const int64_t *sums,
+                                       int64_t start, int64_t end, int S, int lane) {
+    remaining = static_cast<int>(end - start);
     b = h = u = off = U = 0;
     s = Seq{};
-    if (remaining == 0) return;
-    const int groups = (p.B + 31) / 32;
-    int g = 0;
+    if (remaining <= 0) return;
     int64_t before = 0;
-    for (int g0 = 0; g0 < groups; g0 += 32) {
-      const int64_t v = scan64(g0 + lane < groups ? sums[g0 + lane] : 0, lane);
-      const uint32_t past = __ballot_sync(0xffffffffu, before + v > start);
-      const int first = past ? __ffs(past) - 1 : 32;
-      if (first > 0) before += shfl64(v, first - 1);
-      g = g0 + first;
-      if (past) break;
+    if (p.B > 32) {
+      const int groups = (p.B + 31) / 32;
+      int g = 0;
+      for (int g0 = 0; g0 < groups; g0 += 32) {
+        const int64_t v = scan64(g0 + lane < groups ? sums[g0 + lane] : 0, lane);
+        const uint32_t past = __ballot_sync(0xffffffffu, before + v > start);
+        const int first = past ? __ffs(past) - 1 : 32;
+        if (first > 0) before += shfl64(v, first - 1);
+        g = g0 + first;
+        if (past) break;
+      }
+      if (g != group.g) group.load(p, g, S, lane, nullptr);
     }
-    const int mine = g * 32 + lane;
-    Seq t{};
-    int64_t total = 0;
-    if (mine < p.B) {
-      t = load_seq(p, mine, nullptr);
-      total = seq_tiles_total(p, t, S);
-    }
-    const int64_t v = scan64(total, lane);
-    const uint32_t past = __ballot_sync(0xffffffffu, before + v > start);
+    const uint32_t past = __ballot_sync(0xffffffffu, before + group.upto > start);
     const int l = past ? __ffs(past) - 1 : 31;
-    const int64_t upto = shfl64(v - total, l);
-    b = g * 32 + l;
-    s = load_seq(p, b, nullptr);
+    b = group.g * 32 + l;
+    s.q0 = __shfl_sync(0xffffffffu, group.s.q0, l);
+    s.n = __shfl_sync(0xffffffffu, group.s.n, l);
+    s.L = __shfl_sync(0xffffffffu, group.s.L, l);
+    s.base = __shfl_sync(0xffffffffu, group.s.base, l);
+    s.lo = __shfl_sync(0xffffffffu, group.s.lo, l);
+    const int64_t per_head = shfl64(group.per_head, l);
+    int64_t r = start - before - (shfl64(group.upto, l) - p.Hkv * per_head);
     U = (s.n + S - 1) / S;
-    const int64_t rem = start - before - upto;
-    const int64_t per_head = tiles_before(p, s, U, S);
-    for (int bit = 1 << 11; bit > 0; bit >>= 1)          // the last head with h per_head <= rem
-      if ((h + bit) * per_head <= rem) h += bit;
-    const int64_t r = rem - h * per_head;
+    // the head: at most 2048, so a quotient in fp32 is off by one at most
+    h = static_cast<int>(__fdividef(static_cast<float>(r), static_cast<float>(per_head)));
+    h = min(h, p.Hkv - 1);
+    if (h * per_head > r) --h;
+    if (h + 1 < p.Hkv && (h + 1) * per_head <= r) ++h;
+    r -= h * per_head;
     int lo = 0, hi = U;                       // the last unit with tiles_before <= r
+    int64_t at_lo = 0;
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int cand = lo + lane * step;
-      const uint32_t ok =
-          __ballot_sync(0xffffffffu, cand < hi && tiles_before(p, s, cand, S) <= r);
-      lo += (31 - __clz(ok)) * step;          // lane 0 always holds
+      const int64_t f = tiles_before(p, s, min(cand, hi), S);
+      const int win = 31 - __clz(__ballot_sync(0xffffffffu, cand < hi && f <= r));   // lane 0 holds
+      at_lo = shfl64(f, win);
+      lo += win * step;
       hi = min(hi, lo + step);
     }
     u = lo;
-    off = static_cast<int>(r - tiles_before(p, s, u, S));
+    off = static_cast<int>(r - at_lo);
   }
 
   // rest: tiles of the unit after this piece
@@ -264,8 +271,15 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// The same, and the 32 registers are not read before it.
+#define PA_W8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), \
+                    "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+__device__ __forceinline__ void tc_wait_ld32(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : PA_W8(r, 0), PA_W8(r, 8), PA_W8(r, 16), PA_W8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tc_use32(uint32_t *r) {   // orders reads of r after the wait above it
+  asm volatile("" : PA_W8(r, 0), PA_W8(r, 8), PA_W8(r, 16), PA_W8(r, 24)::"memory");
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -373,6 +387,45 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// 32 bytes to global memory; wide: the address is 32-byte aligned, and a whole sector goes at once
+__device__ __forceinline__ void store32(void *dst, const uint32_t *v, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), PA_I8(v, 0)
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
+
+// mbar_wait for the one warp that everything else waits for: it looks again at once, where
+// try_wait may put the warp to sleep and wake it late.
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
+  for (uint32_t it = 0; it < 16 * kWaitSpins; ++it) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
+// One look at a barrier: whether the phase with the given parity is complete.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  return mbar_wait<1>(bar, parity);
+}
+
 // ------------------------------------------------------------------ codes to bf16
 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
@@ -400,6 +453,11 @@ __device__ __forceinline__ uint32_t int4_pair_bf16(uint32_t w, uint32_t w4, int 
   return bf16x2_sub((x & 0x000F000Fu) | 0x43004300u, 0x43084308u);
 }
 
+__device__ __forceinline__ float lds_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -419,8 +477,8 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
 // keeps the two halves off each other's banks.
 template <int KIND>
 __device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, int lane) {
-  constexpr int kBatch = 4;
   if constexpr (KIND == PA_KV_FP8_E4M3) {
+    constexpr int kBatch = 8;
     const int c = lane & 7;                              // 16 codes: columns [16 c, 16 c + 16)
     for (int i0 = 0; i0 < 8; i0 += kBatch) {
       uint4 v[kBatch];
@@ -471,6 +529,25 @@ __device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, 
 
 // ------------------------------------------------------------------ the kernel
 
+// The order of the K and V tiles in the rings: in step j each stream has V of its tile j - 1,
+// then K of its tile j.  n: tiles of each stream.  Every warp that fills or reads a ring goes
+// through all of its tiles in this order: a barrier's parity tells its phase only from the
+// phases next to it.
+struct RingOrder {
+  int n0, n1, j;
+  uint32_t base;               // tiles before this step
+  __device__ __forceinline__ int n(int st) const { return st ? n1 : n0; }
+  __device__ __forceinline__ bool v(int st) const { return j > 0 && j - 1 < n(st); }
+  __device__ __forceinline__ bool k(int st) const { return j < n(st); }
+  __device__ __forceinline__ uint32_t v_at(int st) const { return base + (st ? v(0) + k(0) : 0); }
+  __device__ __forceinline__ uint32_t k_at(int st) const { return v_at(st) + v(st); }
+  __device__ __forceinline__ bool more() const { return j <= max(n0, n1) && n0 + n1 > 0; }
+  __device__ __forceinline__ void step() {
+    base += v(0) + k(0) + v(1) + k(1);
+    ++j;
+  }
+};
+
 // kKind: the pools' pa_kv_dtype.  Codes (D = 128) are restored to bf16 tiles, without their scale,
 // by four warps of their own: K's scale multiplies the scores of a page, V's its weights.
 template <int kD, int kKind, bool kShared>
@@ -487,14 +564,16 @@ struct AttendCfg {
   static constexpr int RING = 2 * TILE;                 // after the two Q tiles
   static constexpr int RAW_RING = RING + STAGES * TILE;
   static constexpr int SMEM = RAW_RING + (QUANT ? RAW * RAW_TILE : 0) + 1024;
-  // Warps 0-7 softmax, then (code pools) four that restore codes, then one each for the
-  // products, the loads and the pieces of each stream.  Registers are dealt out by groups of four
-  // warps: 384 threads start with 168, 64,512 in all, dealt anew as 256 x 208 + 128 x 88 (512
-  // with 128: 256 x 184 + 256 x 72): a softmax thread holds its row's 128 scores.
+  // Warps 0-7 softmax.  Then the products (shared form: a warp for each row tile, so that one's
+  // waits are filled by the other's products; separate form: one warp for both streams), the
+  // pieces, the loads (bf16: two warps with half of every tile's copies each, since a copy is slow
+  // to issue; code pools: one, and four warps that restore codes).  512 threads start with 128 registers, dealt anew
+  // by groups of four warps as 256 x 184 + 256 x 72: a softmax thread holds its row's 128 scores.
   static constexpr int THREADS = QUANT ? 512 : 384;
-  static constexpr int CODE_WARP = 8;
-  static constexpr int MMA_WARP = QUANT ? 12 : 8, LOAD_WARP = MMA_WARP + 1, PIECE_WARP = MMA_WARP + 2;
-  static constexpr int SOFTMAX_REGS = QUANT ? 184 : 208, OTHER_REGS = QUANT ? 72 : 88;
+  static constexpr int MMA_WARP = 8, PIECE_WARP = 10, LOAD_WARP = 11;
+  static constexpr int LOADERS = 1;
+  static constexpr int CODE_WARP = 12;                  // the last four (code pools)
+  static constexpr int SOFTMAX_REGS = QUANT ? 152 : 216, OTHER_REGS = QUANT ? 104 : 72;
   static constexpr int STREAMS = SHARED ? 1 : 2;        // key streams of a CTA
   static constexpr int PIECES = 8;                      // pieces known ahead per stream
   static constexpr int SCALES = 5;                      // tiles whose scales are held per stream
@@ -508,10 +587,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int kPieceBars = 2 * C::STAGES + 9, kRawBars = kPieceBars + 2 * C::STREAMS * C::PIECES;
+  constexpr int kTileBars = 2 * C::STAGES, kClean = 8, kPieceBars = kTileBars + 15 + kClean;
+  constexpr int kRawBars = kPieceBars + 2 * C::STREAMS * C::PIECES;
   constexpr int kBars = kRawBars + (C::QUANT ? 2 * C::RAW + C::STREAMS * C::SCALES : 0);
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ Piece pieces[C::STREAMS][C::PIECES];
+  __shared__ int stream_tiles[2];
   __shared__ uint32_t tmem_slot;
   // scales of the tiles on their way: K's pages (16 tokens each), then V's
   __shared__ float4 scales[C::STREAMS][C::QUANT ? C::SCALES : 1][4];
@@ -519,13 +600,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_u32(bars);
-  auto kv_full = [&](int i) { return bar0 + 8 * i; };
-  auto kv_empty = [&](int i) { return bar0 + 8 * (C::STAGES + i); };
-  auto q_full = [&](int t) { return bar0 + 8 * (2 * C::STAGES + t); };
-  auto s_full = [&](int t) { return bar0 + 8 * (2 * C::STAGES + 2 + t); };
-  auto p_ready = [&](int t) { return bar0 + 8 * (2 * C::STAGES + 4 + t); };
-  auto o_full = [&](int t) { return bar0 + 8 * (2 * C::STAGES + 6 + t); };
-  const uint32_t done_bar = bar0 + 8 * (2 * C::STAGES + 8);
+  auto kv_full = [&](uint32_t k) { return bar0 + 8 * (k % C::STAGES); };
+  auto kv_empty = [&](uint32_t k) { return bar0 + 8 * (C::STAGES + k % C::STAGES); };
+  auto kv_parity = [](uint32_t k) { return (k / C::STAGES) & 1; };
+  auto q_full = [&](int t) { return bar0 + 8 * (kTileBars + t); };
+  auto s_full = [&](int t) { return bar0 + 8 * (kTileBars + 2 + t); };
+  auto p_early = [&](int t) { return bar0 + 8 * (kTileBars + 4 + t); };
+  auto p_ready = [&](int t) { return bar0 + 8 * (kTileBars + 6 + t); };
+  auto o_full = [&](int t) { return bar0 + 8 * (kTileBars + 8 + t); };
+  auto done_bar = [&](int t) { return bar0 + 8 * (kTileBars + 10 + t); };
+  const uint32_t plan_bar = bar0 + 8 * (kTileBars + 12);
+  // the i-th V tile with rows that one product warp clears for both (shared form); the ring holds
+  // fewer such tiles than there are barriers
+  static_assert(C::STAGES / 2 + 1 < kClean, "a barrier of cleared tiles reused too early");
+  auto clean = [&](uint32_t i) { return bar0 + 8 * (kTileBars + 13 + i % kClean); };
+  // row tile t's turn at the tensor core (shared form)
+  auto turn = [&](int t) { return bar0 + 8 * (kTileBars + 13 + kClean + t); };
   // piece k of a stream is known / no longer needed
   auto pc_full = [&](int st, uint32_t k) {
     return bar0 + 8 * (kPieceBars + st * C::PIECES + k % C::PIECES);
@@ -533,21 +623,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto pc_empty = [&](int st, uint32_t k) {
     return bar0 + 8 * (kPieceBars + (C::STREAMS + st) * C::PIECES + k % C::PIECES);
   };
+  auto pc_parity = [](uint32_t k) { return (k / C::PIECES) & 1; };
   // code pools: code tiles landed / restored, scales of a stream's tile n stored
-  auto raw_full = [&](int i) { return bar0 + 8 * (kRawBars + i); };
-  auto raw_empty = [&](int i) { return bar0 + 8 * (kRawBars + C::RAW + i); };
+  auto raw_full = [&](uint32_t k) { return bar0 + 8 * (kRawBars + k % C::RAW); };
+  auto raw_empty = [&](uint32_t k) { return bar0 + 8 * (kRawBars + C::RAW + k % C::RAW); };
+  auto raw_parity = [](uint32_t k) { return (k / C::RAW) & 1; };
   auto sc_full = [&](int st, uint32_t n) {
     return bar0 + 8 * (kRawBars + 2 * C::RAW + st * C::SCALES + n % C::SCALES);
   };
   auto sc_parity = [](uint32_t n) { return (n / C::SCALES) & 1; };
-  auto pc_parity = [](uint32_t k) { return (k / C::PIECES) & 1; };
   const int S = C::SHARED ? 2 * p.tok : p.tok;
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(kv_full(i), C::QUANT ? 4 : 1);           // the restoring warps, or the copies
-      mbar_init(kv_empty(i), 1);
+      mbar_init(kv_full(i), C::QUANT ? 4 : C::LOADERS);  // the warps that fill it
+      mbar_init(kv_empty(i), C::SHARED ? 2 : 1);         // the product warps
     }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 1);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_early(t), 4);
+      mbar_init(p_ready(t), 4);
+      mbar_init(o_full(t), 1);
+      mbar_init(done_bar(t), 1);
+      mbar_init(turn(t), 1);
+    }
+    for (int i = 0; i < kClean; ++i) mbar_init(clean(i), 1);
+    mbar_init(plan_bar, 1);
+    for (int st = 0; st < C::STREAMS; ++st)
+      for (int k = 0; k < C::PIECES; ++k) {
+        mbar_init(pc_full(st, k), 1);
+        mbar_init(pc_empty(st, k), C::LOADERS + (C::SHARED ? 2 + 8 : 1 + 4));   // every reader
+      }
     if constexpr (C::QUANT) {
       for (int i = 0; i < C::RAW; ++i) {
         mbar_init(raw_full(i), 1);
@@ -556,18 +663,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (int st = 0; st < C::STREAMS; ++st)
         for (int n = 0; n < C::SCALES; ++n) mbar_init(sc_full(st, n), 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full(t), 1);
-      mbar_init(s_full(t), 1);
-      mbar_init(p_ready(t), 4);
-      mbar_init(o_full(t), 1);
-    }
-    mbar_init(done_bar, 1);
-    for (int st = 0; st < C::STREAMS; ++st)
-      for (int k = 0; k < C::PIECES; ++k) {
-        mbar_init(pc_full(st, k), 1);
-        mbar_init(pc_empty(st, k), 2 + (C::SHARED ? 8 : 4) + (C::QUANT ? 4 : 0));   // every reader
-      }
     fence_mbar_init();
   }
   if (warp == C::MMA_WARP) {
@@ -579,17 +674,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   pdl_trigger();
   pdl_wait();
 
-  // every CTA counts the tiles: one sum per group of 32 sequences, in the space of the last
-  // stage of the ring (which the loads wait for the piece warps to be done with)
+  // Every CTA counts the tiles of the batch.  Past 32 sequences all warps do, one sum per group of
+  // 32, in the space of the last stage of the ring (whose first tile comes after the plan).
   int64_t *sums = reinterpret_cast<int64_t *>(smem_raw + (sm - smem_u32(smem_raw)) + C::RING +
                                               (C::STAGES - 1) * C::TILE);
   const int groups = (p.B + 31) / 32;
-  for (int g = warp; g < groups; g += C::THREADS / 32) {
-    const int b = g * 32 + lane;
-    int64_t t = 0;
-    if (b < p.B) t = seq_tiles_total(p, load_seq(p, b, blockIdx.x == 0 ? p.err : nullptr), S);
-    t = scan64(t, lane);
-    if (lane == 31) sums[g] = t;
+  int32_t *report = blockIdx.x == 0 ? p.err : nullptr;
+  if (groups > 1) {
+    for (int g = warp; g < groups; g += C::THREADS / 32) {
+      Group x;
+      x.load(p, g, S, lane, report);
+      if (lane == 31) sums[g] = x.upto;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -597,6 +693,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t tmem = tmem_slot;
 
   bool ok = true;
+  // the next piece of a stream, for one of the warps that read them; false after the last
+  auto read_piece = [&](int st, uint32_t k, Piece &x) {
+    ok = ok && mbar_wait(pc_full(st, k), pc_parity(k));
+    if (!ok) return false;
+    x = pieces[st][k % C::PIECES];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(pc_empty(st, k));
+    return x.n > 0;
+  };
+  auto ring_order = [&] {
+    RingOrder r{0, 0, 0, 0};
+    ok = mbar_wait(plan_bar, 0);
+    if (ok) {
+      r.n0 = stream_tiles[0];
+      r.n1 = stream_tiles[1];
+    }
+    return r;
+  };
+
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SOFTMAX_REGS));
     // ---------------------------------------------------------------- softmax, one thread per row
@@ -617,13 +732,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     x.row + tok0, q_full(t));
       ++q_loads;
     };
-    for (uint32_t k = 0;; ++k) {
-      ok = mbar_wait(pc_full(st, k), pc_parity(k));
-      if (!ok) break;
-      const Piece x = pieces[st][k % C::PIECES];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(pc_empty(st, k));
-      if (x.n == 0) break;
+    Piece x;
+    for (uint32_t k = 0; read_piece(st, k, x); ++k) {
       const uint32_t tile0 = tiles;
       tiles += x.n;
       const int ntok = min(p.tok, x.ntok - tok0);        // tokens of this tile
@@ -648,8 +758,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!ok) break;
         s_phase ^= 1;
         if (i == x.n - 1 && row == 0) {
-          // the products with this Q tile are done: the next piece's may come, if that piece is
-          // known (it is, but for a piece that this row tile has no part in)
+          // the products with this Q tile are done: the next piece's may come, if this row tile has
+          // part in it
           const uint32_t k1 = k + 1;
           if (mbar_wait(pc_full(st, k1), pc_parity(k1))) {
             const Piece &y = pieces[st][k1 % C::PIECES];
@@ -662,86 +772,144 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         tc_fence_after();
         if (warp_live) {
-          uint32_t s[kKeys];
-#pragma unroll
-          for (int j = 0; j < kKeys; j += 32) tc_ld32(s + j, tS + j);
-          tc_wait_ld();
-          const float *sc = nullptr;                     // 8 K scales, 8 V scales
+          // code pools: the scales of the tile's pages, read where they are used
+          [[maybe_unused]] uint32_t sc = 0;
           if constexpr (C::QUANT) {
             const uint32_t n = tile0 + i;
             ok = mbar_wait(sc_full(st, n), sc_parity(n));
-            sc = reinterpret_cast<const float *>(scales[st][n % C::SCALES]);
+            sc = smem_u32(scales[st][n % C::SCALES]);
+          }
+          // what a page's scores are multiplied by; above zero, so that -inf stays -inf
+          auto k_factor = [&](int page) {
+            return C::QUANT ? fmaxf(lds_f32(sc + 4 * page) * p.c, 1e-30f) : p.c;
+          };
+          const bool edge = key0 < all_lo || key0 + kKeys > all_hi;
+          const int first = lo - key0;                   // columns [first, first + seen) count
+          const unsigned seen = static_cast<unsigned>(max(0, hi - lo));
+          auto hide = [&](uint32_t *s, int j0) {         // columns [j0, j0 + 32) of the row
+            if (edge) {
 #pragma unroll
-            for (int j = 0; j < kKeys; j += 2) {
-              const float f = sc[j / 16] * p.c;
-              const float2 y = mul2(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])),
-                                    make_float2(f, f));
-              s[j] = __float_as_uint(y.x);
-              s[j + 1] = __float_as_uint(y.y);
+              for (int j = 0; j < 32; ++j)
+                if (static_cast<unsigned>(j0 + j - first) >= seen) s[j] = __float_as_uint(-INFINITY);
+            }
+          };
+          float mx[2] = {-INFINITY, -INFINITY};
+          auto maximum = [&](const uint32_t *s, int j0) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+              float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = j; e < j + 16; e += 4) {
+                y[0] = fmaxf(y[0], fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                y[1] = fmaxf(y[1], fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+              }
+              const float page = fmaxf(y[0], y[1]);
+              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT ? page * k_factor((j0 + j) / 16) : page);
+            }
+          };
+          // bf16 pools: the row's scores stay in registers; code pools, whose threads have fewer,
+          // read them twice.  A block of 32 columns is on its way while another is worked on.
+          uint32_t s[C::QUANT ? 64 : kKeys];
+          if constexpr (C::QUANT) {
+            tc_ld32(s + 32, tS + 96);
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {
+              uint32_t *now = s + 32 * (j & 1);
+              tc_wait_ld32(now);
+              if (j > 0) tc_ld32(s + 32 * (~j & 1), tS + 32 * (j - 1));
+              hide(now, 32 * j);
+              maximum(now, 32 * j);
+            }
+          } else {
+            tc_ld32(s, tS);
+            tc_ld32(s + 32, tS + 32);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              tc_wait_ld32(s + 64 * half);
+              tc_use32(s + 64 * half + 32);
+              if (half == 0) {
+                tc_ld32(s + 64, tS + 64);
+                tc_ld32(s + 96, tS + 96);
+              }
+#pragma unroll
+              for (int j = 64 * half; j < 64 * half + 64; j += 32) {
+                hide(s + j, j);
+                maximum(s + j, j);
+              }
             }
           }
-          if (key0 < all_lo || key0 + kKeys > all_hi) {
-            const int a = lo - key0;
-            const unsigned n = static_cast<unsigned>(max(0, hi - lo));
-#pragma unroll
-            for (int j = 0; j < kKeys; ++j)
-              if (static_cast<unsigned>(j - a) >= n) s[j] = __float_as_uint(-INFINITY);
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int j = 0; j < kKeys; j += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(s[j + e]), __uint_as_float(s[j + 4 + e])));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * (C::QUANT ? 1.f : p.c);
+          const float top = fmaxf(mx[0], mx[1]) * (C::QUANT ? 1.f : p.c);
           if (m == -INFINITY) m = top;                   // O and l are zero so far
           // the reference moves only past kMaxJump octaves: weights stay below 2^8, far
           // inside bf16 and fp32, and O is seldom rescaled
           const bool jump = live && l > 0.f && top > m + kMaxJump;
           if (__any_sync(0xffffffffu, jump)) {
-            const float f = jump ? ex2(m - top) : 1.f;
+            const float g = jump ? ex2(m - top) : 1.f;
             if (jump) m = top;
-            l *= f;
-#pragma unroll
+            l *= g;
+#pragma unroll 1
             for (int j = 0; j < C::D; j += 32) {
               uint32_t o[32];
               tc_ld32(o, tO + j);
-              tc_wait_ld();
+              tc_wait_ld32(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
               tc_st32(tO + j, o);
             }
-            tc_wait_st();
           }
-          const float2 c2 = make_float2(p.c, p.c);
           const float neg = m == -INFINITY ? 0.f : -m;
           const float2 n2 = make_float2(neg, neg);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float2 sum[2] = {};
 #pragma unroll
-          for (int j = 0; j < kKeys; j += 32) {
+          for (int j = 0; j < 4; ++j) {                  // 32 columns at a time; block 0 is here
+            uint32_t *now = C::QUANT ? s + 32 * (j & 1) : s + 32 * j;
+            if constexpr (C::QUANT) {
+              if (j > 0) {
+                tc_wait_ld32(now);
+                hide(now, 32 * j);
+              }
+              if (j < 3) tc_ld32(s + 32 * (~j & 1), tS + 32 * (j + 1));
+            }
             uint32_t packed[16];
+            float c1 = p.c, v1 = 1.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              float2 y = make_float2(__uint_as_float(s[j + 2 * e]), __uint_as_float(s[j + 2 * e + 1]));
-              y = C::QUANT ? add2(y, n2) : fma2(y, c2, n2);
+              if constexpr (C::QUANT) {
+                if (e % 8 == 0) {
+                  c1 = k_factor(2 * j + e / 8);
+                  v1 = lds_f32(sc + 32 + 4 * (2 * j + e / 8));
+                }
+              }
+              float2 y = fma2(make_float2(__uint_as_float(now[2 * e]), __uint_as_float(now[2 * e + 1])),
+                              make_float2(c1, c1), n2);
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum[e & 1] = add2(sum[e & 1], y);
-              if constexpr (C::QUANT) {
-                const float f = sc[8 + (j + 2 * e) / 16];
-                y = mul2(y, make_float2(f, f));
-              }
+              if constexpr (C::QUANT) y = mul2(y, make_float2(v1, v1));
               packed[e] = pack_bf16(y.x, y.y);
             }
-            tc_st16(tS + j / 2, packed);
+            tc_st16(tS + 16 * j, packed);                // over columns already read
+            if (j == kEarly / 32 - 1) {
+              tc_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(p_early(t));    // the second product may begin
+            }
           }
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready(t));
           const float2 both = add2(sum[0], sum[1]);
           l += both.x + both.y;
-          tc_wait_st();
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(p_early(t));
+            mbar_arrive(p_ready(t));
+          }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready(t));
       }
       if (!ok) break;
       ok = mbar_wait(o_full(t), o_phase);
@@ -757,19 +925,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int j = 0; j < C::D; j += 32) {
             uint32_t o[32];
             tc_ld32(o, tO + j);
-            tc_wait_ld();
+            tc_wait_ld32(o);
+            uint32_t v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              v[e] = l > 0.f ? pack_bf16(__uint_as_float(o[2 * e]) * inv,
+                                         __uint_as_float(o[2 * e + 1]) * inv)
+                             : 0u;
             if (live) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint4 v;
-                uint32_t *u = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  u[i] = l > 0.f ? pack_bf16(__uint_as_float(o[8 * e + 2 * i]) * inv,
-                                             __uint_as_float(o[8 * e + 2 * i + 1]) * inv)
-                                 : 0u;
-                reinterpret_cast<uint4 *>(dst + j)[e] = v;
-              }
+              store32(dst + j, v, p.wide);
+              store32(dst + j + 16, v + 8, p.wide);
             }
           }
         } else {
@@ -781,12 +946,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           for (int j = 0; j < C::D; j += 32) {
             uint32_t o[32];
             tc_ld32(o, tO + j);
-            tc_wait_ld();
+            tc_wait_ld32(o);
             if (live) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                reinterpret_cast<uint4 *>(dst + j)[e] =
-                    make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 4; ++e) store32(dst + j + 8 * e, o + 8 * e, true);
             }
           }
         }
@@ -798,321 +961,379 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (uint32_t k = q_used > 0 ? q_used - 1 : 0; k < q_loads; ++k) mbar_wait(q_full(t), k & 1);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-    if (warp >= C::PIECE_WARP) {
-      // ---------------------------------------------------------------- the pieces of a stream
-      const int st = warp - C::PIECE_WARP;
-      if (st < C::STREAMS) {
-        const int worker = blockIdx.x * C::STREAMS + st;
-        int64_t total = 0;
+    if (warp == C::PIECE_WARP) {
+      // ---------------------------------------------------------------- the pieces of the streams
+      Group group;
+      group.g = -1;
+      int64_t total = 0;
+      if (groups == 1) {
+        group.load(p, 0, S, lane, report);
+        total = shfl64(group.upto, 31);
+      } else {
         for (int g = lane; g < groups; g += 32) total += sums[g];
         total = shfl64(scan64(total, lane), 31);
-        const int64_t width = div_up(total, p.workers);
-        const int64_t first = min(total, worker * width);
-        Walker walk;
-        walk.init(p, sums, first, min(total, first + width), S, lane);
-        fence_proxy_async();               // the sums' space is the ring's from here
-        __syncwarp();
-        int4 cut = make_int4(0, 0, 0, 0);
-        for (uint32_t k = 0;; ++k) {
-          Piece x;
-          int rest = 0;
-          const bool more = walk.next(p, S, x, rest);
-          ok = mbar_wait(pc_empty(st, k), pc_parity(k) ^ 1);
-          if (!ok) break;
-          if (lane == 0) {
-            pieces[st][k % C::PIECES] = x;
-            mbar_arrive(pc_full(st, k));
-          }
-          if (!more) break;
-          if (x.starts && !x.ends)
-            cut = make_int4(x.row, x.ntok, x.h, (rest - 1) / static_cast<int>(width) + 1);
-        }
-        if (lane == 0) p.cut[worker] = cut;
       }
-    } else if (warp == C::LOAD_WARP) {
+      const int64_t width = p.workers == 1 ? total
+                                           : static_cast<int64_t>(__umul64hi(
+                                                 static_cast<uint64_t>(total + p.workers - 1),
+                                                 p.over_workers));
+      // this stream's walker and, in the separate form, the other's; they change places
+      Walker walk{}, other{};
+      int4 cut = make_int4(0, 0, 0, 0), other_cut = cut;
+      uint32_t known = 0, other_known = 0;               // pieces published
+      bool over = false, other_over = C::STREAMS == 1;
+      auto swap_streams = [&] {
+        if constexpr (C::STREAMS == 2) {
+          const Walker w = walk;
+          walk = other;
+          other = w;
+          const int4 c4 = cut;
+          cut = other_cut;
+          other_cut = c4;
+          const uint32_t n = known;
+          known = other_known;
+          other_known = n;
+          const bool o = over;
+          over = other_over;
+          other_over = o;
+        }
+      };
+#pragma unroll 1
+      for (int st = 0; st < C::STREAMS; ++st) {
+        const int worker = blockIdx.x * C::STREAMS + st;
+        const int64_t first = min(total, worker * width);
+        walk.init(p, group, sums, first, min(total, first + width), S, lane);
+        if (lane == 0) stream_tiles[st] = walk.remaining;
+        swap_streams();
+      }
+      if (C::STREAMS == 1 && lane == 0) stream_tiles[1] = 0;
+      fence_proxy_async();               // the sums' space is the ring's from here
+      __syncwarp();
+      if (lane == 0) mbar_arrive(plan_bar);
+      int st = 0;
+      uint32_t idle = 0;
+#pragma unroll 1
+      while (!(over && other_over)) {
+        if (!over) {
+          // the shared form may wait for room; the separate one looks at its streams in turn (the
+          // readers of one may need the other's next piece), and sleeps rather than take issue slots
+          // from the softmax
+          const bool room = C::STREAMS == 1
+                                ? mbar_wait(pc_empty(st, known), pc_parity(known) ^ 1)
+                                : mbar_test(pc_empty(st, known), pc_parity(known) ^ 1);
+          if (room) {
+            idle = 0;
+            Piece x;
+            int rest = 0;
+            over = !walk.next(p, S, x, rest);
+            if (lane == 0) {
+              pieces[st][known % C::PIECES] = x;
+              mbar_arrive(pc_full(st, known));
+            }
+            ++known;
+            if (!over && x.starts && !x.ends)
+              cut = make_int4(x.row, x.ntok, x.h, (rest - 1) / static_cast<int>(width) + 1);
+          } else if (C::STREAMS == 1 || ++idle > kWaitSpins / 16) {
+            ok = false;
+            break;
+          } else {
+            __nanosleep(200);
+          }
+        }
+        if (C::STREAMS == 2) {
+          swap_streams();
+          st ^= 1;
+        }
+      }
+      if (lane == 0) {
+        p.cut[blockIdx.x * C::STREAMS + st] = cut;
+        if (C::STREAMS == 2) p.cut[blockIdx.x * C::STREAMS + (st ^ 1)] = other_cut;
+      }
+    } else if (warp >= C::LOAD_WARP && warp < C::LOAD_WARP + C::LOADERS) {
       // ---------------------------------------------------------------- K and V tiles
-      // lane (half, page): one box of 16 tokens x 64 columns; code pools: x a whole row, by lanes
-      // 0-7, while lanes 0-7 and 8-15 fetch the pages' K and V scales
-      const int page = lane & 7, half = C::QUANT ? 0 : lane >> 3;
-      const bool loads = lane < 8 * (C::QUANT ? 1 : C::HALVES);
+      // One box per 16 tokens (a page of a tile) and, in bf16 pools, 64 columns.
+      constexpr int kBox = C::QUANT ? 16 * C::CODE_ROW : 16 * 128;
       constexpr int kRing = C::QUANT ? C::RAW : C::STAGES;
-      auto ring_full = [&](int i) { return C::QUANT ? raw_full(i) : kv_full(i); };
-      auto ring_empty = [&](int i) { return C::QUANT ? raw_empty(i) : kv_empty(i); };
-      struct Tile {
-        bool ok;
-        int h, boxes, blk, g;                              // blk < 0: this lane loads nothing
-        float scale;
+      const int outside = p.nblocks * p.bs;              // a row past the pool reads zeros
+      // Block ids come four tiles (32 runs of 16 tokens, one per lane) at a time, two such chunks
+      // ahead of the copies; scales one.
+      struct Chunk {
+        int h, tile, n, L, lo;                           // n = 0: none
+        int row;                                         // this lane's first pool row; -1: unseen
+        float ks, vs;
       };
-      Piece pc[C::STREAMS] = {};
-      int at[C::STREAMS] = {};
-      uint32_t seen[C::STREAMS] = {};
-      bool over[C::STREAMS] = {};
-      Tile cur[C::STREAMS] = {}, prev[C::STREAMS] = {};
-      auto fetch = [&](int st) {
-        Tile t{};
-        if (over[st]) return t;
-        Piece &x = pc[st];
-        if (at[st] == x.n) {
-          const uint32_t k = seen[st]++;
-          ok = ok && mbar_wait(pc_full(st, k), pc_parity(k));
-          if (!ok) return t;
-          x = pieces[st][k % C::PIECES];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pc_empty(st, k));
-          at[st] = 0;
-          over[st] = x.n == 0;
-          if (over[st]) return t;
+      struct Src {
+        Piece x;
+        int at;
+        uint32_t k;
+        bool over;
+        Chunk cur, nxt;
+        int i;
+      } src[C::STREAMS];
+      auto fetch_chunk = [&](int st) {
+        Chunk c{};
+        Src &z = src[st];
+        if (z.over) return c;
+        if (z.at == z.x.n) {
+          z.over = !read_piece(st, z.k++, z.x);
+          z.at = 0;
+          if (z.over) return c;
         }
-        const int first = (x.tile + at[st]) * kKeys;
-        ++at[st];
-        t.ok = true;
-        t.h = x.h;
-        const int hi = min(x.L, first + kKeys), lo = max(x.lo, first);
-        t.boxes = hi > lo ? (hi + 15) / 16 - lo / 16 : 0;
-        t.g = first + 16 * page;
-        t.blk = -1;
-        if (t.g < hi && t.g + 16 > lo)
-          t.blk = p.block_tables[static_cast<int64_t>(x.seq) * p.max_blocks + t.g / p.bs] & 0x7fffffff;
-        return t;
+        c.h = z.x.h;
+        c.tile = z.x.tile + z.at;
+        c.n = min(4, z.x.n - z.at);
+        z.at += c.n;
+        c.L = z.x.L;
+        c.lo = z.x.lo;
+        c.row = -1;
+        const int g = c.tile * kKeys + 16 * lane;
+        if (g < c.L && g + 16 > c.lo && lane < 8 * c.n)
+          c.row = p.block_tables[static_cast<int64_t>(z.x.seq) * p.max_blocks + g / p.bs] & 0x7fffffff;
+        return c;
       };
-      uint32_t count = 0;
-      auto issue = [&](const CUtensorMap *map, const Tile &t) {
-        const int stage = count % kRing;
-        ok = ok && mbar_wait(ring_empty(stage), ((count / kRing) & 1) ^ 1);
-        if (!ok) return;
-        ++count;
-        constexpr int kBox = C::QUANT ? 16 * C::CODE_ROW : 16 * 128;
-        if (lane == 0)
-          mbar_arrive_expect_tx(ring_full(stage), t.boxes * kBox * (C::QUANT ? 1 : C::HALVES));
-        __syncwarp();
-        if (loads && t.blk >= 0) {
-          int row = p.nblocks * p.bs;                      // outside the pool: reads zeros
-          if (t.blk < p.nblocks)
-            row = t.blk * p.bs + t.g % p.bs;
-          else
+      // block id to pool row (and the scales on their way), when it has come
+      auto resolve = [&](Chunk &c) {
+        c.ks = c.vs = 0.f;
+        if (c.row >= 0) {
+          if (c.row < p.nblocks) {
+            if constexpr (C::QUANT) {
+              const int64_t i = static_cast<int64_t>(c.row) * p.Hkv + c.h;
+              c.ks = p.k_scale[i];
+              c.vs = p.v_scale[i];
+            }
+            c.row = c.row * p.bs + (c.tile * kKeys + 16 * lane) % p.bs;
+          } else {
             set_err(p.err, PA_DEVERR_BLOCK_ID);
-          if constexpr (C::QUANT)
-            tma_load_2d(sm + C::RAW_RING + stage * C::RAW_TILE + page * kBox, map, t.h * C::CODE_ROW,
-                        row, ring_full(stage));
-          else
-            tma_load_2d(sm + C::RING + stage * C::TILE + half * (kKeys * 128) + page * kBox, map,
-                        t.h * C::D + half * 64, row, ring_full(stage));
+            c.row = outside;
+          }
         }
       };
-      // A tile's block ids are fetched two tiles ahead of its copy and its scales one ahead.
-      uint32_t tiles[C::STREAMS] = {};
-      Tile nxt[C::STREAMS] = {};
-      auto fetch_scale = [&](Tile &t) {
-        t.scale = 0.f;
-        if (C::QUANT && t.ok && lane < 16 && t.blk >= 0 && t.blk < p.nblocks)
-          t.scale = (lane < 8 ? p.k_scale : p.v_scale)[static_cast<int64_t>(t.blk) * p.Hkv + t.h];
+      uint32_t issued = 0;                               // the last tile this warp has issued, + 1
+      // rows: the pages' first pool rows, in every lane (-1: unseen)
+      auto issue = [&](const CUtensorMap *map, uint32_t k, int h, const int (&rows)[8], bool zeros) {
+        const uint32_t full = C::QUANT ? raw_full(k) : kv_full(k);
+        ok = ok && mbar_wait(C::QUANT ? raw_empty(k) : kv_empty(k), ((k / kRing) & 1) ^ 1);
+        if (!ok) return;
+        issued = k + 1;
+        if (elect_one()) {
+          uint32_t boxes = 0;
+#pragma unroll
+          for (int page = 0; page < 8; ++page) boxes += rows[page] >= 0 || zeros;
+          mbar_arrive_expect_tx(full, boxes * kBox * (C::QUANT ? 1 : C::HALVES));
+          const uint32_t dst = C::QUANT ? sm + C::RAW_RING + (k % kRing) * C::RAW_TILE
+                                        : sm + C::RING + (k % kRing) * C::TILE;
+#pragma unroll
+          for (int page = 0; page < 8; ++page) {
+            if (rows[page] < 0 && !zeros) continue;
+            const int row = rows[page] < 0 ? outside : rows[page];
+#pragma unroll
+            for (int half = 0; half < (C::QUANT ? 1 : C::HALVES); ++half)
+              tma_load_2d(dst + half * (kKeys * 128) + page * kBox, map,
+                          h * (C::QUANT ? C::CODE_ROW : C::D) + half * 64, row, full);
+          }
+        }
+        __syncwarp();
       };
+      RingOrder r = ring_order();
+      int prev_h[C::STREAMS] = {}, rows[C::STREAMS][8] = {};
+      uint32_t tiles[C::STREAMS] = {};
 #pragma unroll
       for (int st = 0; st < C::STREAMS; ++st) {
-        cur[st] = fetch(st);
-        fetch_scale(cur[st]);
-        if (cur[st].ok) nxt[st] = fetch(st);
+        Src &z = src[st];
+        z.x.n = z.at = z.i = 0;
+        z.k = 0;
+        z.over = false;
+        z.cur = fetch_chunk(st);
+        z.nxt = fetch_chunk(st);
+        resolve(z.cur);
       }
-      for (bool more = true; more && ok;) {
-        more = false;
+      auto next_tile = [&](int st, int &h, int (&to)[8]) {
+        Src &z = src[st];
+        if (z.i == z.cur.n) {
+          z.cur = z.nxt;
+          resolve(z.cur);
+          z.nxt = fetch_chunk(st);
+          z.i = 0;
+        }
+        h = z.cur.h;
+#pragma unroll
+        for (int page = 0; page < 8; ++page)
+          to[page] = __shfl_sync(0xffffffffu, z.cur.row, z.i * 8 + page);
+        if constexpr (C::QUANT) {
+          const uint32_t n = tiles[st]++;
+          float *sc = reinterpret_cast<float *>(scales[st][n % C::SCALES]);
+          if ((lane >> 3) == z.i) {
+            sc[lane & 7] = z.cur.ks;
+            sc[8 + (lane & 7)] = z.cur.vs;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sc_full(st, n));
+        }
+        ++z.i;
+      };
+      for (; ok && r.more(); r.step()) {
 #pragma unroll
         for (int st = 0; st < C::STREAMS; ++st) {
-          if (!ok || !(prev[st].ok || cur[st].ok)) continue;
-          more = true;
-          fetch_scale(nxt[st]);
-          const Tile far = nxt[st].ok ? fetch(st) : Tile{};
-          if (prev[st].ok) issue(&tmV, prev[st]);
-          if (cur[st].ok) {
-            if constexpr (C::QUANT) {
-              const uint32_t n = tiles[st]++;
-              if (lane < 16) reinterpret_cast<float *>(scales[st][n % C::SCALES])[lane] = cur[st].scale;
-              __syncwarp();
-              if (lane == 0) mbar_arrive(sc_full(st, n));
-            }
-            issue(&tmK, cur[st]);
+          // pages of V that no token sees read zeros (bf16): a weight of 0 times what lies there
+          // must be 0; codes are never infinite or NaN once restored
+          if (r.v(st)) issue(&tmV, r.v_at(st), prev_h[st], rows[st], !C::QUANT);
+          if (ok && r.k(st)) {
+            next_tile(st, prev_h[st], rows[st]);
+            issue(&tmK, r.k_at(st), prev_h[st], rows[st], false);
           }
-          prev[st] = cur[st];
-          cur[st] = nxt[st];
-          nxt[st] = far;
         }
       }
-      if (!ok) {
-        // the copies in flight land in this CTA's memory: wait for them before leaving
-        for (uint32_t k = count > kRing ? count - kRing : 0; k < count; ++k)
-          mbar_wait(ring_full(k % kRing), (k / kRing) & 1);
-      }
-    } else if (C::QUANT && warp < C::MMA_WARP) {
+      // after a wait that gave up, the copies in flight must have landed before the CTA's memory goes
+      if (!ok)
+        for (uint32_t k = issued > kRing ? issued - kRing : 0; k < issued; ++k)
+          mbar_wait(C::QUANT ? raw_full(k) : kv_full(k), (k / kRing) & 1);
+    } else if (C::QUANT && warp >= C::CODE_WARP) {
       // ---------------------------------------------------------------- codes to bf16 tiles
-      // in the order of the ring, until the pieces' tiles are all done
-      uint32_t todo[C::STREAMS] = {}, next_piece[C::STREAMS] = {}, count = 0;
-      bool over[C::STREAMS] = {};
-      bool v_due[C::STREAMS] = {};
-      auto one = [&] {
-        const int from = count % C::RAW, to = count % C::STAGES;
-        ok = ok && mbar_wait(raw_full(from), (count / C::RAW) & 1) &&
-             mbar_wait(kv_empty(to), ((count / C::STAGES) & 1) ^ 1);
-        if (!ok) return;
-        ++count;
-        restore_tile<C::KIND>(sm + C::RAW_RING + from * C::RAW_TILE, sm + C::RING + to * C::TILE,
-                              warp - C::CODE_WARP, lane);
+      const RingOrder r = ring_order();
+      const uint32_t all = 2 * (r.n0 + r.n1);
+      for (uint32_t k = 0; ok && k < all; ++k) {
+        ok = mbar_wait(raw_full(k), raw_parity(k)) && mbar_wait(kv_empty(k), kv_parity(k) ^ 1);
+        if (!ok) break;
+        restore_tile<C::KIND>(sm + C::RAW_RING + (k % C::RAW) * C::RAW_TILE,
+                              sm + C::RING + (k % C::STAGES) * C::TILE, warp - C::CODE_WARP, lane);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(raw_empty(from));
-          mbar_arrive(kv_full(to));
-        }
-      };
-      for (bool more = true; more && ok;) {
-        more = false;
-#pragma unroll
-        for (int st = 0; st < C::STREAMS; ++st) {
-          if (todo[st] == 0 && !over[st]) {
-            const uint32_t k = next_piece[st]++;
-            ok = ok && mbar_wait(pc_full(st, k), pc_parity(k));
-            if (!ok) break;
-            todo[st] = pieces[st][k % C::PIECES].n;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pc_empty(st, k));
-            over[st] = todo[st] == 0;
-          }
-          if (v_due[st]) one();                          // V of the tile before
-          v_due[st] = todo[st] > 0;
-          if (v_due[st]) {
-            --todo[st];
-            one();                                       // K
-            more = true;
-          }
+          mbar_arrive(raw_empty(k));
+          mbar_arrive(kv_full(k));
         }
       }
-    } else if (warp == C::MMA_WARP) {
+    } else if (warp < C::MMA_WARP + 2) {
       // ---------------------------------------------------------------- matrix products
+      // shared form: this warp's row tile t0; separate form: row tile st of each stream, by one warp
+      const int t0 = warp - C::MMA_WARP;
       const uint32_t idS = mma_desc(kKeys, false) | (p.negate ? kNegateA : 0u);
       constexpr uint32_t idO = mma_desc(C::D, true);
-      struct Tile {
-        bool ok, first, last, two;
-        int tile, lo, L;
-      };
-      Piece pc[C::STREAMS] = {};
-      int at[C::STREAMS] = {};
-      uint32_t seen[C::STREAMS] = {};
-      bool over[C::STREAMS] = {};
-      Tile cur[C::STREAMS] = {}, prev[C::STREAMS] = {};
-      auto fetch = [&](int st) {
-        Tile t{};
-        if (over[st]) return t;
-        if (at[st] == pc[st].n) {
-          const uint32_t k = seen[st]++;
-          ok = ok && mbar_wait(pc_full(st, k), pc_parity(k));
-          if (!ok) return t;
-          pc[st] = pieces[st][k % C::PIECES];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pc_empty(st, k));
-          at[st] = 0;
-          over[st] = pc[st].n == 0;
-          if (over[st]) return t;
-        }
-        t.ok = true;
-        t.first = at[st] == 0;
-        t.two = C::SHARED && pc[st].ntok > p.tok;
-        t.tile = pc[st].tile + at[st];
-        t.lo = pc[st].lo;
-        t.L = pc[st].L;
-        t.last = ++at[st] == pc[st].n;
-        return t;
-      };
-      uint32_t count = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      // rows of a V tile that no token sees may hold anything: they become zeros, since
-      // 0 * NaN would reach the sum
-      auto clear_unseen = [&](const Tile &t, int stage) {
-        const int a = t.lo - t.tile * kKeys, z = t.L - t.tile * kKeys;     // seen rows [a, z)
-        if (a <= 0 && z >= kKeys) return;
-        const uint32_t base = sm + C::RING + stage * C::TILE;
-        for (int r = 0; r < kKeys; ++r) {
-          if (r >= a && r < z) continue;
-          if (lane < 8 * C::HALVES)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                             base + (lane >> 3) * (kKeys * 128) + r * 128 + (lane & 7) * 16),
-                         "r"(0u)
-                         : "memory");
-        }
-        fence_proxy_async();
-        __syncwarp();
-      };
-      auto mma_s = [&](int t, int stage) {                 // S_t = Q_t K^T
-        if (lane == 0) {
-          const uint64_t a = smem_desc(sm + t * C::TILE, 16, 1024);
-          const uint64_t b = smem_desc(sm + C::RING + stage * C::TILE, 16, 1024);
-  #pragma unroll
-          for (int k = 0; k < C::D / 16; ++k) {
-            const uint32_t o = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
-            tc_mma_ss(tmem + t * kKeys, a + o, b + o, idS, k > 0);
-          }
-          tc_commit(s_full(t));
-        }
-        __syncwarp();
-      };
-      auto mma_o = [&](int t, int stage, const Tile &x) {  // O_t += P_t V
-        if (lane == 0) {
-          const uint64_t b = smem_desc(sm + C::RING + stage * C::TILE, kKeys * 128, 1024);
-  #pragma unroll
-          for (int k = 0; k < kKeys / 16; ++k)
-            tc_mma_ts(tmem + 256 + t * 128, tmem + t * kKeys + k * 8, b + ((k * 16 * 128) >> 4), idO,
-                      !x.first || k > 0);
-          if (x.last) tc_commit(o_full(t));
-        }
-        __syncwarp();
-      };
-      auto full = [&](uint32_t k) {
-        ok = ok && mbar_wait(kv_full(k % C::STAGES), (k / C::STAGES) & 1);
-      };
-      auto release = [&](uint32_t k) {
-        if (ok && lane == 0) tc_commit(kv_empty(k % C::STAGES));
-      };
-  #pragma unroll
-      for (int st = 0; st < C::STREAMS; ++st) cur[st] = fetch(st);
-      for (bool more = true; more && ok;) {
-        more = false;
-  #pragma unroll
+      const uint64_t q_desc = smem_desc(sm, 16, 1024);
+      const uint64_t k_desc = smem_desc(sm + C::RING, 16, 1024);
+      const uint64_t v_desc = smem_desc(sm + C::RING, kKeys * 128, 1024);
+      struct Stream {
+        Piece x;
+        int i;                                           // the piece's tile that K is due of
+        uint32_t piece, q_phase, p_phase;
+        // the tile that V is due of: first / last of its piece, the rows [lo, hi) of it that some
+        // token sees, whether this row tile has part in it
+        bool first, last, mine;
+        int lo, hi;
+      } z[C::STREAMS] = {};
+      uint32_t cleared = 0;
+      // Shared form: the row tiles take turns at the tensor core, O_t += P_t V and the next S_t at a
+      // time.  Left to themselves their products would run interleaved and end together, and then
+      // both softmaxes would run while the tensor core waits.
+      // A barrier is slow to look at while the tensor core reads shared memory, so everything but
+      // the weights' last part is waited for ahead of the turn, and the turn goes on while the last
+      // products are still being issued.
+      uint32_t turns = 0;
+      if (C::SHARED && t0 == 1 && lane == 0) mbar_arrive(turn(0));
+      RingOrder r = ring_order();
+      for (; ok && r.more() && t0 < 3 - C::STREAMS; r.step()) {
+#pragma unroll
         for (int st = 0; st < C::STREAMS; ++st) {
-          const bool v = prev[st].ok, k = cur[st].ok;
-          if (!ok || !(v || k)) continue;
-          more = true;
-          const uint32_t vk = count, kk = count + (v ? 1 : 0);
-          count = kk + (k ? 1 : 0);
-  #pragma unroll
-          for (int i = 0; i < (C::SHARED ? 2 : 1); ++i) {
-            const int t = C::SHARED ? i : st;
-            if (v && (i == 0 || prev[st].two)) {
-              if (i == 0) {
-                full(vk);
-                if (ok) clear_unseen(prev[st], vk % C::STAGES);
+          Stream &y = z[st];
+          const int t = C::SHARED ? t0 : st;
+          const uint32_t tS = tmem + t * kKeys, tO = tmem + 256 + t * 128;
+          const bool v = r.v(st), k = r.k(st);
+          const uint32_t v_at = r.v_at(st), k_at = r.k_at(st);
+          const bool o_first = y.first, o_last = y.last, do_o = v && y.mine;
+          if (v) {
+            ok = ok && mbar_spin(kv_full(v_at), kv_parity(v_at));
+            // rows next to the seen ones in their page may hold anything
+            const int head = C::QUANT || y.lo <= 0 ? 0 : y.lo & 15;
+            const int tail = C::QUANT || y.hi >= kKeys || y.hi <= 0 ? 0 : -y.hi & 15;
+            if (ok && head + tail > 0) {
+              if (t0 == 0) {
+                const uint32_t tile = sm + C::RING + (v_at % C::STAGES) * C::TILE;
+                for (int e = lane; e < (head + tail) * 8 * C::HALVES; e += 32) {
+                  const int n = e / (8 * C::HALVES), chunk = e % (8 * C::HALVES);
+                  const int row = n < head ? y.lo - head + n : y.hi + n - head;
+                  sts128(tile + (chunk >> 3) * (kKeys * 128) + row * 128 + (chunk & 7) * 16,
+                         make_uint4(0, 0, 0, 0));
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (C::SHARED && lane == 0) mbar_arrive(clean(cleared));
+              } else {
+                ok = mbar_wait(clean(cleared), (cleared / kClean) & 1);
               }
-              ok = ok && mbar_wait(p_ready(t), p_phase[t]);
-              p_phase[t] ^= 1;
-              if (ok) {
-                tc_fence_after();
-                mma_o(t, vk % C::STAGES, prev[st]);
-              }
-            }
-            if (v && i == (C::SHARED ? 1 : 0)) release(vk);
-            if (k && (i == 0 || cur[st].two)) {
-              if (i == 0) full(kk);
-              if (cur[st].first) {
-                ok = ok && mbar_wait(q_full(t), q_phase[t]);
-                q_phase[t] ^= 1;
-              }
-              if (ok) mma_s(t, kk % C::STAGES);
+              ++cleared;
             }
           }
-          if (k) release(kk);
-          prev[st] = cur[st];
-          if (k) cur[st] = fetch(st);
+          if (k) {
+            if (y.i == y.x.n) {
+              read_piece(st, y.piece++, y.x);
+              y.i = 0;
+            }
+            y.mine = !C::SHARED || t == 0 || y.x.ntok > p.tok;
+            y.first = y.i == 0;
+            y.last = y.i == y.x.n - 1;
+            y.lo = y.x.lo - (y.x.tile + y.i) * kKeys;
+            y.hi = y.x.L - (y.x.tile + y.i) * kKeys;
+            ++y.i;
+            ok = ok && mbar_spin(kv_full(k_at), kv_parity(k_at));
+            if (y.mine && y.first) {
+              ok = ok && mbar_spin(q_full(t), y.q_phase);
+              y.q_phase ^= 1;
+            }
+          }
+          const bool do_s = k && y.mine;
+          if (do_o) ok = ok && mbar_spin(p_early(t), y.p_phase);
+          if (C::SHARED) ok = ok && mbar_spin(turn(t0), turns++ & 1);
+          if (do_o) {                                    // O_t += P_t V
+            const uint64_t b = v_desc + (v_at % C::STAGES) * (C::TILE >> 4);
+            if (ok) {
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int e = 0; e < kEarly / 16; ++e)
+                  tc_mma_ts(tO, tS + e * 8, b + ((e * 16 * 128) >> 4), idO, !o_first || e > 0);
+              }
+              __syncwarp();
+              ok = mbar_spin(p_ready(t), y.p_phase);
+            }
+            y.p_phase ^= 1;
+            if (ok) {
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll
+                for (int e = kEarly / 16; e < kKeys / 16; ++e)
+                  tc_mma_ts(tO, tS + e * 8, b + ((e * 16 * 128) >> 4), idO, 1);
+                if (o_last) tc_commit(o_full(t));
+                tc_commit(kv_empty(v_at));
+              }
+              __syncwarp();
+            }
+          } else if (v && ok && lane == 0) {
+            mbar_arrive(kv_empty(v_at));
+          }
+          if (do_s) {                                    // S_t = Q_t K^T
+            if (ok && elect_one()) {
+              const uint64_t a = q_desc + t * (C::TILE >> 4);
+              const uint64_t b = k_desc + (k_at % C::STAGES) * (C::TILE >> 4);
+#pragma unroll
+              for (int e = 0; e < C::D / 16; ++e) {
+                if (C::SHARED && e == C::D / 32) mbar_arrive(turn(t0 ^ 1));
+                const uint32_t o = ((e >> 2) * (kKeys * 128) + (e & 3) * 32) >> 4;
+                tc_mma_ss(tS, a + o, b + o, idS, e > 0);
+              }
+              tc_commit(s_full(t));
+              tc_commit(kv_empty(k_at));
+            }
+            __syncwarp();
+          } else {
+            if (k && ok && lane == 0) mbar_arrive(kv_empty(k_at));
+            if (C::SHARED && ok && lane == 0) mbar_arrive(turn(t0 ^ 1));
+          }
         }
       }
-      // nothing of this CTA's products is in flight when its memory goes
-      if (lane == 0) tc_commit(done_bar);
+      // nothing of this warp's products is in flight when the CTA's memory goes
+      if (lane == 0) tc_commit(done_bar(t0));
       __syncwarp();
-      ok = mbar_wait(done_bar, 0) && ok;
+      ok = mbar_wait(done_bar(t0), 0) && ok;
     }
   }
   if (!ok && lane == 0) set_err(p.err, PA_DEVERR_TIMEOUT);
@@ -1253,11 +1474,13 @@ pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t 
   p.causal = causal;
   p.tok = plan.tok;
   p.workers = plan.workers;
+  p.over_workers = ~uint64_t(0) / plan.workers + 1;       // exact for totals below 2^55
   p.rows = plan.rows;
   // c > 0 keeps a masked score's c s at -inf; 1e-30 scores every key alike, as 0 does
   const float c = sm_scale * kLog2e;
   p.c = fmaxf(fabsf(c), 1e-30f);
   p.negate = c < 0.f;
+  p.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   CUtensorMap mq, mk, mv;
   if (!make_query_map(&mq, q, s, T, plan.tok) || !make_pool_map(&mk, k_pool, s, 1) ||
       !make_pool_map(&mv, v_pool, s, 1))
