@@ -461,8 +461,9 @@ typedef struct {
  *     a' = a c - b s,  b' = b c + a s,   c, s = cos_sin[positions[t]][j], [rotary_dim / 2 + j]
  * in fp32 (each product and sum rounded), rounded once to bf16; the other channels are copied.
  * q_out holds the rotated queries; the rotated keys and the values are written as by
- * pa_reshape_and_cache with k_new = the rotated keys (bf16, E4M3 and 4-bit pools: the same
- * bytes and scales).
+ * pa_reshape_and_cache with k_new = the rotated keys, except that a quantised block's scale is
+ * absmax times the fp32 reciprocal of the largest code (there: absmax divided by it; the two
+ * differ by one unit in the last place at most).
  *   cos_sin [num_positions, rotary_dim] fp32: cosines, then sines, of each position's angles
  *     (any frequencies and scaling the caller puts in);
  *   positions [B] int32; slot_mapping [B] int64;

@@ -453,11 +453,6 @@ __device__ __forceinline__ uint32_t int4_pair_bf16(uint32_t w, uint32_t w4, int 
   return bf16x2_sub((x & 0x000F000Fu) | 0x43004300u, 0x43084308u);
 }
 
-__device__ __forceinline__ float lds_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr));
-  return v;
-}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -472,24 +467,24 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
-// A tile's codes (as TMA swizzled them) to a bf16 tile (128-byte swizzle), by four warps.
+// A tile's codes (as TMA swizzled them) to a bf16 tile (128-byte swizzle), by kWarps warps.
 // Neighbouring lanes write both 64-column halves of a row at once; the order of a lane's stores
 // keeps the two halves off each other's banks.
-template <int KIND>
+template <int KIND, int kWarps>
 __device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, int lane) {
   if constexpr (KIND == PA_KV_FP8_E4M3) {
-    constexpr int kBatch = 8;
+    constexpr int kSteps = 32 / kWarps;                  // of four rows
     const int c = lane & 7;                              // 16 codes: columns [16 c, 16 c + 16)
-    for (int i0 = 0; i0 < 8; i0 += kBatch) {
-      uint4 v[kBatch];
+    {
+      uint4 v[kSteps];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = (i0 + i) * 16 + w * 4 + (lane >> 3);
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = (i * kWarps + w) * 4 + (lane >> 3);
         v[i] = lds128(raw + r * 128 + ((c ^ (r & 7)) << 4));
       }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int r = (i0 + i) * 16 + w * 4 + (lane >> 3);
+      for (int i = 0; i < kSteps; ++i) {
+        const int r = (i * kWarps + w) * 4 + (lane >> 3);
         const uint4 lo = make_uint4(e4m3_pair_bf16(v[i].x, 0), e4m3_pair_bf16(v[i].x, 1),
                                     e4m3_pair_bf16(v[i].y, 0), e4m3_pair_bf16(v[i].y, 1));
         const uint4 hi = make_uint4(e4m3_pair_bf16(v[i].z, 0), e4m3_pair_bf16(v[i].z, 1),
@@ -501,16 +496,17 @@ __device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, 
       }
     }
   } else {
+    constexpr int kSteps = 16 / kWarps;                  // of eight rows
     const int c = lane & 3;                              // 32 codes: columns [32 c, 32 c + 32)
-    uint4 v[4];
+    uint4 v[kSteps];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 32 + w * 8 + (lane >> 2);
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = (i * kWarps + w) * 8 + (lane >> 2);
       v[i] = lds128(raw + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 32 + w * 8 + (lane >> 2);
+    for (int i = 0; i < kSteps; ++i) {
+      const int r = (i * kWarps + w) * 8 + (lane >> 2);
       const uint32_t row = dst + (c >> 1) * (kKeys * 128) + r * 128;
       const bool swap = c >= 2;
       if (swap) v[i] = make_uint4(v[i].z, v[i].w, v[i].x, v[i].y);
@@ -569,11 +565,11 @@ struct AttendCfg {
   // pieces, the loads (bf16: two warps with half of every tile's copies each, since a copy is slow
   // to issue; code pools: one, and four warps that restore codes).  512 threads start with 128 registers, dealt anew
   // by groups of four warps as 256 x 184 + 256 x 72: a softmax thread holds its row's 128 scores.
-  static constexpr int THREADS = QUANT ? 512 : 384;
+  static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr int MMA_WARP = 8, PIECE_WARP = 10, LOAD_WARP = 11;
   static constexpr int LOADERS = 1;
-  static constexpr int CODE_WARP = 12;                  // the last four (code pools)
-  static constexpr int SOFTMAX_REGS = QUANT ? 152 : 216, OTHER_REGS = QUANT ? 104 : 72;
+  static constexpr int CODE_WARP = 12, CODE_WARPS = 8;  // code pools
+  static constexpr int SOFTMAX_REGS = QUANT ? 144 : 216, OTHER_REGS = QUANT ? 64 : 72;
   static constexpr int STREAMS = SHARED ? 1 : 2;        // key streams of a CTA
   static constexpr int PIECES = 8;                      // pieces known ahead per stream
   static constexpr int SCALES = 5;                      // tiles whose scales are held per stream
@@ -636,7 +632,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(kv_full(i), C::QUANT ? 4 : C::LOADERS);  // the warps that fill it
+      mbar_init(kv_full(i), C::QUANT ? C::CODE_WARPS : C::LOADERS);  // the warps that fill it
       mbar_init(kv_empty(i), C::SHARED ? 2 : 1);         // the product warps
     }
     for (int t = 0; t < 2; ++t) {
@@ -658,7 +654,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if constexpr (C::QUANT) {
       for (int i = 0; i < C::RAW; ++i) {
         mbar_init(raw_full(i), 1);
-        mbar_init(raw_empty(i), 4);
+        mbar_init(raw_empty(i), C::CODE_WARPS);
       }
       for (int st = 0; st < C::STREAMS; ++st)
         for (int n = 0; n < C::SCALES; ++n) mbar_init(sc_full(st, n), 1);
@@ -754,7 +750,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       float l = 0.f;
       for (int i = 0; i < x.n; ++i) {
         const int key0 = (x.tile + i) * kKeys;
-        ok = mbar_wait(s_full(t), s_phase);
+        // what each page's scores are multiplied by (above zero, so that -inf stays -inf), and its
+        // weights; code pools have a scale a page, read before the scores are there
+        float fk[8], fv[8];
+        if constexpr (C::QUANT) {
+          const uint32_t n = tile0 + i;
+          ok = mbar_wait(sc_full(st, n), sc_parity(n));
+          const float4 *sc = scales[st][n % C::SCALES];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            *reinterpret_cast<float4 *>(fk + 4 * e) = sc[e];
+            *reinterpret_cast<float4 *>(fv + 4 * e) = sc[2 + e];
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) fk[e] = fmaxf(fk[e] * p.c, 1e-30f);
+        }
+        ok = ok && mbar_wait(s_full(t), s_phase);
         if (!ok) break;
         s_phase ^= 1;
         if (i == x.n - 1 && row == 0) {
@@ -772,17 +783,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         tc_fence_after();
         if (warp_live) {
-          // code pools: the scales of the tile's pages, read where they are used
-          [[maybe_unused]] uint32_t sc = 0;
-          if constexpr (C::QUANT) {
-            const uint32_t n = tile0 + i;
-            ok = mbar_wait(sc_full(st, n), sc_parity(n));
-            sc = smem_u32(scales[st][n % C::SCALES]);
-          }
-          // what a page's scores are multiplied by; above zero, so that -inf stays -inf
-          auto k_factor = [&](int page) {
-            return C::QUANT ? fmaxf(lds_f32(sc + 4 * page) * p.c, 1e-30f) : p.c;
-          };
           const bool edge = key0 < all_lo || key0 + kKeys > all_hi;
           const int first = lo - key0;                   // columns [first, first + seen) count
           const unsigned seen = static_cast<unsigned>(max(0, hi - lo));
@@ -804,7 +804,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 y[1] = fmaxf(y[1], fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
               }
               const float page = fmaxf(y[0], y[1]);
-              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT ? page * k_factor((j0 + j) / 16) : page);
+              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT ? page * fk[(j0 + j) / 16] : page);
             }
           };
           // bf16 pools: the row's scores stay in registers; code pools, whose threads have fewer,
@@ -871,21 +871,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               if (j < 3) tc_ld32(s + 32 * (~j & 1), tS + 32 * (j + 1));
             }
             uint32_t packed[16];
-            float c1 = p.c, v1 = 1.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              if constexpr (C::QUANT) {
-                if (e % 8 == 0) {
-                  c1 = k_factor(2 * j + e / 8);
-                  v1 = lds_f32(sc + 32 + 4 * (2 * j + e / 8));
-                }
-              }
+              const float c1 = C::QUANT ? fk[2 * j + e / 8] : p.c;
               float2 y = fma2(make_float2(__uint_as_float(now[2 * e]), __uint_as_float(now[2 * e + 1])),
                               make_float2(c1, c1), n2);
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum[e & 1] = add2(sum[e & 1], y);
-              if constexpr (C::QUANT) y = mul2(y, make_float2(v1, v1));
+              if constexpr (C::QUANT) y = mul2(y, make_float2(fv[2 * j + e / 8], fv[2 * j + e / 8]));
               packed[e] = pack_bf16(y.x, y.y);
             }
             tc_st16(tS + 16 * j, packed);                // over columns already read
@@ -1194,7 +1188,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (uint32_t k = 0; ok && k < all; ++k) {
         ok = mbar_wait(raw_full(k), raw_parity(k)) && mbar_wait(kv_empty(k), kv_parity(k) ^ 1);
         if (!ok) break;
-        restore_tile<C::KIND>(sm + C::RAW_RING + (k % C::RAW) * C::RAW_TILE,
+        restore_tile<C::KIND, C::CODE_WARPS>(sm + C::RAW_RING + (k % C::RAW) * C::RAW_TILE,
                               sm + C::RING + (k % C::STAGES) * C::TILE, warp - C::CODE_WARP, lane);
         fence_proxy_async();
         __syncwarp();
@@ -1371,24 +1365,34 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p)
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
     float l = 0.f, o[E] = {};
-    for (int i = 0; i <= cut.w; ++i) {
-      const float2 ml = p.part_ml[slot(i)];
-      if (!(ml.y > 0.f)) continue;
-      const float f = ex2(ml.x - M);
-      l += f * ml.y;
-      const float *src = p.part_o + slot(i) * D + lane * E;
-      if constexpr (E == 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(src);
-        o[0] += f * v.x;
-        o[1] += f * v.y;
-        o[2] += f * v.z;
-        o[3] += f * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2 *>(src);
-        o[0] += f * v.x;
-        o[1] += f * v.y;
+    for (int i0 = 0; i0 <= cut.w; i0 += 32) {            // a piece per lane, then a lane's weight to all
+      float f = 0.f;
+      if (i0 + lane <= cut.w) {
+        const float2 ml = p.part_ml[slot(i0 + lane)];
+        if (ml.y > 0.f) f = ex2(ml.x - M);
+        l += f * ml.y;
+      }
+      const int n = min(32, cut.w + 1 - i0);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float g = __shfl_sync(0xffffffffu, f, i);
+        const float *src = p.part_o + slot(i0 + i) * D + lane * E;
+        // a piece without seen keys has all weights zero, and so is its O
+        if constexpr (E == 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(src);
+          o[0] += g * v.x;
+          o[1] += g * v.y;
+          o[2] += g * v.z;
+          o[3] += g * v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2 *>(src);
+          o[0] += g * v.x;
+          o[1] += g * v.y;
+        }
       }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     const float inv = l > 0.f ? 1.f / l : 0.f;
     uint16_t *dst = p.out + (static_cast<int64_t>(cut.x + tok) * p.Hq + cut.z * p.G +
                              (rr - in_tile * p.G)) * D + lane * E;
@@ -1434,7 +1438,7 @@ pa_status launch(const AttendParams &p, const CUtensorMap &mq, const CUtensorMap
   if (launch_pdl(kernel, dim3(p.workers / C::STREAMS), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p) !=
       cudaSuccess)
     return PA_ERR_CUDA;
-  const dim3 grid(p.workers, C::SHARED ? 8 : 4);
+  const dim3 grid(p.workers, (p.rows + 7) / 8);          // a warp per row
   return launch_pdl(attend_merge_kernel<C::D>, grid, dim3(256), 0, stream, p) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;

@@ -10,6 +10,7 @@ namespace pa {
 struct Fp8Codec {
   static constexpr int kRowBytes = 128;
   static constexpr float kMaxCode = 448.f;
+  static constexpr float kPerCode = 1.f / 448.f;
   using Word = uint32_t;
   static __device__ __forceinline__ Word encode(const float (&v)[4], float s) {
     if (s == 0.f) return 0u;
@@ -36,6 +37,7 @@ __device__ __forceinline__ uint32_t int4_code(float x, float scale) {
 struct Int4Codec {
   static constexpr int kRowBytes = 64;
   static constexpr float kMaxCode = 7.f;
+  static constexpr float kPerCode = 1.f / 7.f;
   using Word = uint16_t;
   static __device__ __forceinline__ Word encode(const float (&v)[4], float s) {
     uint32_t code = 0;

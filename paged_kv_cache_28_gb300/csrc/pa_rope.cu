@@ -6,10 +6,12 @@
 //     a' = a cos - b sin,   b' = b cos + a sin
 // in fp32 with each product and sum rounded (no fused multiply-add, so that the bits are those
 // of the written formula), rounded once to bf16.  The rotated keys and the values then go to
-// the cache exactly as pa_reshape_and_cache would write them.
+// the cache as pa_reshape_and_cache writes them.
 //
 // Nothing here is reused but the table row of a token, so the kernels are bound by HBM: each
 // vector is read once and written once.
+#include <algorithm>
+
 #include "pa_codec.cuh"
 #include "pa_common.cuh"
 #include "pa_internal.h"
@@ -36,20 +38,19 @@ __device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
                      __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
 }
 
-// Whether token t is written: a slot in the pool and a position in the table.
-__device__ __forceinline__ bool token_ok(const RopeParams &p, int t, int64_t slot, bool report) {
+// Whether a token is written: a slot in the pool and a position in the table.
+__device__ __forceinline__ bool token_ok(const RopeParams &p, int64_t slot, int pos, bool report) {
   if (slot < 0) return false;                            // padding
   int bits = 0;
   if (slot >= static_cast<int64_t>(p.nblocks) * p.bs) bits |= PA_DEVERR_SLOT;
-  const int pos = p.positions[t];
   if (pos < 0 || pos >= p.num_positions) bits |= PA_DEVERR_POSITION;
   if (bits && report) set_err(p.err, bits);
   return bits == 0;
 }
 
-// One thread's share of a head: 16 channels as two 16-byte chunks that hold eight whole pairs.
+// One thread's share of a head: 16 channels as two 16-byte chunks that hold eight whole pairs
+// (channels j and j + r / 2, or neighbours), and their angles.
 struct Item {
-  int c0, c1;            // first channels of the chunks
   bool rotates;
   float cos[8], sin[8];
 };
@@ -57,9 +58,6 @@ struct Item {
 template <bool kInterleaved>
 __device__ __forceinline__ void load_item(const RopeParams &p, int item, int pos, Item &x) {
   x.rotates = item < p.r / 16;
-  const bool split = x.rotates && !kInterleaved;         // pairs (j, j + r / 2)
-  x.c0 = split ? 8 * item : 16 * item;
-  x.c1 = split ? p.r / 2 + 8 * item : 16 * item + 8;
   if (!x.rotates) return;
   const float4 *row =
       reinterpret_cast<const float4 *>(p.cos_sin + static_cast<int64_t>(pos) * p.r + 8 * item);
@@ -92,13 +90,15 @@ __device__ __forceinline__ void rotate_item(const Item &x, uint4 &a, uint4 &b) {
 
 // Heads first, first + step, ... < last of token t, counted through the queries, then (bf16
 // pools) the keys and the values; this thread's item of each.  Four heads' loads are in flight
-// at once.
+// at once, the first four's before the token's slot, position and angles are there.
 template <int D, bool kInterleaved>
-__device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int64_t slot, const Item &x,
-                                           int first, int step, int last) {
+__device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int item, int first, int step,
+                                           int last, bool report) {
   constexpr int U = 4;
-  for (int h0 = first; h0 < last; h0 += step * U) {
-    uint4 a[U], b[U];
+  const bool split = !kInterleaved && item < p.r / 16;
+  const int c0 = split ? 8 * item : 16 * item, c1 = split ? p.r / 2 + 8 * item : 16 * item + 8;
+  uint4 a[U], b[U];
+  auto load = [&](int h0) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int h = h0 + i * step;
@@ -106,9 +106,18 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int64_t s
       const uint16_t *src = h < p.Hq ? p.q + t * p.q_stride + h * D
                             : h < p.Hq + p.Hkv ? p.k + t * p.k_stride + (h - p.Hq) * D
                                                : p.v + t * p.v_stride + (h - p.Hq - p.Hkv) * D;
-      a[i] = *reinterpret_cast<const uint4 *>(src + x.c0);
-      b[i] = *reinterpret_cast<const uint4 *>(src + x.c1);
+      a[i] = *reinterpret_cast<const uint4 *>(src + c0);
+      b[i] = *reinterpret_cast<const uint4 *>(src + c1);
     }
+  };
+  load(first);
+  const int64_t slot = p.slots[t];
+  const int pos = p.positions[t];
+  if (!token_ok(p, slot, pos, report)) return;
+  Item x;
+  load_item<kInterleaved>(p, item, pos, x);
+  for (int h0 = first; h0 < last; h0 += step * U) {
+    if (h0 > first) load(h0);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int h = h0 + i * step;
@@ -119,8 +128,8 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int64_t s
           : h < p.Hq + p.Hkv
               ? reinterpret_cast<uint16_t *>(p.k_pool) + (slot * p.Hkv + h - p.Hq) * D
               : reinterpret_cast<uint16_t *>(p.v_pool) + (slot * p.Hkv + h - p.Hq - p.Hkv) * D;
-      *reinterpret_cast<uint4 *>(dst + x.c0) = a[i];
-      *reinterpret_cast<uint4 *>(dst + x.c1) = b[i];
+      *reinterpret_cast<uint4 *>(dst + c0) = a[i];
+      *reinterpret_cast<uint4 *>(dst + c1) = b[i];
     }
   }
 }
@@ -131,173 +140,188 @@ __global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
   pdl_trigger();
   pdl_wait();
   constexpr int kItems = D / 16, kHeads = 128 / kItems;
-  const int t = blockIdx.x;
-  const int64_t slot = p.slots[t];
-  if (!token_ok(p, t, slot, threadIdx.x == 0 && blockIdx.y == 0)) return;
-  Item x;
-  load_item<kInterleaved>(p, threadIdx.x % kItems, p.positions[t], x);
-  rope_heads<D, kInterleaved>(p, t, slot, x, (p.q ? 0 : p.Hq) + blockIdx.y * kHeads + threadIdx.x / kItems,
-                              gridDim.y * kHeads, p.Hq + 2 * p.Hkv);
+  rope_heads<D, kInterleaved>(p, blockIdx.x, threadIdx.x % kItems,
+                              (p.q ? 0 : p.Hq) + blockIdx.y * kHeads + threadIdx.x / kItems,
+                              gridDim.y * kHeads, p.Hq + 2 * p.Hkv,
+                              threadIdx.x == 0 && blockIdx.y == 0);
 }
 
-// Quantised pools (D = 128).  CTAs [0, T) write the cache: as in pa_reshape_and_cache, the
-// first token of the call in a block (its leader) applies every token of the call in that
-// block, in token order; the others leave.  A warp takes (KV head, K or V) jobs, a lane four
-// consecutive channels.  The codes of a job's rows stay in shared memory while its tokens are
-// applied, so a token that raises the scale costs no trip to the pool, and each row is written
-// once.  CTAs [T, 2 T) rotate the queries.
+// Quantised pools (D = 128).  The first CTAs write the cache, kTokens tokens each; as in
+// pa_reshape_and_cache, the first token of the call in a block (its leader) stands for every
+// token of the call in that block, applied in token order.  A warp takes (KV head, K or V) jobs,
+// a lane four consecutive channels.  The codes of a job's rows stay in shared memory while its
+// tokens are applied, so a token that raises the scale costs no trip to the pool, and each row
+// is written once.  The other CTAs rotate the queries of a token each.
+//
+// The scale is absmax times the fp32 reciprocal of the largest code (pa_reshape_and_cache
+// divides: the two differ by one unit in the last place at most); codes are x / scale, rounded,
+// in both.
 template <class Codec, bool kInterleaved>
-__global__ void __launch_bounds__(256) rope_quant_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(256) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens) {
   using Word = typename Codec::Word;
   constexpr int D = 128, kWarps = 8, kBatch = 8;
+  extern __shared__ uint32_t smem[];                     // [kWarps][bs][32] words: a job's rows
   __shared__ int members[256];      // this chunk's tokens of the block, in token order
   __shared__ int member_off[256];
   __shared__ int warp_count[kWarps];
   __shared__ uint32_t offsets_seen;
-  __shared__ Word codes[kWarps][32][32];                 // a job's rows: one word per lane
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x >= p.T) {
-    const int t = blockIdx.x - p.T;
-    if (!token_ok(p, t, p.slots[t], false)) return;
-    Item x;
-    load_item<kInterleaved>(p, tid % 8, p.positions[t], x);
-    rope_heads<D, kInterleaved>(p, t, 0, x, tid / 8, 32, p.Hq);
+  if (blockIdx.x >= cache_ctas) {
+    rope_heads<D, kInterleaved>(p, blockIdx.x - cache_ctas, tid % 8, tid / 8, 32, p.Hq, false);
     return;
   }
-  const int t = blockIdx.x;
-  const int64_t slot = p.slots[t];
-  if (!token_ok(p, t, slot, tid == 0)) return;
-  const int64_t nslots = static_cast<int64_t>(p.nblocks) * p.bs;
-  const int64_t blk = slot / p.bs, blk0 = blk * p.bs;
-  auto in_block = [&](int u, int64_t o) {
-    return o >= blk0 && o < blk0 + p.bs && o < nslots && token_ok(p, u, o, false);
-  };
-  // A token right after another of its block (a prompt's tokens fill their blocks in order)
-  // leaves at once; the others look through the call: an earlier token of the block leads it,
-  // and without a later one past the first 256 tokens one look is enough.
-  if (t > 0 && in_block(t - 1, p.slots[t - 1])) return;
-  int earlier = 0, later = 0;
-#pragma unroll 4
-  for (int u = tid; u < t - 1; u += 256) earlier |= in_block(u, p.slots[u]);
-  if (__syncthreads_or(earlier)) return;
-#pragma unroll 4
-  for (int u = t + 256 + tid; u < p.T; u += 256) later |= in_block(u, p.slots[u]);
-  const int end = __syncthreads_or(later) ? p.T : min(p.T, t + 256);
-  if (tid == 0) offsets_seen = 0u;
-  for (int c0 = t; c0 < end; c0 += 256) {
-    // the chunk's tokens of this block, in token order (ballot compaction)
-    const int u = c0 + tid;
-    const int64_t o = u < p.T ? p.slots[u] : -1;
-    const bool mine = u < p.T && in_block(u, o);
-    const uint32_t ballot = __ballot_sync(0xffffffffu, mine);
-    if (lane == 0) warp_count[warp] = __popc(ballot);
-    __syncthreads();
-    int before = 0, n = 0;
-    for (int w = 0; w < kWarps; ++w) {
-      before += w < warp ? warp_count[w] : 0;
-      n += warp_count[w];
-    }
-    if (mine) {
-      const int i = before + __popc(ballot & ((1u << lane) - 1u));
-      const int off = static_cast<int>(o - blk0);
-      members[i] = u;
-      member_off[i] = off;
-      // a second token for one slot: applied after the first, and reported
-      if (atomicOr(&offsets_seen, 1u << off) & (1u << off)) set_err(p.err, PA_DEVERR_FP8_CONFLICT);
-    }
-    __syncthreads();
-    for (int job = warp; job < 2 * p.Hkv; job += kWarps) {
-      const int h = job >> 1;
-      const bool is_v = job & 1;
-      uint8_t *pool = is_v ? p.v_pool : p.k_pool;
-      float *scale = (is_v ? p.v_scale : p.k_scale) + blk * p.Hkv + h;
-      const uint16_t *src = (is_v ? p.v : p.k) + h * D + lane * 4;
-      const int64_t stride = is_v ? p.v_stride : p.k_stride;
-      auto word = [&](int r) {
-        return reinterpret_cast<Word *>(pool + ((blk0 + r) * p.Hkv + h) * int64_t(Codec::kRowBytes) +
-                                        lane * sizeof(Word));
-      };
-      float s = *scale;
-      uint32_t held = 0;                                 // rows whose codes are in shared memory
-      for (int i0 = 0; i0 < n; i0 += kBatch) {
-        uint2 raw[kBatch];
+  Word *codes = reinterpret_cast<Word *>(smem) + warp * p.bs * 32 + lane;    // row r: codes[32 r]
+  for (int t = blockIdx.x * tokens; t < min(p.T, (static_cast<int>(blockIdx.x) + 1) * tokens); ++t) {
+    const int64_t slot = p.slots[t];
+    if (!token_ok(p, slot, p.positions[t], tid == 0)) continue;
+    const int64_t blk = slot / p.bs, blk0 = blk * p.bs;
+    auto in_block = [&](int u, int64_t o) {
+      return o >= blk0 && o < blk0 + p.bs && token_ok(p, o, p.positions[u], false);
+    };
+    // A token right after another of its block (a prompt's tokens fill their blocks in order)
+    // leaves at once; the others look through the call: an earlier token of the block leads it,
+    // and without a later one past the first 256 tokens one look is enough.
+    if (t > 0 && in_block(t - 1, p.slots[t - 1])) continue;
+    int earlier = 0, later = 0;
+#pragma unroll 8
+    for (int u = tid; u < t - 1; u += 256) earlier |= in_block(u, p.slots[u]);
+#pragma unroll 8
+    for (int u = t + 256 + tid; u < p.T; u += 256) later |= in_block(u, p.slots[u]);
+    const int others = __syncthreads_or(earlier | later);
+    if (others && __syncthreads_or(earlier)) continue;
+    const int end = others ? p.T : min(p.T, t + 256);
+    if (tid == 0) offsets_seen = 0u;
+    for (int c0 = t; c0 < end; c0 += 256) {
+      // the chunk's tokens of this block, in token order (ballot compaction)
+      const int u = c0 + tid;
+      const int64_t o = u < p.T ? p.slots[u] : -1;
+      const bool mine = u < p.T && in_block(u, o);
+      const uint32_t ballot = __ballot_sync(0xffffffffu, mine);
+      if (lane == 0) warp_count[warp] = __popc(ballot);
+      __syncthreads();
+      int before = 0, n = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        before += w < warp ? warp_count[w] : 0;
+        n += warp_count[w];
+      }
+      if (mine) {
+        const int i = before + __popc(ballot & ((1u << lane) - 1u));
+        const int off = static_cast<int>(o - blk0);
+        members[i] = u;
+        member_off[i] = off;
+        // a second token for one slot: applied after the first, and reported
+        if (atomicOr(&offsets_seen, 1u << off) & (1u << off)) set_err(p.err, PA_DEVERR_FP8_CONFLICT);
+      }
+      __syncthreads();
+      for (int job = warp; job < 2 * p.Hkv; job += kWarps) {
+        const int h = job >> 1;
+        const bool is_v = job & 1;
+        uint8_t *pool = is_v ? p.v_pool : p.k_pool;
+        float *scale = (is_v ? p.v_scale : p.k_scale) + blk * p.Hkv + h;
+        const uint16_t *src = (is_v ? p.v : p.k) + h * D + lane * 4;
+        const int64_t stride = is_v ? p.v_stride : p.k_stride;
+        auto word = [&](int r) {
+          return reinterpret_cast<Word *>(pool + ((blk0 + r) * p.Hkv + h) * int64_t(Codec::kRowBytes) +
+                                          lane * sizeof(Word));
+        };
+        // the lane's own angles: its four channels' pairs lie r / 8 lanes away, or it has two pairs
+        const bool turns = !is_v && lane * 4 < p.r;
+        const bool upper = !kInterleaved && lane * 4 >= p.r / 2;
+        const int j = kInterleaved ? lane * 2 : lane * 4 - (upper ? p.r / 2 : 0);
+        const int peer = (upper ? lane - p.r / 8 : lane + p.r / 8) & 31;
+        float s = *scale;
+        uint32_t held = 0;                               // rows whose codes are in shared memory
+        for (int i0 = 0; i0 < n; i0 += kBatch) {
+          // a batch's vectors, rotated and rounded as the cache takes them, and their maxima
+          uint2 x[kBatch];
+          float amax[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if (i0 + i < n) raw[i] = *reinterpret_cast<const uint2 *>(src + members[i0 + i] * stride);
+          for (int i = 0; i < kBatch; ++i)
+            if (i0 + i < n) x[i] = *reinterpret_cast<const uint2 *>(src + members[i0 + i] * stride);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          if (i0 + i >= n) break;
-          const int off = member_off[i0 + i];
-          float v[4] = {bf16_lo(raw[i].x), bf16_hi(raw[i].x), bf16_lo(raw[i].y), bf16_hi(raw[i].y)};
-          if (!is_v) {
-            // the lane's own angles: four pairs half a rotation apart (the partner channels are
-            // r / 8 lanes away), or two neighbouring pairs
-            const bool turns = lane * 4 < p.r;
-            const bool upper = !kInterleaved && lane * 4 >= p.r / 2;
-            const float *row = p.cos_sin + static_cast<int64_t>(p.positions[members[i0 + i]]) * p.r;
-            if constexpr (kInterleaved) {
-              if (turns) {
-                const float2 c = __ldg(reinterpret_cast<const float2 *>(row) + lane);
-                const float2 sn = __ldg(reinterpret_cast<const float2 *>(row + p.r / 2) + lane);
-                const float2 y = turn(v[0], v[1], c.x, sn.x), z = turn(v[2], v[3], c.y, sn.y);
-                v[0] = y.x, v[1] = y.y, v[2] = z.x, v[3] = z.y;
-              }
-            } else {
-              const int peer = (upper ? lane - p.r / 8 : lane + p.r / 8) & 31;
-              float w[4];
+          for (int i = 0; i < kBatch; ++i) {
+            if (i0 + i >= n) break;
+            if (!is_v) {
+              const float v[4] = {bf16_lo(x[i].x), bf16_hi(x[i].x), bf16_lo(x[i].y), bf16_hi(x[i].y)};
+              const float *row = p.cos_sin + static_cast<int64_t>(p.positions[members[i0 + i]]) * p.r + j;
+              if constexpr (kInterleaved) {
+                if (turns) {
+                  const float2 c = __ldg(reinterpret_cast<const float2 *>(row));
+                  const float2 sn = __ldg(reinterpret_cast<const float2 *>(row + p.r / 2));
+                  const float2 y = turn(v[0], v[1], c.x, sn.x), z = turn(v[2], v[3], c.y, sn.y);
+                  x[i] = make_uint2(pack_bf16(y.x, y.y), pack_bf16(z.x, z.y));
+                }
+              } else {
+                const uint32_t w0 = __shfl_sync(0xffffffffu, x[i].x, peer);
+                const uint32_t w1 = __shfl_sync(0xffffffffu, x[i].y, peer);
+                const float w[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
+                if (turns) {
+                  const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
+                  const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
+                  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+                  float y[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w[e] = __shfl_sync(0xffffffffu, v[e], peer);
-              if (turns) {
-                const int j = lane * 4 - (upper ? p.r / 2 : 0);
-                const float4 c = __ldg(reinterpret_cast<const float4 *>(row + j));
-                const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2 + j));
-                const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  v[e] = upper ? turn(w[e], v[e], cc[e], ss[e]).y : turn(v[e], w[e], cc[e], ss[e]).x;
+                  for (int e = 0; e < 4; ++e)
+                    y[e] = upper ? turn(w[e], v[e], cc[e], ss[e]).y : turn(v[e], w[e], cc[e], ss[e]).x;
+                  x[i] = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
+                }
               }
             }
-            if (turns) {                                 // the cache takes the bf16 key
-              const uint32_t lo = pack_bf16(v[0], v[1]), hi = pack_bf16(v[2], v[3]);
-              v[0] = bf16_lo(lo), v[1] = bf16_hi(lo), v[2] = bf16_lo(hi), v[3] = bf16_hi(hi);
-            }
+            amax[i] = fmaxf(fmaxf(fabsf(bf16_lo(x[i].x)), fabsf(bf16_hi(x[i].x))),
+                            fmaxf(fabsf(bf16_lo(x[i].y)), fabsf(bf16_hi(x[i].y))));
           }
-          float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
 #pragma unroll
           for (int sh = 16; sh > 0; sh >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, sh));
-          const float cand = __fdiv_rn(amax, Codec::kMaxCode);
-          const float s_new = (off == 0 || cand > s) ? cand : s;
-          if (off > 0 && s_new > s) {
-            for (int r = 0; r < off; ++r) {
-              const Word c = held >> r & 1 ? codes[warp][r][lane] : *word(r);
-              codes[warp][r][lane] = Codec::reencode(c, s, s_new);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], sh));
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            if (i0 + i >= n) break;
+            const int off = member_off[i0 + i];
+            const float cand = __fmul_rn(amax[i], Codec::kPerCode);
+            const float s_new = (off == 0 || cand > s) ? cand : s;
+            if (off > 0 && s_new > s) {
+              for (int r = 0; r < off; ++r) {
+                const Word c = held >> r & 1 ? codes[32 * r] : *word(r);
+                codes[32 * r] = Codec::reencode(c, s, s_new);
+              }
+              held |= (1u << off) - 1u;
             }
-            held |= (1u << off) - 1u;
+            const float v[4] = {bf16_lo(x[i].x), bf16_hi(x[i].x), bf16_lo(x[i].y), bf16_hi(x[i].y)};
+            codes[32 * off] = Codec::encode(v, s_new);
+            held |= 1u << off;
+            s = s_new;
           }
-          codes[warp][off][lane] = Codec::encode(v, s_new);
-          held |= 1u << off;
-          s = s_new;
         }
+        for (int r = 0; r < p.bs; ++r)
+          if (held >> r & 1) *word(r) = codes[32 * r];
+        if (lane == 0) *scale = s;
       }
-      for (int r = 0; r < p.bs; ++r)
-        if (held >> r & 1) *word(r) = codes[warp][r][lane];
-      if (lane == 0) *scale = s;
+      __syncthreads();   // the member lists and the scales are reused by the next chunk
     }
-    __syncthreads();   // the member lists and the scales are reused by the next chunk
   }
 }
 
 template <int D, bool I>
 cudaError_t launch_bf16(const RopeParams &p, cudaStream_t stream) {
-  return launch_pdl(rope_bf16_kernel<D, I>, dim3(p.T), dim3(128), 0, stream, p);
+  // few tokens: their heads go over several CTAs, about two per SM
+  constexpr int kHeads = 128 / (D / 16);
+  const int heads = p.Hq + 2 * p.Hkv;
+  const int shares = std::max(1, std::min((heads + kHeads - 1) / kHeads, 304 / p.T));
+  return launch_pdl(rope_bf16_kernel<D, I>, dim3(p.T, shares), dim3(128), 0, stream, p);
 }
 
 template <class Codec, bool I>
 cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
-  return launch_pdl(rope_quant_kernel<Codec, I>, dim3(p.q ? 2 * p.T : p.T), dim3(256), 0, stream, p);
+  // a prompt's tokens mostly leave at once, so a CTA looks at several; a batch's stay
+  const int tokens = p.T >= 2048 ? 8 : 1;
+  const int cache_ctas = (p.T + tokens - 1) / tokens;
+  const size_t smem = 8 * 32 * sizeof(typename Codec::Word) * p.bs;
+  return launch_pdl(rope_quant_kernel<Codec, I>, dim3(cache_ctas + (p.q ? p.T : 0)), dim3(256), smem,
+                    stream, p, cache_ctas, tokens);
 }
 
 }  // namespace

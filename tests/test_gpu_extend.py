@@ -382,6 +382,35 @@ def rotated(x, cos_sin, pos, interleaved):
     return y
 
 
+def write_codes(x, pool, scale, slots, bs, kind):
+    """The quantised write in the order of the tokens, one after the other, in fp32."""
+    top = {"fp8": 448.0, "int4": 7.0}[kind]
+    per_code = torch.tensor(1.0 / top, dtype=torch.float32, device="cuda")
+    code = restore(pool, torch.ones_like(scale), kind).float()
+
+    def encode(v, s):
+        y = torch.where(s == 0, torch.zeros_like(v), v / torch.where(s == 0, torch.ones_like(s), s))
+        return y.clamp(-448, 448).to(torch.float8_e4m3fn).float() if kind == "fp8" else y.round().clamp(-7, 7)
+
+    for t, slot in enumerate(slots.tolist()):
+        if slot < 0:
+            continue
+        blk, off = divmod(slot, bs)
+        v, old = x[t].float(), scale[blk].clone()
+        cand = v.abs().amax(-1) * per_code
+        new = cand if off == 0 else torch.maximum(old, cand)
+        if off:
+            again = encode(code[blk, :off] * old[:, None], new[:, None])
+            code[blk, :off] = torch.where((new > old)[:, None], again, code[blk, :off])
+        code[blk, off] = encode(v, new[:, None])
+        scale[blk] = new
+    if kind == "fp8":
+        pool.copy_(code.to(torch.float8_e4m3fn).view(torch.uint8))
+    else:
+        u = (code + 8).to(torch.uint8)
+        pool.copy_(u[..., 0::2] | (u[..., 1::2] << 4))
+
+
 class Append:
     def __init__(self, T, Hq, Hkv, D=128, bs=16, kind="bf16", r=None, interleaved=False, fused=False, seed=0,
                  order="runs", nblocks=None):
@@ -429,14 +458,19 @@ class Append:
                              self.slots, self.err, interleaved=self.interleaved)
 
     def check(self, keep=None):
-        """Queries against 64 bits; keys and values: the bytes of the separate calls."""
+        """Queries against 64 bits; keys and values: the bytes of the plain formula (bf16 pools: of
+        pa_reshape_and_cache)."""
         keep = self.slots >= 0 if keep is None else keep
         pools = [x.clone() for x in self.pools]
         scales = [None if x is None else x.clone() for x in self.scales]
         self.run()
         k = rotated(self.k, self.cos_sin, self.pos.long().clamp(0, self.npos - 1), self.interleaved).bfloat16()
         slots = torch.where(keep, self.slots, -1)
-        pa.pa_reshape_and_cache(self.shape, k, self.v.contiguous(), *pools, *scales, slots, None)
+        if self.kind == "bf16":
+            pa.pa_reshape_and_cache(self.shape, k, self.v.contiguous(), *pools, None, None, slots, None)
+        else:
+            write_codes(k, pools[0], scales[0], slots, self.bs, self.kind)
+            write_codes(self.v, pools[1], scales[1], slots, self.bs, self.kind)
         torch.cuda.synchronize()
         for x, y in zip(self.pools + self.scales, pools + scales):
             assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
@@ -457,6 +491,18 @@ class Append:
                                                  (True, 16, False), (False, 112, False)])
 def test_rope_and_cache(kind, T, Hq, Hkv, bs, order, interleaved, r, fused):
     Append(T, Hq, Hkv, 128, bs, kind, r, interleaved, fused, seed=T + r, order=order).check()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+def test_scales_agree_with_reshape_and_cache(kind):
+    """The scales of the two writers are off by one unit in the last place at most."""
+    a = Append(300, 8, 4, kind=kind, seed=9)
+    k = rotated(a.k, a.cos_sin, a.pos.long(), False).bfloat16()
+    pools, scales = [x.clone() for x in a.pools], [x.clone() for x in a.scales]
+    a.run()
+    pa.pa_reshape_and_cache(a.shape, k, a.v, *pools, *scales, a.slots, None)
+    for x, y in zip(a.scales, scales):
+        assert ((x - y).abs() <= 2.0 ** -23 * y).all()
 
 
 @pytest.mark.parametrize("interleaved,r", [(False, 64), (True, 64), (False, 48), (True, 16)])
