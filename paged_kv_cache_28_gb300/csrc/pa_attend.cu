@@ -453,6 +453,11 @@ __device__ __forceinline__ uint32_t int4_pair_bf16(uint32_t w, uint32_t w4, int 
   return bf16x2_sub((x & 0x000F000Fu) | 0x43004300u, 0x43084308u);
 }
 
+__device__ __forceinline__ float2 lds_f32x2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -750,20 +755,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       float l = 0.f;
       for (int i = 0; i < x.n; ++i) {
         const int key0 = (x.tile + i) * kKeys;
-        // what each page's scores are multiplied by (above zero, so that -inf stays -inf), and its
-        // weights; code pools have a scale a page, read before the scores are there
-        float fk[8], fv[8];
+        // code pools: the scales of the tile's pages, K's then V's
+        [[maybe_unused]] uint32_t sc = 0;
         if constexpr (C::QUANT) {
           const uint32_t n = tile0 + i;
           ok = mbar_wait(sc_full(st, n), sc_parity(n));
-          const float4 *sc = scales[st][n % C::SCALES];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            *reinterpret_cast<float4 *>(fk + 4 * e) = sc[e];
-            *reinterpret_cast<float4 *>(fv + 4 * e) = sc[2 + e];
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) fk[e] = fmaxf(fk[e] * p.c, 1e-30f);
+          sc = smem_u32(scales[st][n % C::SCALES]);
         }
         ok = ok && mbar_wait(s_full(t), s_phase);
         if (!ok) break;
@@ -793,8 +790,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (static_cast<unsigned>(j0 + j - first) >= seen) s[j] = __float_as_uint(-INFINITY);
             }
           };
+          // what the scores of a block's two pages are multiplied by: above zero, so that -inf stays
+          auto k_factors = [&](int block) {
+            if constexpr (!C::QUANT) return make_float2(p.c, p.c);
+            const float2 f = lds_f32x2(sc + 8 * block);
+            return make_float2(fmaxf(f.x * p.c, 1e-30f), fmaxf(f.y * p.c, 1e-30f));
+          };
           float mx[2] = {-INFINITY, -INFINITY};
-          auto maximum = [&](const uint32_t *s, int j0) {
+          auto maximum = [&](const uint32_t *s, float2 f) {   // of a block of 32 columns
 #pragma unroll
             for (int j = 0; j < 32; j += 16) {
               float y[2] = {-INFINITY, -INFINITY};
@@ -804,21 +807,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 y[1] = fmaxf(y[1], fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
               }
               const float page = fmaxf(y[0], y[1]);
-              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT ? page * fk[(j0 + j) / 16] : page);
+              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT ? page * (j ? f.y : f.x) : page);
             }
           };
-          // bf16 pools: the row's scores stay in registers; code pools, whose threads have fewer,
-          // read them twice.  A block of 32 columns is on its way while another is worked on.
+          // A block of 32 columns is on its way while another is worked on.  bf16 pools: the row's
+          // scores stay in registers; code pools read them twice, in loops: with their restoring
+          // warps' code beside it, the unrolled form waits for instructions half of its time.
           uint32_t s[C::QUANT ? 64 : kKeys];
           if constexpr (C::QUANT) {
             tc_ld32(s + 32, tS + 96);
-#pragma unroll
-            for (int j = 3; j >= 0; --j) {
-              uint32_t *now = s + 32 * (j & 1);
-              tc_wait_ld32(now);
-              if (j > 0) tc_ld32(s + 32 * (~j & 1), tS + 32 * (j - 1));
-              hide(now, 32 * j);
-              maximum(now, 32 * j);
+#pragma unroll 1
+            for (int j = 2; j >= 0; j -= 2) {            // blocks j + 1 and j
+              const float2 f1 = k_factors(j + 1), f0 = k_factors(j);
+              tc_wait_ld32(s + 32);
+              tc_ld32(s, tS + 32 * j);
+              hide(s + 32, 32 * j + 32);
+              maximum(s + 32, f1);
+              tc_wait_ld32(s);
+              if (j > 0) tc_ld32(s + 32, tS + 32);
+              hide(s, 32 * j);
+              maximum(s, f0);
             }
           } else {
             tc_ld32(s, tS);
@@ -834,7 +842,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
               for (int j = 64 * half; j < 64 * half + 64; j += 32) {
                 hide(s + j, j);
-                maximum(s + j, j);
+                maximum(s + j, make_float2(1.f, 1.f));
               }
             }
           }
@@ -860,35 +868,48 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const float neg = m == -INFINITY ? 0.f : -m;
           const float2 n2 = make_float2(neg, neg);
           float2 sum[2] = {};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {                  // 32 columns at a time; block 0 is here
-            uint32_t *now = C::QUANT ? s + 32 * (j & 1) : s + 32 * j;
-            if constexpr (C::QUANT) {
-              if (j > 0) {
-                tc_wait_ld32(now);
-                hide(now, 32 * j);
-              }
-              if (j < 3) tc_ld32(s + 32 * (~j & 1), tS + 32 * (j + 1));
-            }
+          // the weights of block j, over columns that are already read
+          auto weights = [&](const uint32_t *s, int j, float2 f) {
+            float2 v = make_float2(1.f, 1.f);
+            if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
             uint32_t packed[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float c1 = C::QUANT ? fk[2 * j + e / 8] : p.c;
-              float2 y = fma2(make_float2(__uint_as_float(now[2 * e]), __uint_as_float(now[2 * e + 1])),
+              const float c1 = e < 8 ? f.x : f.y, v1 = e < 8 ? v.x : v.y;
+              float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
                               make_float2(c1, c1), n2);
               y.x = ex2(y.x);
               y.y = ex2(y.y);
               sum[e & 1] = add2(sum[e & 1], y);
-              if constexpr (C::QUANT) y = mul2(y, make_float2(fv[2 * j + e / 8], fv[2 * j + e / 8]));
+              if constexpr (C::QUANT) y = mul2(y, make_float2(v1, v1));
               packed[e] = pack_bf16(y.x, y.y);
             }
-            tc_st16(tS + 16 * j, packed);                // over columns already read
+            tc_st16(tS + 16 * j, packed);
             if (j == kEarly / 32 - 1) {
               tc_wait_st();
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(p_early(t));    // the second product may begin
             }
+          };
+          if constexpr (C::QUANT) {
+#pragma unroll 1
+            for (int j = 0; j < 4; j += 2) {             // blocks j (here, or on its way) and j + 1
+              const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
+              if (j > 0) {
+                tc_wait_ld32(s);
+                hide(s, 32 * j);
+              }
+              tc_ld32(s + 32, tS + 32 * j + 32);
+              weights(s, j, f0);
+              tc_wait_ld32(s + 32);
+              if (j == 0) tc_ld32(s, tS + 64);
+              hide(s + 32, 32 * j + 32);
+              weights(s + 32, j + 1, f1);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) weights(s + 32 * j, j, make_float2(p.c, p.c));
           }
           tc_wait_st();
           tc_fence_before();
@@ -1438,6 +1459,8 @@ pa_status launch(const AttendParams &p, const CUtensorMap &mq, const CUtensorMap
   if (launch_pdl(kernel, dim3(p.workers / C::STREAMS), dim3(C::THREADS), C::SMEM, stream, mq, mk, mv, p) !=
       cudaSuccess)
     return PA_ERR_CUDA;
+  // a sequence of one tile has units of one tile, which no segment bound cuts
+  if (static_cast<int64_t>(p.max_blocks) * p.bs <= kKeys) return PA_OK;
   const dim3 grid(p.workers, (p.rows + 7) / 8);          // a warp per row
   return launch_pdl(attend_merge_kernel<C::D>, grid, dim3(256), 0, stream, p) == cudaSuccess
              ? PA_OK

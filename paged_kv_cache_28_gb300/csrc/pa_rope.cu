@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
                               threadIdx.x == 0 && blockIdx.y == 0);
 }
 
-// Quantised pools (D = 128).  The first CTAs write the cache, kTokens tokens each; as in
+// Quantised pools (D = 128).  `cache_ctas` CTAs write the cache, `tokens` tokens each; as in
 // pa_reshape_and_cache, the first token of the call in a block (its leader) stands for every
 // token of the call in that block, applied in token order.  A warp takes (KV head, K or V) jobs,
 // a lane four consecutive channels.  The codes of a job's rows stay in shared memory while its
@@ -157,26 +157,30 @@ __global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
 // divides: the two differ by one unit in the last place at most); codes are x / scale, rounded,
 // in both.
 template <class Codec, bool kInterleaved>
-__global__ void __launch_bounds__(256) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens) {
+__global__ void __launch_bounds__(256, 4) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens) {
   using Word = typename Codec::Word;
   constexpr int D = 128, kWarps = 8, kBatch = 8;
   extern __shared__ uint32_t smem[];                     // [kWarps][bs][32] words: a job's rows
   __shared__ int members[256];      // this chunk's tokens of the block, in token order
   __shared__ int member_off[256];
   __shared__ int warp_count[kWarps];
+  __shared__ uint2 vectors[kWarps][kBatch][32];
   __shared__ uint32_t offsets_seen;
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (blockIdx.x >= cache_ctas) {
-    rope_heads<D, kInterleaved>(p, blockIdx.x - cache_ctas, tid % 8, tid / 8, 32, p.Hq, false);
+  // the two kinds of CTA alternate, so that the writers' arithmetic runs beside the queries' traffic
+  const int period = gridDim.x / cache_ctas, nth = blockIdx.x / period;
+  if (blockIdx.x % period != 0 || nth >= cache_ctas) {
+    const int t = blockIdx.x - min(nth + 1, cache_ctas);
+    rope_heads<D, kInterleaved>(p, t, tid % 8, tid / 8, 32, p.Hq, false);
     return;
   }
   Word *codes = reinterpret_cast<Word *>(smem) + warp * p.bs * 32 + lane;    // row r: codes[32 r]
-  for (int t = blockIdx.x * tokens; t < min(p.T, (static_cast<int>(blockIdx.x) + 1) * tokens); ++t) {
+  for (int t = nth * tokens; t < min(p.T, (nth + 1) * tokens); ++t) {
     const int64_t slot = p.slots[t];
     if (!token_ok(p, slot, p.positions[t], tid == 0)) continue;
-    const int64_t blk = slot / p.bs, blk0 = blk * p.bs;
+    const int64_t blk = slot >> (p.bs == 16 ? 4 : 5), blk0 = blk * p.bs;
     auto in_block = [&](int u, int64_t o) {
       return o >= blk0 && o < blk0 + p.bs && token_ok(p, o, p.positions[u], false);
     };
@@ -222,16 +226,16 @@ __global__ void __launch_bounds__(256) rope_quant_kernel(const RopeParams p, int
         float *scale = (is_v ? p.v_scale : p.k_scale) + blk * p.Hkv + h;
         const uint16_t *src = (is_v ? p.v : p.k) + h * D + lane * 4;
         const int64_t stride = is_v ? p.v_stride : p.k_stride;
-        auto word = [&](int r) {
-          return reinterpret_cast<Word *>(pool + ((blk0 + r) * p.Hkv + h) * int64_t(Codec::kRowBytes) +
-                                          lane * sizeof(Word));
-        };
+        Word *const rows = reinterpret_cast<Word *>(
+            pool + (blk0 * p.Hkv + h) * int64_t(Codec::kRowBytes) + lane * sizeof(Word));
+        const int pitch = p.Hkv * (Codec::kRowBytes / int(sizeof(Word)));     // words to the next row
         // the lane's own angles: its four channels' pairs lie r / 8 lanes away, or it has two pairs
         const bool turns = !is_v && lane * 4 < p.r;
         const bool upper = !kInterleaved && lane * 4 >= p.r / 2;
         const int j = kInterleaved ? lane * 2 : lane * 4 - (upper ? p.r / 2 : 0);
         const int peer = (upper ? lane - p.r / 8 : lane + p.r / 8) & 31;
         float s = *scale;
+        ByReciprocal over(1.f);
         uint32_t held = 0;                               // rows whose codes are in shared memory
         for (int i0 = 0; i0 < n; i0 += kBatch) {
           // a batch's vectors, rotated and rounded as the cache takes them, and their maxima
@@ -261,10 +265,10 @@ __global__ void __launch_bounds__(256) rope_quant_kernel(const RopeParams p, int
                   const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
                   const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
                   const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
-                  float y[4];
+                  float y[4];                            // a cos - b sin, or b cos + a sin
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
-                    y[e] = upper ? turn(w[e], v[e], cc[e], ss[e]).y : turn(v[e], w[e], cc[e], ss[e]).x;
+                    y[e] = __fadd_rn(__fmul_rn(v[e], cc[e]), __fmul_rn(w[e], upper ? ss[e] : -ss[e]));
                   x[i] = make_uint2(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]));
                 }
               }
@@ -277,27 +281,47 @@ __global__ void __launch_bounds__(256) rope_quant_kernel(const RopeParams p, int
 #pragma unroll
             for (int i = 0; i < kBatch; ++i)
               amax[i] = fmaxf(amax[i], __shfl_xor_sync(0xffffffffu, amax[i], sh));
+          // lane i: the scale that the batch's token i asks for.  The vectors wait in shared memory,
+          // so that the tokens can be taken in a loop: unrolled, this part overflows the
+          // instruction cache (it did: 155 us against 87 for 9,485 tokens).
+          float want = 0.f;
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            if (i0 + i >= n) break;
+            if (lane == i) want = __fmul_rn(amax[i], Codec::kPerCode);
+            if (i0 + i < n) vectors[warp][i][lane] = x[i];
+          }
+#pragma unroll 1
+          for (int i = 0; i < kBatch && i0 + i < n; ++i) {
             const int off = member_off[i0 + i];
-            const float cand = __fmul_rn(amax[i], Codec::kPerCode);
+            const float cand = __shfl_sync(0xffffffffu, want, i);
             const float s_new = (off == 0 || cand > s) ? cand : s;
+            if (s_new != s || i0 + i == 0) over = ByReciprocal(s_new);
+            const bool fits = over.fits();
             if (off > 0 && s_new > s) {
-              for (int r = 0; r < off; ++r) {
-                const Word c = held >> r & 1 ? codes[32 * r] : *word(r);
-                codes[32 * r] = Codec::reencode(c, s, s_new);
+              const uint32_t below = (1u << off) - 1u;
+              if ((held & below) != below)
+                for (int r = 0; r < off; ++r)
+                  if (!(held >> r & 1)) codes[32 * r] = rows[r * pitch];
+              held |= below;
+              if (fits) {
+#pragma unroll 2
+                for (int r = 0; r < off; ++r) codes[32 * r] = Codec::reencode_over(codes[32 * r], s, over);
+              } else {
+#pragma unroll 1
+                for (int r = 0; r < off; ++r) codes[32 * r] = Codec::reencode(codes[32 * r], s, s_new);
               }
-              held |= (1u << off) - 1u;
             }
-            const float v[4] = {bf16_lo(x[i].x), bf16_hi(x[i].x), bf16_lo(x[i].y), bf16_hi(x[i].y)};
-            codes[32 * off] = Codec::encode(v, s_new);
+            const uint2 y = vectors[warp][i][lane];
+            const float v[4] = {bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y)};
+            codes[32 * off] = fits ? Codec::encode_over(v, over) : Codec::encode(v, s_new);
             held |= 1u << off;
             s = s_new;
           }
         }
-        for (int r = 0; r < p.bs; ++r)
-          if (held >> r & 1) *word(r) = codes[32 * r];
+        for (uint32_t left = held; left; left &= left - 1) {
+          const int r = __ffs(left) - 1;
+          rows[r * pitch] = codes[32 * r];
+        }
         if (lane == 0) *scale = s;
       }
       __syncthreads();   // the member lists and the scales are reused by the next chunk
@@ -320,6 +344,9 @@ cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
   const int tokens = p.T >= 2048 ? 8 : 1;
   const int cache_ctas = (p.T + tokens - 1) / tokens;
   const size_t smem = 8 * 32 * sizeof(typename Codec::Word) * p.bs;
+  const cudaError_t e = cudaFuncSetAttribute(rope_quant_kernel<Codec, I>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * 1024);
+  if (e != cudaSuccess) return e;
   return launch_pdl(rope_quant_kernel<Codec, I>, dim3(cache_ctas + (p.q ? p.T : 0)), dim3(256), smem,
                     stream, p, cache_ctas, tokens);
 }

@@ -505,6 +505,24 @@ def test_scales_agree_with_reshape_and_cache(kind):
         assert ((x - y).abs() <= 2.0 ** -23 * y).all()
 
 
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+@pytest.mark.parametrize("spread", [3, 40, 100])
+def test_rope_codes_of_far_apart_values(kind, spread):
+    """Codes are correctly rounded quotients whatever the scale: values over 2^-spread .. 2^spread, a
+    block of zeros, and scales near the ends of the range."""
+    a = Append(400, 4, 4, kind=kind, seed=40 + spread, order="shuffled")
+    g = torch.Generator(device="cuda").manual_seed(spread)
+    for x in (a.k, a.v):
+        x.copy_((x.float() * 2.0 ** torch.randint(-spread, spread + 1, (400, 4, 1), generator=g, device="cuda")).bfloat16())
+        x[:, 1] *= 2.0 ** -spread
+        x[:, 2] = 0
+    for s in a.scales:
+        s.zero_()
+    for x in a.pools:
+        x.fill_(0x38 if kind == "fp8" else 0x88)
+    a.check()
+
+
 @pytest.mark.parametrize("interleaved,r", [(False, 64), (True, 64), (False, 48), (True, 16)])
 def test_rope_and_cache_small_heads(interleaved, r):
     Append(77, 9, 3, 64, 16, "bf16", r, interleaved, True, seed=r).check()
