@@ -33,7 +33,7 @@ namespace {
 
 constexpr int kKeys = 128;              // keys per tile
 constexpr int kRows = 128;              // rows per tile
-constexpr int kEarly = 96;              // keys whose weights are announced ahead of the rest
+constexpr int kEarly = 64;              // keys whose weights are announced ahead of the rest
 constexpr float kMaxJump = 8.f;         // the reference maximum moves only past this many octaves
 
 struct AttendParams {
@@ -45,6 +45,7 @@ struct AttendParams {
   float2 *part_ml;                      // [2 workers][rows]: (reference maximum times c, l)
   int4 *cut;                            // [workers]: the unit a worker leaves unfinished
   int B, Hq, Hkv, G, T, bs, max_blocks, nblocks, window, causal, tok, workers, rows;
+  int unit_cost;                        // what a unit costs besides its tiles, in tiles
   uint64_t over_workers;                // 2^64 / workers, rounded up
   float c;                              // |sm_scale| log2(e)
   uint32_t negate;                      // sm_scale < 0: the products take -Q
@@ -83,7 +84,9 @@ __device__ __forceinline__ Seq load_seq(const AttendParams &p, int b, int32_t *e
   return s;
 }
 
-// Key tiles of unit u (tokens [u S, (u + 1) S) of the sequence): first tile and count.
+// Key tiles of unit u (tokens [u S, (u + 1) S) of the sequence): first tile and count.  In the
+// stream that is cut into segments a unit is `unit_cost` tiles longer: its start and end take about
+// as long as that, and so batches of short and long units balance.
 __device__ __forceinline__ void unit_tiles(const AttendParams &p, const Seq &s, int u, int S,
                                            int &t0, int &count) {
   int hi = s.L, lo = 0;
@@ -105,15 +108,16 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int a, int64_t b) {
   return (a * (n * (n - 1) / 2) + n * b - rest) >> 7;
 }
 
-// Key tiles of the first u units of one KV head of a sequence.
+// Length of the first u units of one KV head of a sequence in the stream.
 __device__ int64_t tiles_before(const AttendParams &p, const Seq &s, int u, int S) {
   if (u == 0) return 0;
   int t0, count;
   if (!p.causal || s.L == 0) {
     unit_tiles(p, s, 0, S, t0, count);
-    return static_cast<int64_t>(u) * count;
+    return static_cast<int64_t>(u) * (count + p.unit_cost);
   }
-  int64_t sum = floor_sum(u, S, static_cast<int64_t>(s.base) + S + kKeys - 1);
+  int64_t sum = floor_sum(u, S, static_cast<int64_t>(s.base) + S + kKeys - 1) +
+                static_cast<int64_t>(u) * p.unit_cost;
   const int64_t end = s.base + static_cast<int64_t>(u) * S;
   if (end > s.L) sum += (s.L + kKeys - 1) / kKeys - (end + kKeys - 1) / kKeys;   // a short last unit
   if (p.window > 0) {
@@ -145,25 +149,36 @@ struct Piece {
   int starts, ends;            // holds the unit's first / last key tile
 };
 
-// The tiles of the sequences before each point of the batch, as one warp sees them: lane i
-// holds sequence i of a group of 32.
+// The stream over a group of 32 sequences, as one warp sees it: lane i holds sequence i.
 struct Group {
-  int g;                       // -1: none
   Seq s;
-  int64_t per_head, upto;      // tiles of one KV head; of the group through this sequence
+  int units;                   // units up to and with this sequence
+  int64_t per_head, upto;      // length of one KV head; of the group up to and with this sequence
 
   __device__ __forceinline__ void load(const AttendParams &p, int group, int S, int lane,
                                        int32_t *err) {
-    g = group;
     const int b = group * 32 + lane;
     s = Seq{};
     per_head = 0;
+    int U = 0;
     if (b < p.B) {
       s = load_seq(p, b, err);
-      per_head = tiles_before(p, s, (s.n + S - 1) / S, S);
+      U = (s.n + S - 1) / S;
+      per_head = tiles_before(p, s, U, S);
     }
     upto = scan64(p.Hkv * per_head, lane);
+    units = U * p.Hkv;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, units, d);
+      if (lane >= d) units += o;
+    }
   }
+};
+
+struct GroupSum {
+  int64_t upto;
+  int64_t units;
 };
 
 // The pieces of one worker, in order.
@@ -172,30 +187,36 @@ struct Walker {
   int remaining;
   Seq s;
 
-  // tiles [start, end) of the stream; sums: tiles of each group of 32 sequences (more than 32)
-  __device__ __forceinline__ void init(const AttendParams &p, Group &group, const int64_t *sums,
-                                       int64_t start, int64_t end, int S, int lane) {
-    remaining = static_cast<int>(end - start);
+  // Stand at place `start` of the stream; returns the key tiles before it.  sums: of each group of
+  // 32 sequences (where there are more than 32), total: of the batch.
+  __device__ __forceinline__ int64_t place(const AttendParams &p, const GroupSum *sums,
+                                           const GroupSum &total, Group &group, int64_t start, int S,
+                                           int lane) {
     b = h = u = off = U = 0;
     s = Seq{};
-    if (remaining <= 0) return;
-    int64_t before = 0;
+    if (start >= total.upto) return total.upto - p.unit_cost * total.units;
+    int64_t before = 0, units = 0;
+    int g = 0;
     if (p.B > 32) {
       const int groups = (p.B + 31) / 32;
-      int g = 0;
       for (int g0 = 0; g0 < groups; g0 += 32) {
-        const int64_t v = scan64(g0 + lane < groups ? sums[g0 + lane] : 0, lane);
+        const bool real = g0 + lane < groups;
+        const int64_t v = scan64(real ? sums[g0 + lane].upto : 0, lane);
+        const int64_t n = scan64(real ? sums[g0 + lane].units : 0, lane);
         const uint32_t past = __ballot_sync(0xffffffffu, before + v > start);
         const int first = past ? __ffs(past) - 1 : 32;
-        if (first > 0) before += shfl64(v, first - 1);
+        if (first > 0) {
+          before += shfl64(v, first - 1);
+          units += shfl64(n, first - 1);
+        }
         g = g0 + first;
         if (past) break;
       }
-      if (g != group.g) group.load(p, g, S, lane, nullptr);
+      group.load(p, g, S, lane, nullptr);
     }
     const uint32_t past = __ballot_sync(0xffffffffu, before + group.upto > start);
     const int l = past ? __ffs(past) - 1 : 31;
-    b = group.g * 32 + l;
+    b = g * 32 + l;
     s.q0 = __shfl_sync(0xffffffffu, group.s.q0, l);
     s.n = __shfl_sync(0xffffffffu, group.s.n, l);
     s.L = __shfl_sync(0xffffffffu, group.s.L, l);
@@ -204,6 +225,7 @@ struct Walker {
     const int64_t per_head = shfl64(group.per_head, l);
     int64_t r = start - before - (shfl64(group.upto, l) - p.Hkv * per_head);
     U = (s.n + S - 1) / S;
+    units += __shfl_sync(0xffffffffu, group.units, l) - p.Hkv * U;
     // the head: at most 2048, so a quotient in fp32 is off by one at most
     h = static_cast<int>(__fdividef(static_cast<float>(r), static_cast<float>(per_head)));
     h = min(h, p.Hkv - 1);
@@ -223,18 +245,27 @@ struct Walker {
     }
     u = lo;
     off = static_cast<int>(r - at_lo);
+    units += h * U + u;
+    int t0, count;
+    unit_tiles(p, s, u, S, t0, count);
+    return start - off - p.unit_cost * units + min(off, count);
   }
 
   // rest: tiles of the unit after this piece
   __device__ __forceinline__ bool next(const AttendParams &p, int S, Piece &x, int &rest) {
     x.n = 0;
-    if (remaining == 0) return false;
-    while (U == 0) {                          // sequences without query tokens
-      s = load_seq(p, ++b, nullptr);
-      U = (s.n + S - 1) / S;
-    }
     int t0, count;
-    unit_tiles(p, s, u, S, t0, count);
+    while (true) {
+      if (remaining <= 0) return false;
+      while (U == 0) {                        // sequences without query tokens
+        s = load_seq(p, ++b, nullptr);
+        U = (s.n + S - 1) / S;
+      }
+      unit_tiles(p, s, u, S, t0, count);
+      if (off < count) break;
+      remaining -= count + p.unit_cost - off;   // the segment begins behind the unit's last tile
+      next_unit(p);
+    }
     x.seq = b;
     x.h = h;
     x.row = s.q0 + u * S;
@@ -246,20 +277,22 @@ struct Walker {
     x.lo = s.lo;
     x.starts = off == 0;
     off += x.n;
-    remaining -= x.n;
     rest = count - off;
     x.ends = rest == 0;
-    if (x.ends) {
-      off = 0;
-      if (++u == U) {
-        u = 0;
-        if (++h == p.Hkv) {
-          h = 0;
-          U = 0;                              // the next sequence is read when it is wanted
-        }
+    remaining -= x.n + (x.ends ? p.unit_cost : 0);
+    if (x.ends) next_unit(p);
+    return true;
+  }
+
+  __device__ __forceinline__ void next_unit(const AttendParams &p) {
+    off = 0;
+    if (++u == U) {
+      u = 0;
+      if (++h == p.Hkv) {
+        h = 0;
+        U = 0;                                // the next sequence is read when it is wanted
       }
     }
-    return true;
   }
 };
 
@@ -576,7 +609,7 @@ struct AttendCfg {
   static constexpr int CODE_WARP = 12, CODE_WARPS = 8;  // code pools
   static constexpr int SOFTMAX_REGS = QUANT ? 144 : 216, OTHER_REGS = QUANT ? 64 : 72;
   static constexpr int STREAMS = SHARED ? 1 : 2;        // key streams of a CTA
-  static constexpr int PIECES = 8;                      // pieces known ahead per stream
+  static constexpr int PIECES = 6;                      // pieces known ahead per stream
   static constexpr int SCALES = 5;                      // tiles whose scales are held per stream
   // the scales of tile j + SCALES are stored before its K is issued; by then the copies have
   // come 2 (SCALES - 1) past V of tile j, which must be further than both rings hold
@@ -588,12 +621,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     attend_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const AttendParams p) {
   extern __shared__ uint8_t smem_raw[];
-  constexpr int kTileBars = 2 * C::STAGES, kClean = 8, kPieceBars = kTileBars + 15 + kClean;
+  constexpr int kTileBars = 2 * C::STAGES, kClean = 8, kPieceBars = kTileBars + 14 + kClean;
   constexpr int kRawBars = kPieceBars + 2 * C::STREAMS * C::PIECES;
   constexpr int kBars = kRawBars + (C::QUANT ? 2 * C::RAW + C::STREAMS * C::SCALES : 0);
   __shared__ __align__(8) uint64_t bars[kBars];
   __shared__ Piece pieces[C::STREAMS][C::PIECES];
-  __shared__ int stream_tiles[2];
+  __shared__ Walker places[C::STREAMS + 1];              // the bounds of this CTA's segments
+  __shared__ int64_t tiles_at[C::STREAMS + 1];
+  __shared__ int segment_width;
   __shared__ uint32_t tmem_slot;
   // scales of the tiles on their way: K's pages (16 tokens each), then V's
   __shared__ float4 scales[C::STREAMS][C::QUANT ? C::SCALES : 1][4];
@@ -610,13 +645,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto p_ready = [&](int t) { return bar0 + 8 * (kTileBars + 6 + t); };
   auto o_full = [&](int t) { return bar0 + 8 * (kTileBars + 8 + t); };
   auto done_bar = [&](int t) { return bar0 + 8 * (kTileBars + 10 + t); };
-  const uint32_t plan_bar = bar0 + 8 * (kTileBars + 12);
   // the i-th V tile with rows that one product warp clears for both (shared form); the ring holds
   // fewer such tiles than there are barriers
   static_assert(C::STAGES / 2 + 1 < kClean, "a barrier of cleared tiles reused too early");
-  auto clean = [&](uint32_t i) { return bar0 + 8 * (kTileBars + 13 + i % kClean); };
+  auto clean = [&](uint32_t i) { return bar0 + 8 * (kTileBars + 12 + i % kClean); };
   // row tile t's turn at the tensor core (shared form)
-  auto turn = [&](int t) { return bar0 + 8 * (kTileBars + 13 + kClean + t); };
+  auto turn = [&](int t) { return bar0 + 8 * (kTileBars + 12 + kClean + t); };
   // piece k of a stream is known / no longer needed
   auto pc_full = [&](int st, uint32_t k) {
     return bar0 + 8 * (kPieceBars + st * C::PIECES + k % C::PIECES);
@@ -650,7 +684,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(turn(t), 1);
     }
     for (int i = 0; i < kClean; ++i) mbar_init(clean(i), 1);
-    mbar_init(plan_bar, 1);
     for (int st = 0; st < C::STREAMS; ++st)
       for (int k = 0; k < C::PIECES; ++k) {
         mbar_init(pc_full(st, k), 1);
@@ -675,19 +708,48 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   pdl_trigger();
   pdl_wait();
 
-  // Every CTA counts the tiles of the batch.  Past 32 sequences all warps do, one sum per group of
-  // 32, in the space of the last stage of the ring (whose first tile comes after the plan).
-  int64_t *sums = reinterpret_cast<int64_t *>(smem_raw + (sm - smem_u32(smem_raw)) + C::RING +
-                                              (C::STAGES - 1) * C::TILE);
+  // Every CTA lays out the batch's tiles.  Past 32 sequences all warps do, one sum per group of 32,
+  // in the space of the ring; then a warp for each bound of this CTA's segments finds its place.
+  GroupSum *sums = reinterpret_cast<GroupSum *>(smem_raw + (sm - smem_u32(smem_raw)) + C::RING);
   const int groups = (p.B + 31) / 32;
   int32_t *report = blockIdx.x == 0 ? p.err : nullptr;
   if (groups > 1) {
     for (int g = warp; g < groups; g += C::THREADS / 32) {
       Group x;
       x.load(p, g, S, lane, report);
-      if (lane == 31) sums[g] = x.upto;
+      if (lane == 31) sums[g] = GroupSum{x.upto, x.units};
+    }
+    __syncthreads();
+  }
+  if (warp >= 8 && warp <= 8 + C::STREAMS) {
+    Group group;
+    GroupSum total{0, 0};
+    if (groups == 1) {
+      group.load(p, 0, S, lane, warp == 8 ? report : nullptr);
+      total = GroupSum{shfl64(group.upto, 31), __shfl_sync(0xffffffffu, group.units, 31)};
+    } else {
+      for (int g = lane; g < groups; g += 32) {
+        total.upto += sums[g].upto;
+        total.units += sums[g].units;
+      }
+      total.upto = shfl64(scan64(total.upto, lane), 31);
+      total.units = shfl64(scan64(total.units, lane), 31);
+    }
+    const int64_t width = p.workers == 1 ? total.upto
+                                         : static_cast<int64_t>(__umul64hi(
+                                               static_cast<uint64_t>(total.upto + p.workers - 1),
+                                               p.over_workers));
+    const int64_t start = (static_cast<int64_t>(blockIdx.x) * C::STREAMS + warp - 8) * width;
+    Walker w;
+    const int64_t tiles = w.place(p, sums, total, group, start, S, lane);
+    w.remaining = static_cast<int>(max(static_cast<int64_t>(0), min(width, total.upto - start)));
+    if (lane == 0) {
+      places[warp - 8] = w;
+      tiles_at[warp - 8] = tiles;
+      if (warp == 8) segment_width = static_cast<int>(width);
     }
   }
+  fence_proxy_async();                                   // the sums' space is TMA's from here
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -704,13 +766,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     return x.n > 0;
   };
   auto ring_order = [&] {
-    RingOrder r{0, 0, 0, 0};
-    ok = mbar_wait(plan_bar, 0);
-    if (ok) {
-      r.n0 = stream_tiles[0];
-      r.n1 = stream_tiles[1];
-    }
-    return r;
+    return RingOrder{static_cast<int>(tiles_at[1] - tiles_at[0]),
+                     C::STREAMS == 2 ? static_cast<int>(tiles_at[C::STREAMS] - tiles_at[1]) : 0, 0, 0};
   };
 
   if (warp < 8) {
@@ -733,12 +790,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     x.row + tok0, q_full(t));
       ++q_loads;
     };
-    Piece x;
-    for (uint32_t k = 0; read_piece(st, k, x); ++k) {
-      const uint32_t tile0 = tiles;
-      tiles += x.n;
+    auto done_with = [&](uint32_t k) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pc_empty(st, k));
+    };
+    for (uint32_t k = 0;; ++k) {
+      ok = ok && mbar_wait(pc_full(st, k), pc_parity(k));
+      if (!ok) break;
+      // the piece stays where it is until its rows are written, rather than in registers
+      const Piece &x = pieces[st][k % C::PIECES];
+      const int n_tiles = x.n, tile_0 = x.tile;
+      if (n_tiles == 0) break;
+      [[maybe_unused]] const uint32_t tile0 = tiles;
+      tiles += n_tiles;
       const int ntok = min(p.tok, x.ntok - tok0);        // tokens of this tile
-      if (ntok <= 0) continue;
+      if (ntok <= 0) {
+        done_with(k);
+        continue;
+      }
       if (row == 0 && !q_sent) load_q(x);
       __syncwarp();
       q_sent = false;
@@ -753,8 +822,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int all_lo = p.causal && p.window > 0 ? x.pos + tok0 + ntok - p.window : 0;
       float m = -INFINITY;                               // reference maximum, times c
       float l = 0.f;
-      for (int i = 0; i < x.n; ++i) {
-        const int key0 = (x.tile + i) * kKeys;
+      for (int i = 0; i < n_tiles; ++i) {
+        const int key0 = (tile_0 + i) * kKeys;
         // code pools: the scales of the tile's pages, K's then V's
         [[maybe_unused]] uint32_t sc = 0;
         if constexpr (C::QUANT) {
@@ -765,7 +834,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         ok = ok && mbar_wait(s_full(t), s_phase);
         if (!ok) break;
         s_phase ^= 1;
-        if (i == x.n - 1 && row == 0) {
+        if (i == n_tiles - 1 && row == 0) {
           // the products with this Q tile are done: the next piece's may come, if this row tile has
           // part in it
           const uint32_t k1 = k + 1;
@@ -970,6 +1039,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
       tc_fence_before();
+      done_with(k);
     }
     // after a wait that gave up, a Q tile may still be arriving
     if (!ok && row == 0)
@@ -978,22 +1048,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
     if (warp == C::PIECE_WARP) {
       // ---------------------------------------------------------------- the pieces of the streams
-      Group group;
-      group.g = -1;
-      int64_t total = 0;
-      if (groups == 1) {
-        group.load(p, 0, S, lane, report);
-        total = shfl64(group.upto, 31);
-      } else {
-        for (int g = lane; g < groups; g += 32) total += sums[g];
-        total = shfl64(scan64(total, lane), 31);
-      }
-      const int64_t width = p.workers == 1 ? total
-                                           : static_cast<int64_t>(__umul64hi(
-                                                 static_cast<uint64_t>(total + p.workers - 1),
-                                                 p.over_workers));
       // this stream's walker and, in the separate form, the other's; they change places
-      Walker walk{}, other{};
+      Walker walk = places[0], other = places[C::STREAMS - 1];
       int4 cut = make_int4(0, 0, 0, 0), other_cut = cut;
       uint32_t known = 0, other_known = 0;               // pieces published
       bool over = false, other_over = C::STREAMS == 1;
@@ -1013,18 +1069,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           other_over = o;
         }
       };
-#pragma unroll 1
-      for (int st = 0; st < C::STREAMS; ++st) {
-        const int worker = blockIdx.x * C::STREAMS + st;
-        const int64_t first = min(total, worker * width);
-        walk.init(p, group, sums, first, min(total, first + width), S, lane);
-        if (lane == 0) stream_tiles[st] = walk.remaining;
-        swap_streams();
-      }
-      if (C::STREAMS == 1 && lane == 0) stream_tiles[1] = 0;
-      fence_proxy_async();               // the sums' space is the ring's from here
-      __syncwarp();
-      if (lane == 0) mbar_arrive(plan_bar);
       int st = 0;
       uint32_t idle = 0;
 #pragma unroll 1
@@ -1047,7 +1091,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             ++known;
             if (!over && x.starts && !x.ends)
-              cut = make_int4(x.row, x.ntok, x.h, (rest - 1) / static_cast<int>(width) + 1);
+              cut = make_int4(x.row, x.ntok, x.h, (rest - 1) / segment_width + 1);
           } else if (C::STREAMS == 1 || ++idle > kWaitSpins / 16) {
             ok = false;
             break;
@@ -1501,6 +1545,7 @@ pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t 
   p.causal = causal;
   p.tok = plan.tok;
   p.workers = plan.workers;
+  p.unit_cost = plan.shared ? 2 : 2;
   p.over_workers = ~uint64_t(0) / plan.workers + 1;       // exact for totals below 2^55
   p.rows = plan.rows;
   // c > 0 keeps a masked score's c s at -inf; 1e-30 scores every key alike, as 0 does
