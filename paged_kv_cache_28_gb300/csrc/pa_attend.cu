@@ -412,14 +412,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("mul.rn.f32x2 %0, %1, %2;"
-      : "=l"(reinterpret_cast<uint64_t &>(d))
-      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-  return d;
-}
-
 // 32 bytes to global memory; wide: the address is 32-byte aligned, and a whole sector goes at once
 __device__ __forceinline__ void store32(void *dst, const uint32_t *v, bool wide) {
   if (wide) {
@@ -438,25 +430,24 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// mbar_wait for the one warp that everything else waits for: it looks again at once, where
-// try_wait may put the warp to sleep and wake it late.
-__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
-  for (uint32_t it = 0; it < 16 * kWaitSpins; ++it) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (done) return true;
-  }
-  return false;
-}
-
 // One look at a barrier: whether the phase with the given parity is complete.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  return mbar_wait<1>(bar, parity);
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// mbar_wait for the warps that everything else waits for: they look again at once, where try_wait
+// may put the warp to sleep and wake it late.
+__device__ __forceinline__ bool mbar_spin(uint32_t bar, uint32_t parity) {
+  for (uint32_t it = 0; it < 16 * kWaitSpins; ++it)
+    if (mbar_test(bar, parity)) return true;
+  return false;
 }
 
 // ------------------------------------------------------------------ codes to bf16
@@ -563,23 +554,17 @@ __device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, 
 
 // ------------------------------------------------------------------ the kernel
 
-// The order of the K and V tiles in the rings: in step j each stream has V of its tile j - 1,
-// then K of its tile j.  n: tiles of each stream.  Every warp that fills or reads a ring goes
-// through all of its tiles in this order: a barrier's parity tells its phase only from the
-// phases next to it.
+// Step j of a stream of n tiles: the products with V of tile j - 1, then those with K of tile j.
+// Its ring holds K and V tiles in turn: tile j's are its 2 j-th and the one after.  Every warp that
+// fills or reads a ring goes through all of its tiles in this order: a barrier's parity tells its
+// phase only from the phases next to it.
 struct RingOrder {
-  int n0, n1, j;
-  uint32_t base;               // tiles before this step
-  __device__ __forceinline__ int n(int st) const { return st ? n1 : n0; }
-  __device__ __forceinline__ bool v(int st) const { return j > 0 && j - 1 < n(st); }
-  __device__ __forceinline__ bool k(int st) const { return j < n(st); }
-  __device__ __forceinline__ uint32_t v_at(int st) const { return base + (st ? v(0) + k(0) : 0); }
-  __device__ __forceinline__ uint32_t k_at(int st) const { return v_at(st) + v(st); }
-  __device__ __forceinline__ bool more() const { return j <= max(n0, n1) && n0 + n1 > 0; }
-  __device__ __forceinline__ void step() {
-    base += v(0) + k(0) + v(1) + k(1);
-    ++j;
-  }
+  int n, j;
+  __device__ __forceinline__ bool more() const { return j <= n && n > 0; }
+  __device__ __forceinline__ bool v() const { return j > 0; }
+  __device__ __forceinline__ bool k() const { return j < n; }
+  __device__ __forceinline__ uint32_t v_at() const { return 2 * j - 1; }
+  __device__ __forceinline__ uint32_t k_at() const { return 2 * j; }
 };
 
 // kKind: the pools' pa_kv_dtype.  Codes (D = 128) are restored to bf16 tiles, without their scale,
@@ -592,28 +577,31 @@ struct AttendCfg {
   static constexpr int TILE = kKeys * D * 2;            // bytes of a Q, K or V tile
   static constexpr int CODE_ROW = KIND == PA_KV_INT4 ? 64 : 128;
   static constexpr int RAW_TILE = kKeys * CODE_ROW;
-  // the ring of K and V tiles; code pools: as many code tiles wait before it (224 KB with Q)
-  static constexpr int STAGES = D == 64 ? 12 : KIND == PA_KV_BF16 ? 5 : KIND == PA_KV_FP8_E4M3 ? 3 : 4;
-  static constexpr int RAW = QUANT ? 4 : 1;
+  // the rings of K and V tiles, one per stream; code pools: rings of code tiles before them (at most
+  // 224 KB with Q)
+  static constexpr int STAGES =
+      D == 64 ? 12 : !kShared ? 4 : KIND == PA_KV_BF16 ? 5 : KIND == PA_KV_FP8_E4M3 ? 3 : 4;
+  static constexpr int RAW = !QUANT ? 1 : KIND == PA_KV_FP8_E4M3 && !kShared ? 2 : 4;
   static constexpr int RING = 2 * TILE;                 // after the two Q tiles
   static constexpr int RAW_RING = RING + STAGES * TILE;
   static constexpr int SMEM = RAW_RING + (QUANT ? RAW * RAW_TILE : 0) + 1024;
-  // Warps 0-7 softmax.  Then the products (shared form: a warp for each row tile, so that one's
-  // waits are filled by the other's products; separate form: one warp for both streams), the
-  // pieces, the loads (bf16: two warps with half of every tile's copies each, since a copy is slow
-  // to issue; code pools: one, and four warps that restore codes).  512 threads start with 128 registers, dealt anew
+  // Warps 0-7 softmax.  Then the products (a warp for each row tile, so that one's waits are
+  // filled by the other's products), the pieces, the loads and, for code pools, eight that restore
+  // codes.  XX threads start with 128 registers, dealt anew
   // by groups of four warps as 256 x 184 + 256 x 72: a softmax thread holds its row's 128 scores.
   static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr int MMA_WARP = 8, PIECE_WARP = 10, LOAD_WARP = 11;
-  static constexpr int LOADERS = 1;
   static constexpr int CODE_WARP = 12, CODE_WARPS = 8;  // code pools
   static constexpr int SOFTMAX_REGS = QUANT ? 144 : 216, OTHER_REGS = QUANT ? 64 : 72;
   static constexpr int STREAMS = SHARED ? 1 : 2;        // key streams of a CTA
+  static constexpr int PER = STAGES / STREAMS;          // ring stages of a stream
+  static constexpr int RAW_PER = QUANT ? RAW / STREAMS : 1;
+  static constexpr int RESTORERS = CODE_WARPS / STREAMS;   // warps that restore a stream's codes
   static constexpr int PIECES = 6;                      // pieces known ahead per stream
   static constexpr int SCALES = 5;                      // tiles whose scales are held per stream
   // the scales of tile j + SCALES are stored before its K is issued; by then the copies have
   // come 2 (SCALES - 1) past V of tile j, which must be further than both rings hold
-  static_assert(!QUANT || 2 * (SCALES - 1) >= RAW + STAGES, "scales overwritten too early");
+  static_assert(!QUANT || 2 * (SCALES - 1) >= RAW_PER + PER, "scales overwritten too early");
 };
 
 template <class C>
@@ -636,9 +624,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t sm = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t bar0 = smem_u32(bars);
-  auto kv_full = [&](uint32_t k) { return bar0 + 8 * (k % C::STAGES); };
-  auto kv_empty = [&](uint32_t k) { return bar0 + 8 * (C::STAGES + k % C::STAGES); };
-  auto kv_parity = [](uint32_t k) { return (k / C::STAGES) & 1; };
+  // K or V tile k of a stream: in shared memory / no longer needed
+  auto kv_stage = [](int st, uint32_t k) { return st * C::PER + k % C::PER; };
+  auto kv_full = [&](int st, uint32_t k) { return bar0 + 8 * kv_stage(st, k); };
+  auto kv_empty = [&](int st, uint32_t k) { return bar0 + 8 * (C::STAGES + kv_stage(st, k)); };
+  auto kv_parity = [](uint32_t k) { return (k / C::PER) & 1; };
   auto q_full = [&](int t) { return bar0 + 8 * (kTileBars + t); };
   auto s_full = [&](int t) { return bar0 + 8 * (kTileBars + 2 + t); };
   auto p_early = [&](int t) { return bar0 + 8 * (kTileBars + 4 + t); };
@@ -647,7 +637,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   auto done_bar = [&](int t) { return bar0 + 8 * (kTileBars + 10 + t); };
   // the i-th V tile with rows that one product warp clears for both (shared form); the ring holds
   // fewer such tiles than there are barriers
-  static_assert(C::STAGES / 2 + 1 < kClean, "a barrier of cleared tiles reused too early");
+  static_assert(C::PER / 2 + 1 < kClean, "a barrier of cleared tiles reused too early");
   auto clean = [&](uint32_t i) { return bar0 + 8 * (kTileBars + 12 + i % kClean); };
   // row tile t's turn at the tensor core (shared form)
   auto turn = [&](int t) { return bar0 + 8 * (kTileBars + 12 + kClean + t); };
@@ -660,9 +650,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   };
   auto pc_parity = [](uint32_t k) { return (k / C::PIECES) & 1; };
   // code pools: code tiles landed / restored, scales of a stream's tile n stored
-  auto raw_full = [&](uint32_t k) { return bar0 + 8 * (kRawBars + k % C::RAW); };
-  auto raw_empty = [&](uint32_t k) { return bar0 + 8 * (kRawBars + C::RAW + k % C::RAW); };
-  auto raw_parity = [](uint32_t k) { return (k / C::RAW) & 1; };
+  auto raw_stage = [](int st, uint32_t k) { return st * C::RAW_PER + k % C::RAW_PER; };
+  auto raw_full = [&](int st, uint32_t k) { return bar0 + 8 * (kRawBars + raw_stage(st, k)); };
+  auto raw_empty = [&](int st, uint32_t k) { return bar0 + 8 * (kRawBars + C::RAW + raw_stage(st, k)); };
+  auto raw_parity = [](uint32_t k) { return (k / C::RAW_PER) & 1; };
   auto sc_full = [&](int st, uint32_t n) {
     return bar0 + 8 * (kRawBars + 2 * C::RAW + st * C::SCALES + n % C::SCALES);
   };
@@ -671,8 +662,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(kv_full(i), C::QUANT ? C::CODE_WARPS : C::LOADERS);  // the warps that fill it
-      mbar_init(kv_empty(i), C::SHARED ? 2 : 1);         // the product warps
+      mbar_init(bar0 + 8 * i, C::QUANT ? C::RESTORERS : 1);      // kv_full: the warps that fill it
+      mbar_init(bar0 + 8 * (C::STAGES + i), C::SHARED ? 2 : 1);  // kv_empty: the product warps
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
@@ -687,12 +678,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int st = 0; st < C::STREAMS; ++st)
       for (int k = 0; k < C::PIECES; ++k) {
         mbar_init(pc_full(st, k), 1);
-        mbar_init(pc_empty(st, k), C::LOADERS + (C::SHARED ? 2 + 8 : 1 + 4));   // every reader
+        mbar_init(pc_empty(st, k), 1 + (C::SHARED ? 2 + 8 : 1 + 4));   // every reader
       }
     if constexpr (C::QUANT) {
       for (int i = 0; i < C::RAW; ++i) {
-        mbar_init(raw_full(i), 1);
-        mbar_init(raw_empty(i), C::CODE_WARPS);
+        mbar_init(bar0 + 8 * (kRawBars + i), 1);                     // raw_full
+        mbar_init(bar0 + 8 * (kRawBars + C::RAW + i), C::RESTORERS);  // raw_empty
       }
       for (int st = 0; st < C::STREAMS; ++st)
         for (int n = 0; n < C::SCALES; ++n) mbar_init(sc_full(st, n), 1);
@@ -765,9 +756,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (lane == 0) mbar_arrive(pc_empty(st, k));
     return x.n > 0;
   };
-  auto ring_order = [&] {
-    return RingOrder{static_cast<int>(tiles_at[1] - tiles_at[0]),
-                     C::STREAMS == 2 ? static_cast<int>(tiles_at[C::STREAMS] - tiles_at[1]) : 0, 0, 0};
+  auto ring_order = [&](int st) {
+    return RingOrder{static_cast<int>(tiles_at[st + 1] - tiles_at[st]), 0};
   };
 
   if (warp < 8) {
@@ -859,11 +849,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (static_cast<unsigned>(j0 + j - first) >= seen) s[j] = __float_as_uint(-INFINITY);
             }
           };
-          // what the scores of a block's two pages are multiplied by: above zero, so that -inf stays
+          // what the scores of a block's two pages are multiplied by
           auto k_factors = [&](int block) {
-            if constexpr (!C::QUANT) return make_float2(p.c, p.c);
-            const float2 f = lds_f32x2(sc + 8 * block);
-            return make_float2(fmaxf(f.x * p.c, 1e-30f), fmaxf(f.y * p.c, 1e-30f));
+            return C::QUANT ? lds_f32x2(sc + 8 * block) : make_float2(p.c, p.c);
           };
           float mx[2] = {-INFINITY, -INFINITY};
           auto maximum = [&](const uint32_t *s, float2 f) {   // of a block of 32 columns
@@ -880,22 +868,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
           };
           // A block of 32 columns is on its way while another is worked on.  bf16 pools: the row's
-          // scores stay in registers; code pools read them twice, in loops: with their restoring
-          // warps' code beside it, the unrolled form waits for instructions half of its time.
+          // scores stay in registers; code pools, whose threads have fewer, read half of them twice.
           uint32_t s[C::QUANT ? 64 : kKeys];
           if constexpr (C::QUANT) {
-            tc_ld32(s + 32, tS + 96);
 #pragma unroll 1
-            for (int j = 2; j >= 0; j -= 2) {            // blocks j + 1 and j
-              const float2 f1 = k_factors(j + 1), f0 = k_factors(j);
-              tc_wait_ld32(s + 32);
+            for (int j = 2; j >= 0; j -= 2) {            // blocks j and j + 1
               tc_ld32(s, tS + 32 * j);
-              hide(s + 32, 32 * j + 32);
-              maximum(s + 32, f1);
+              tc_ld32(s + 32, tS + 32 * j + 32);
+              const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
               tc_wait_ld32(s);
-              if (j > 0) tc_ld32(s + 32, tS + 32);
+              tc_use32(s + 32);
               hide(s, 32 * j);
               maximum(s, f0);
+              hide(s + 32, 32 * j + 32);
+              maximum(s + 32, f1);
             }
           } else {
             tc_ld32(s, tS);
@@ -935,23 +921,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
           }
           const float neg = m == -INFINITY ? 0.f : -m;
-          const float2 n2 = make_float2(neg, neg);
+          // The weights of block j, over columns that are already read.  Code pools: V's scale enters
+          // in the exponent, and leaves the sums of its page again.
           float2 sum[2] = {};
-          // the weights of block j, over columns that are already read
           auto weights = [&](const uint32_t *s, int j, float2 f) {
-            float2 v = make_float2(1.f, 1.f);
+            float2 v = make_float2(0.f, 0.f);
             if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
             uint32_t packed[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float c1 = e < 8 ? f.x : f.y, v1 = e < 8 ? v.x : v.y;
-              float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
-                              make_float2(c1, c1), n2);
-              y.x = ex2(y.x);
-              y.y = ex2(y.y);
-              sum[e & 1] = add2(sum[e & 1], y);
-              if constexpr (C::QUANT) y = mul2(y, make_float2(v1, v1));
-              packed[e] = pack_bf16(y.x, y.y);
+            for (int half = 0; half < 2; ++half) {
+              const float c1 = half ? f.y : f.x, lv = half ? v.y : v.x;
+              const float2 shift = make_float2(neg + lv, neg + lv);
+              float2 page[2] = {};
+#pragma unroll
+              for (int e = 8 * half; e < 8 * half + 8; ++e) {
+                float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                make_float2(c1, c1), shift);
+                y.x = ex2(y.x);
+                y.y = ex2(y.y);
+                float2 &to = C::QUANT ? page[e & 1] : sum[e & 1];
+                to = add2(to, y);
+                packed[e] = pack_bf16(y.x, y.y);
+              }
+              if constexpr (C::QUANT) {
+                const float back = ex2(-lv);
+                sum[half] = fma2(add2(page[0], page[1]), make_float2(back, back), sum[half]);
+              }
             }
             tc_st16(tS + 16 * j, packed);
             if (j == kEarly / 32 - 1) {
@@ -962,19 +957,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
           };
           if constexpr (C::QUANT) {
-#pragma unroll 1
-            for (int j = 0; j < 4; j += 2) {             // blocks j (here, or on its way) and j + 1
+            // (the separate form in a loop: its few tiles a CTA wait for instructions first of all)
+#pragma unroll(C::SHARED ? 2 : 1)
+            for (int j = 0; j < 4; j += 2) {
               const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
               if (j > 0) {
                 tc_wait_ld32(s);
-                hide(s, 32 * j);
+                tc_use32(s + 32);
+                hide(s, 64);
+                hide(s + 32, 96);
               }
-              tc_ld32(s + 32, tS + 32 * j + 32);
               weights(s, j, f0);
-              tc_wait_ld32(s + 32);
-              if (j == 0) tc_ld32(s, tS + 64);
-              hide(s + 32, 32 * j + 32);
+              if (j == 0) tc_ld32(s, tS + 64);           // columns that are not written over yet
               weights(s + 32, j + 1, f1);
+              if (j == 0) tc_ld32(s + 32, tS + 96);
             }
           } else {
 #pragma unroll
@@ -1108,11 +1104,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         p.cut[blockIdx.x * C::STREAMS + st] = cut;
         if (C::STREAMS == 2) p.cut[blockIdx.x * C::STREAMS + (st ^ 1)] = other_cut;
       }
-    } else if (warp >= C::LOAD_WARP && warp < C::LOAD_WARP + C::LOADERS) {
+    } else if (warp == C::LOAD_WARP) {
       // ---------------------------------------------------------------- K and V tiles
       // One box per 16 tokens (a page of a tile) and, in bf16 pools, 64 columns.
       constexpr int kBox = C::QUANT ? 16 * C::CODE_ROW : 16 * 128;
-      constexpr int kRing = C::QUANT ? C::RAW : C::STAGES;
+      constexpr int kRing = C::QUANT ? C::RAW_PER : C::PER;
       const int outside = p.nblocks * p.bs;              // a row past the pool reads zeros
       // Block ids come four tiles (32 runs of 16 tokens, one per lane) at a time, two such chunks
       // ahead of the copies; scales one.
@@ -1167,20 +1163,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       };
-      uint32_t issued = 0;                               // the last tile this warp has issued, + 1
+      auto full_bar = [&](int st, uint32_t k) { return C::QUANT ? raw_full(st, k) : kv_full(st, k); };
+      auto room_bar = [&](int st, uint32_t k) { return C::QUANT ? raw_empty(st, k) : kv_empty(st, k); };
       // rows: the pages' first pool rows, in every lane (-1: unseen)
-      auto issue = [&](const CUtensorMap *map, uint32_t k, int h, const int (&rows)[8], bool zeros) {
-        const uint32_t full = C::QUANT ? raw_full(k) : kv_full(k);
-        ok = ok && mbar_wait(C::QUANT ? raw_empty(k) : kv_empty(k), ((k / kRing) & 1) ^ 1);
-        if (!ok) return;
-        issued = k + 1;
+      auto issue = [&](const CUtensorMap *map, int st, uint32_t k, int h, const int (&rows)[8],
+                       bool zeros) {
+        const uint32_t full = full_bar(st, k);
         if (elect_one()) {
           uint32_t boxes = 0;
 #pragma unroll
           for (int page = 0; page < 8; ++page) boxes += rows[page] >= 0 || zeros;
           mbar_arrive_expect_tx(full, boxes * kBox * (C::QUANT ? 1 : C::HALVES));
-          const uint32_t dst = C::QUANT ? sm + C::RAW_RING + (k % kRing) * C::RAW_TILE
-                                        : sm + C::RING + (k % kRing) * C::TILE;
+          const uint32_t dst = C::QUANT ? sm + C::RAW_RING + raw_stage(st, k) * C::RAW_TILE
+                                        : sm + C::RING + kv_stage(st, k) * C::TILE;
 #pragma unroll
           for (int page = 0; page < 8; ++page) {
             if (rows[page] < 0 && !zeros) continue;
@@ -1193,11 +1188,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         __syncwarp();
       };
-      RingOrder r = ring_order();
-      int prev_h[C::STREAMS] = {}, rows[C::STREAMS][8] = {};
+      int head[C::STREAMS] = {}, rows[C::STREAMS][8] = {};
+      uint32_t next[C::STREAMS] = {}, all[C::STREAMS];   // K and V tiles issued, and in all
       uint32_t tiles[C::STREAMS] = {};
 #pragma unroll
       for (int st = 0; st < C::STREAMS; ++st) {
+        all[st] = 2 * ring_order(st).n;
         Src &z = src[st];
         z.x.n = z.at = z.i = 0;
         z.k = 0;
@@ -1222,56 +1218,76 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const uint32_t n = tiles[st]++;
           float *sc = reinterpret_cast<float *>(scales[st][n % C::SCALES]);
           if ((lane >> 3) == z.i) {
-            sc[lane & 7] = z.cur.ks;
-            sc[8 + (lane & 7)] = z.cur.vs;
+            // c times K's scale and log2 of V's, both kept above zero: a zero scale's codes add
+            // nothing, and -inf stays -inf
+            sc[lane & 7] = fmaxf(z.cur.ks * p.c, 1e-30f);
+            sc[8 + (lane & 7)] = __log2f(fmaxf(z.cur.vs, 1e-30f));
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(sc_full(st, n));
         }
         ++z.i;
       };
-      for (; ok && r.more(); r.step()) {
+      uint32_t idle = 0;
+      for (bool more = true; more && ok;) {
+        more = false;
 #pragma unroll
         for (int st = 0; st < C::STREAMS; ++st) {
-          // pages of V that no token sees read zeros (bf16): a weight of 0 times what lies there
-          // must be 0; codes are never infinite or NaN once restored
-          if (r.v(st)) issue(&tmV, r.v_at(st), prev_h[st], rows[st], !C::QUANT);
-          if (ok && r.k(st)) {
-            next_tile(st, prev_h[st], rows[st]);
-            issue(&tmK, r.k_at(st), prev_h[st], rows[st], false);
+          const uint32_t k = next[st];
+          if (!ok || k == all[st]) continue;
+          more = true;
+          // one stream: wait for room; two: see which has some
+          const uint32_t parity = ((k / kRing) & 1) ^ 1;
+          if (C::STREAMS == 1) {
+            ok = mbar_wait(room_bar(st, k), parity);
+          } else if (!mbar_test(room_bar(st, k), parity)) {
+            ok = ++idle < 4 * kWaitSpins;
+            continue;
+          }
+          if (!ok) break;
+          idle = 0;
+          next[st] = k + 1;
+          if (k & 1) {
+            // pages of V that no token sees read zeros (bf16): a weight of 0 times what lies there
+            // must be 0; codes are never infinite or NaN once restored
+            issue(&tmV, st, k, head[st], rows[st], !C::QUANT);
+          } else {
+            next_tile(st, head[st], rows[st]);
+            if (ok) issue(&tmK, st, k, head[st], rows[st], false);
+            else next[st] = k;
           }
         }
       }
       // after a wait that gave up, the copies in flight must have landed before the CTA's memory goes
       if (!ok)
-        for (uint32_t k = issued > kRing ? issued - kRing : 0; k < issued; ++k)
-          mbar_wait(C::QUANT ? raw_full(k) : kv_full(k), (k / kRing) & 1);
+        for (int st = 0; st < C::STREAMS; ++st)
+          for (uint32_t k = next[st] > kRing ? next[st] - kRing : 0; k < next[st]; ++k)
+            mbar_wait(full_bar(st, k), (k / kRing) & 1);
     } else if (C::QUANT && warp >= C::CODE_WARP) {
       // ---------------------------------------------------------------- codes to bf16 tiles
-      const RingOrder r = ring_order();
-      const uint32_t all = 2 * (r.n0 + r.n1);
+      const int st = (warp - C::CODE_WARP) / C::RESTORERS, w = (warp - C::CODE_WARP) % C::RESTORERS;
+      const uint32_t all = 2 * ring_order(st).n;
       for (uint32_t k = 0; ok && k < all; ++k) {
-        ok = mbar_wait(raw_full(k), raw_parity(k)) && mbar_wait(kv_empty(k), kv_parity(k) ^ 1);
+        ok = mbar_wait(raw_full(st, k), raw_parity(k)) && mbar_wait(kv_empty(st, k), kv_parity(k) ^ 1);
         if (!ok) break;
-        restore_tile<C::KIND, C::CODE_WARPS>(sm + C::RAW_RING + (k % C::RAW) * C::RAW_TILE,
-                              sm + C::RING + (k % C::STAGES) * C::TILE, warp - C::CODE_WARP, lane);
+        restore_tile<C::KIND, C::RESTORERS>(sm + C::RAW_RING + raw_stage(st, k) * C::RAW_TILE,
+                                            sm + C::RING + kv_stage(st, k) * C::TILE, w, lane);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(raw_empty(k));
-          mbar_arrive(kv_full(k));
+          mbar_arrive(raw_empty(st, k));
+          mbar_arrive(kv_full(st, k));
         }
       }
     } else if (warp < C::MMA_WARP + 2) {
       // ---------------------------------------------------------------- matrix products
-      // shared form: this warp's row tile t0; separate form: row tile st of each stream, by one warp
-      const int t0 = warp - C::MMA_WARP;
+      const int t = warp - C::MMA_WARP, st = C::SHARED ? 0 : t;      // this warp's row tile and stream
       const uint32_t idS = mma_desc(kKeys, false) | (p.negate ? kNegateA : 0u);
       constexpr uint32_t idO = mma_desc(C::D, true);
       const uint64_t q_desc = smem_desc(sm, 16, 1024);
       const uint64_t k_desc = smem_desc(sm + C::RING, 16, 1024);
       const uint64_t v_desc = smem_desc(sm + C::RING, kKeys * 128, 1024);
-      struct Stream {
+      struct {
         Piece x;
         int i;                                           // the piece's tile that K is due of
         uint32_t piece, q_phase, p_phase;
@@ -1279,7 +1295,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // token sees, whether this row tile has part in it
         bool first, last, mine;
         int lo, hi;
-      } z[C::STREAMS] = {};
+      } y{};
       uint32_t cleared = 0;
       // Shared form: the row tiles take turns at the tensor core, O_t += P_t V and the next S_t at a
       // time.  Left to themselves their products would run interleaved and end together, and then
@@ -1288,111 +1304,105 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // the weights' last part is waited for ahead of the turn, and the turn goes on while the last
       // products are still being issued.
       uint32_t turns = 0;
-      if (C::SHARED && t0 == 1 && lane == 0) mbar_arrive(turn(0));
-      RingOrder r = ring_order();
-      for (; ok && r.more() && t0 < 3 - C::STREAMS; r.step()) {
-#pragma unroll
-        for (int st = 0; st < C::STREAMS; ++st) {
-          Stream &y = z[st];
-          const int t = C::SHARED ? t0 : st;
-          const uint32_t tS = tmem + t * kKeys, tO = tmem + 256 + t * 128;
-          const bool v = r.v(st), k = r.k(st);
-          const uint32_t v_at = r.v_at(st), k_at = r.k_at(st);
-          const bool o_first = y.first, o_last = y.last, do_o = v && y.mine;
-          if (v) {
-            ok = ok && mbar_spin(kv_full(v_at), kv_parity(v_at));
-            // rows next to the seen ones in their page may hold anything
-            const int head = C::QUANT || y.lo <= 0 ? 0 : y.lo & 15;
-            const int tail = C::QUANT || y.hi >= kKeys || y.hi <= 0 ? 0 : -y.hi & 15;
-            if (ok && head + tail > 0) {
-              if (t0 == 0) {
-                const uint32_t tile = sm + C::RING + (v_at % C::STAGES) * C::TILE;
-                for (int e = lane; e < (head + tail) * 8 * C::HALVES; e += 32) {
-                  const int n = e / (8 * C::HALVES), chunk = e % (8 * C::HALVES);
-                  const int row = n < head ? y.lo - head + n : y.hi + n - head;
-                  sts128(tile + (chunk >> 3) * (kKeys * 128) + row * 128 + (chunk & 7) * 16,
-                         make_uint4(0, 0, 0, 0));
-                }
-                fence_proxy_async();
-                __syncwarp();
-                if (C::SHARED && lane == 0) mbar_arrive(clean(cleared));
-              } else {
-                ok = mbar_wait(clean(cleared), (cleared / kClean) & 1);
+      if (C::SHARED && t == 1 && lane == 0) mbar_arrive(turn(0));
+      const uint32_t tS = tmem + t * kKeys, tO = tmem + 256 + t * 128;
+      for (RingOrder r = ring_order(st); ok && r.more(); ++r.j) {
+        const bool v = r.v(), k = r.k();
+        const uint32_t v_at = r.v_at(), k_at = r.k_at();
+        const bool o_first = y.first, o_last = y.last, do_o = v && y.mine;
+        if (v) {
+          ok = ok && mbar_spin(kv_full(st, v_at), kv_parity(v_at));
+          // rows next to the seen ones in their page may hold anything
+          const int head = C::QUANT || y.lo <= 0 ? 0 : y.lo & 15;
+          const int tail = C::QUANT || y.hi >= kKeys || y.hi <= 0 ? 0 : -y.hi & 15;
+          if (ok && head + tail > 0) {
+            if (!C::SHARED || t == 0) {
+              const uint32_t tile = sm + C::RING + kv_stage(st, v_at) * C::TILE;
+              for (int e = lane; e < (head + tail) * 8 * C::HALVES; e += 32) {
+                const int n = e / (8 * C::HALVES), chunk = e % (8 * C::HALVES);
+                const int row = n < head ? y.lo - head + n : y.hi + n - head;
+                sts128(tile + (chunk >> 3) * (kKeys * 128) + row * 128 + (chunk & 7) * 16,
+                       make_uint4(0, 0, 0, 0));
               }
-              ++cleared;
-            }
-          }
-          if (k) {
-            if (y.i == y.x.n) {
-              read_piece(st, y.piece++, y.x);
-              y.i = 0;
-            }
-            y.mine = !C::SHARED || t == 0 || y.x.ntok > p.tok;
-            y.first = y.i == 0;
-            y.last = y.i == y.x.n - 1;
-            y.lo = y.x.lo - (y.x.tile + y.i) * kKeys;
-            y.hi = y.x.L - (y.x.tile + y.i) * kKeys;
-            ++y.i;
-            ok = ok && mbar_spin(kv_full(k_at), kv_parity(k_at));
-            if (y.mine && y.first) {
-              ok = ok && mbar_spin(q_full(t), y.q_phase);
-              y.q_phase ^= 1;
-            }
-          }
-          const bool do_s = k && y.mine;
-          if (do_o) ok = ok && mbar_spin(p_early(t), y.p_phase);
-          if (C::SHARED) ok = ok && mbar_spin(turn(t0), turns++ & 1);
-          if (do_o) {                                    // O_t += P_t V
-            const uint64_t b = v_desc + (v_at % C::STAGES) * (C::TILE >> 4);
-            if (ok) {
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int e = 0; e < kEarly / 16; ++e)
-                  tc_mma_ts(tO, tS + e * 8, b + ((e * 16 * 128) >> 4), idO, !o_first || e > 0);
-              }
+              fence_proxy_async();
               __syncwarp();
-              ok = mbar_spin(p_ready(t), y.p_phase);
+              if (C::SHARED && lane == 0) mbar_arrive(clean(cleared));
+            } else {
+              ok = mbar_wait(clean(cleared), (cleared / kClean) & 1);
             }
-            y.p_phase ^= 1;
-            if (ok) {
-              tc_fence_after();
-              if (elect_one()) {
-#pragma unroll
-                for (int e = kEarly / 16; e < kKeys / 16; ++e)
-                  tc_mma_ts(tO, tS + e * 8, b + ((e * 16 * 128) >> 4), idO, 1);
-                if (o_last) tc_commit(o_full(t));
-                tc_commit(kv_empty(v_at));
-              }
-              __syncwarp();
-            }
-          } else if (v && ok && lane == 0) {
-            mbar_arrive(kv_empty(v_at));
+            ++cleared;
           }
-          if (do_s) {                                    // S_t = Q_t K^T
-            if (ok && elect_one()) {
-              const uint64_t a = q_desc + t * (C::TILE >> 4);
-              const uint64_t b = k_desc + (k_at % C::STAGES) * (C::TILE >> 4);
+        }
+        if (k) {
+          if (y.i == y.x.n) {
+            read_piece(st, y.piece++, y.x);
+            y.i = 0;
+          }
+          y.mine = !C::SHARED || t == 0 || y.x.ntok > p.tok;
+          y.first = y.i == 0;
+          y.last = y.i == y.x.n - 1;
+          y.lo = y.x.lo - (y.x.tile + y.i) * kKeys;
+          y.hi = y.x.L - (y.x.tile + y.i) * kKeys;
+          ++y.i;
+          ok = ok && mbar_spin(kv_full(st, k_at), kv_parity(k_at));
+          if (y.mine && y.first) {
+            ok = ok && mbar_spin(q_full(t), y.q_phase);
+            y.q_phase ^= 1;
+          }
+        }
+        const bool do_s = k && y.mine;
+        if (do_o) ok = ok && mbar_spin(p_early(t), y.p_phase);
+        if (C::SHARED) ok = ok && mbar_spin(turn(t), turns++ & 1);
+        if (do_o) {                                    // O_t += P_t V
+          const uint64_t b = v_desc + kv_stage(st, v_at) * (C::TILE >> 4);
+          if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
-              for (int e = 0; e < C::D / 16; ++e) {
-                if (C::SHARED && e == C::D / 32) mbar_arrive(turn(t0 ^ 1));
-                const uint32_t o = ((e >> 2) * (kKeys * 128) + (e & 3) * 32) >> 4;
-                tc_mma_ss(tS, a + o, b + o, idS, e > 0);
-              }
-              tc_commit(s_full(t));
-              tc_commit(kv_empty(k_at));
+              for (int e = 0; e < kEarly / 16; ++e)
+                tc_mma_ts(tO, tS + e * 8, b + ((e * 16 * 128) >> 4), idO, !o_first || e > 0);
             }
             __syncwarp();
-          } else {
-            if (k && ok && lane == 0) mbar_arrive(kv_empty(k_at));
-            if (C::SHARED && ok && lane == 0) mbar_arrive(turn(t0 ^ 1));
+            ok = mbar_spin(p_ready(t), y.p_phase);
           }
+          y.p_phase ^= 1;
+          if (ok) {
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int e = kEarly / 16; e < kKeys / 16; ++e)
+                tc_mma_ts(tO, tS + e * 8, b + ((e * 16 * 128) >> 4), idO, 1);
+              if (o_last) tc_commit(o_full(t));
+              tc_commit(kv_empty(st, v_at));
+            }
+            __syncwarp();
+          }
+        } else if (v && ok && lane == 0) {
+          mbar_arrive(kv_empty(st, v_at));
+        }
+        if (do_s) {                                    // S_t = Q_t K^T
+          if (ok && elect_one()) {
+            const uint64_t a = q_desc + t * (C::TILE >> 4);
+            const uint64_t b = k_desc + kv_stage(st, k_at) * (C::TILE >> 4);
+#pragma unroll
+            for (int e = 0; e < C::D / 16; ++e) {
+              if (C::SHARED && e == C::D / 32) mbar_arrive(turn(t ^ 1));
+              const uint32_t o = ((e >> 2) * (kKeys * 128) + (e & 3) * 32) >> 4;
+              tc_mma_ss(tS, a + o, b + o, idS, e > 0);
+            }
+            tc_commit(s_full(t));
+            tc_commit(kv_empty(st, k_at));
+          }
+          __syncwarp();
+        } else {
+          if (k && ok && lane == 0) mbar_arrive(kv_empty(st, k_at));
+          if (C::SHARED && ok && lane == 0) mbar_arrive(turn(t ^ 1));
         }
       }
       // nothing of this warp's products is in flight when the CTA's memory goes
-      if (lane == 0) tc_commit(done_bar(t0));
+      if (lane == 0) tc_commit(done_bar(t));
       __syncwarp();
-      ok = mbar_wait(done_bar(t0), 0) && ok;
+      ok = mbar_wait(done_bar(t), 0) && ok;
     }
   }
   if (!ok && lane == 0) set_err(p.err, PA_DEVERR_TIMEOUT);
