@@ -496,13 +496,14 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
                : "memory");
 }
 
-// A tile's codes (as TMA swizzled them) to a bf16 tile (128-byte swizzle), by kWarps warps.
+// The codes of a tile's kTokens tokens (as TMA swizzled them) to rows of a bf16 tile (128-byte
+// swizzle), by kWarps warps.
 // Neighbouring lanes write both 64-column halves of a row at once; the order of a lane's stores
 // keeps the two halves off each other's banks.
-template <int KIND, int kWarps>
+template <int KIND, int kTokens, int kWarps>
 __device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, int lane) {
   if constexpr (KIND == PA_KV_FP8_E4M3) {
-    constexpr int kSteps = 32 / kWarps;                  // of four rows
+    constexpr int kSteps = kTokens / 4 / kWarps;         // of four rows
     const int c = lane & 7;                              // 16 codes: columns [16 c, 16 c + 16)
     {
       uint4 v[kSteps];
@@ -525,7 +526,7 @@ __device__ __forceinline__ void restore_tile(uint32_t raw, uint32_t dst, int w, 
       }
     }
   } else {
-    constexpr int kSteps = 16 / kWarps;                  // of eight rows
+    constexpr int kSteps = kTokens / 8 / kWarps;         // of eight rows
     const int c = lane & 3;                              // 32 codes: columns [32 c, 32 c + 32)
     uint4 v[kSteps];
 #pragma unroll
@@ -576,12 +577,14 @@ struct AttendCfg {
   static constexpr int HALVES = D / 64;                 // 128-byte column chunks of a bf16 row
   static constexpr int TILE = kKeys * D * 2;            // bytes of a Q, K or V tile
   static constexpr int CODE_ROW = KIND == PA_KV_INT4 ? 64 : 128;
-  static constexpr int RAW_TILE = kKeys * CODE_ROW;
+  // code tiles come in halves where their ring is short
+  static constexpr int SPLIT = KIND == PA_KV_FP8_E4M3 && !kShared ? 2 : 1;
+  static constexpr int RAW_TILE = kKeys * CODE_ROW / SPLIT;
   // the rings of K and V tiles, one per stream; code pools: rings of code tiles before them (at most
   // 224 KB with Q)
   static constexpr int STAGES =
       D == 64 ? 12 : !kShared ? 4 : KIND == PA_KV_BF16 ? 5 : KIND == PA_KV_FP8_E4M3 ? 3 : 4;
-  static constexpr int RAW = !QUANT ? 1 : KIND == PA_KV_FP8_E4M3 && !kShared ? 2 : 4;
+  static constexpr int RAW = QUANT ? 4 : 1;
   static constexpr int RING = 2 * TILE;                 // after the two Q tiles
   static constexpr int RAW_RING = RING + STAGES * TILE;
   static constexpr int SMEM = RAW_RING + (QUANT ? RAW * RAW_TILE : 0) + 1024;
@@ -601,7 +604,7 @@ struct AttendCfg {
   static constexpr int SCALES = 5;                      // tiles whose scales are held per stream
   // the scales of tile j + SCALES are stored before its K is issued; by then the copies have
   // come 2 (SCALES - 1) past V of tile j, which must be further than both rings hold
-  static_assert(!QUANT || 2 * (SCALES - 1) >= RAW_PER + PER, "scales overwritten too early");
+  static_assert(!QUANT || 2 * (SCALES - 1) >= RAW_PER / SPLIT + PER, "scales overwritten too early");
 };
 
 template <class C>
@@ -662,7 +665,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(bar0 + 8 * i, C::QUANT ? C::RESTORERS : 1);      // kv_full: the warps that fill it
+      mbar_init(bar0 + 8 * i, C::QUANT ? C::RESTORERS * C::SPLIT : 1);  // kv_full: the warps that fill it
       mbar_init(bar0 + 8 * (C::STAGES + i), C::SHARED ? 2 : 1);  // kv_empty: the product warps
     }
     for (int t = 0; t < 2; ++t) {
@@ -1163,37 +1166,40 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       };
-      auto full_bar = [&](int st, uint32_t k) { return C::QUANT ? raw_full(st, k) : kv_full(st, k); };
-      auto room_bar = [&](int st, uint32_t k) { return C::QUANT ? raw_empty(st, k) : kv_empty(st, k); };
-      // rows: the pages' first pool rows, in every lane (-1: unseen)
-      auto issue = [&](const CUtensorMap *map, int st, uint32_t k, int h, const int (&rows)[8],
+      // tile (or part of a tile) u of this warp's ring
+      auto full_bar = [&](int st, uint32_t u) { return C::QUANT ? raw_full(st, u) : kv_full(st, u); };
+      auto room_bar = [&](int st, uint32_t u) { return C::QUANT ? raw_empty(st, u) : kv_empty(st, u); };
+      // rows: the pages' first pool rows, in every lane (-1: unseen); pages [first, first + kPages)
+      constexpr int kPages = 8 / C::SPLIT;
+      auto issue = [&](const CUtensorMap *map, int st, uint32_t u, int h, const int (&rows)[8], int first,
                        bool zeros) {
-        const uint32_t full = full_bar(st, k);
+        const uint32_t full = full_bar(st, u);
         if (elect_one()) {
           uint32_t boxes = 0;
 #pragma unroll
-          for (int page = 0; page < 8; ++page) boxes += rows[page] >= 0 || zeros;
+          for (int page = 0; page < 8; ++page)
+            boxes += page - first >= 0 && page - first < kPages && (rows[page] >= 0 || zeros);
           mbar_arrive_expect_tx(full, boxes * kBox * (C::QUANT ? 1 : C::HALVES));
-          const uint32_t dst = C::QUANT ? sm + C::RAW_RING + raw_stage(st, k) * C::RAW_TILE
-                                        : sm + C::RING + kv_stage(st, k) * C::TILE;
+          const uint32_t dst = C::QUANT ? sm + C::RAW_RING + raw_stage(st, u) * C::RAW_TILE
+                                        : sm + C::RING + kv_stage(st, u) * C::TILE;
 #pragma unroll
           for (int page = 0; page < 8; ++page) {
-            if (rows[page] < 0 && !zeros) continue;
+            if (page < first || page >= first + kPages || (rows[page] < 0 && !zeros)) continue;
             const int row = rows[page] < 0 ? outside : rows[page];
 #pragma unroll
             for (int half = 0; half < (C::QUANT ? 1 : C::HALVES); ++half)
-              tma_load_2d(dst + half * (kKeys * 128) + page * kBox, map,
+              tma_load_2d(dst + half * (kKeys * 128) + (page - first) * kBox, map,
                           h * (C::QUANT ? C::CODE_ROW : C::D) + half * 64, row, full);
           }
         }
         __syncwarp();
       };
       int head[C::STREAMS] = {}, rows[C::STREAMS][8] = {};
-      uint32_t next[C::STREAMS] = {}, all[C::STREAMS];   // K and V tiles issued, and in all
+      uint32_t next[C::STREAMS] = {}, all[C::STREAMS];   // tiles (parts) issued, and in all
       uint32_t tiles[C::STREAMS] = {};
 #pragma unroll
       for (int st = 0; st < C::STREAMS; ++st) {
-        all[st] = 2 * ring_order(st).n;
+        all[st] = 2 * C::SPLIT * ring_order(st).n;
         Src &z = src[st];
         z.x.n = z.at = z.i = 0;
         z.k = 0;
@@ -1233,49 +1239,53 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         more = false;
 #pragma unroll
         for (int st = 0; st < C::STREAMS; ++st) {
-          const uint32_t k = next[st];
-          if (!ok || k == all[st]) continue;
+          const uint32_t u = next[st], k = u / C::SPLIT;
+          const int first = static_cast<int>(u % C::SPLIT) * kPages;
+          if (!ok || u == all[st]) continue;
           more = true;
           // one stream: wait for room; two: see which has some
-          const uint32_t parity = ((k / kRing) & 1) ^ 1;
+          const uint32_t parity = ((u / kRing) & 1) ^ 1;
           if (C::STREAMS == 1) {
-            ok = mbar_wait(room_bar(st, k), parity);
-          } else if (!mbar_test(room_bar(st, k), parity)) {
+            ok = mbar_wait(room_bar(st, u), parity);
+          } else if (!mbar_test(room_bar(st, u), parity)) {
             ok = ++idle < 4 * kWaitSpins;
             continue;
           }
           if (!ok) break;
           idle = 0;
-          next[st] = k + 1;
           if (k & 1) {
             // pages of V that no token sees read zeros (bf16): a weight of 0 times what lies there
             // must be 0; codes are never infinite or NaN once restored
-            issue(&tmV, st, k, head[st], rows[st], !C::QUANT);
+            issue(&tmV, st, u, head[st], rows[st], first, !C::QUANT);
           } else {
-            next_tile(st, head[st], rows[st]);
-            if (ok) issue(&tmK, st, k, head[st], rows[st], false);
-            else next[st] = k;
+            if (first == 0) next_tile(st, head[st], rows[st]);
+            if (!ok) break;
+            issue(&tmK, st, u, head[st], rows[st], first, false);
           }
+          next[st] = u + 1;
         }
       }
       // after a wait that gave up, the copies in flight must have landed before the CTA's memory goes
       if (!ok)
         for (int st = 0; st < C::STREAMS; ++st)
-          for (uint32_t k = next[st] > kRing ? next[st] - kRing : 0; k < next[st]; ++k)
-            mbar_wait(full_bar(st, k), (k / kRing) & 1);
+          for (uint32_t u = next[st] > kRing ? next[st] - kRing : 0; u < next[st]; ++u)
+            mbar_wait(full_bar(st, u), (u / kRing) & 1);
     } else if (C::QUANT && warp >= C::CODE_WARP) {
       // ---------------------------------------------------------------- codes to bf16 tiles
       const int st = (warp - C::CODE_WARP) / C::RESTORERS, w = (warp - C::CODE_WARP) % C::RESTORERS;
-      const uint32_t all = 2 * ring_order(st).n;
-      for (uint32_t k = 0; ok && k < all; ++k) {
-        ok = mbar_wait(raw_full(st, k), raw_parity(k)) && mbar_wait(kv_empty(st, k), kv_parity(k) ^ 1);
+      const uint32_t all = 2 * C::SPLIT * ring_order(st).n;
+      for (uint32_t u = 0; ok && u < all; ++u) {
+        const uint32_t k = u / C::SPLIT, part = u % C::SPLIT;
+        ok = mbar_wait(raw_full(st, u), raw_parity(u)) &&
+             (part > 0 || mbar_wait(kv_empty(st, k), kv_parity(k) ^ 1));
         if (!ok) break;
-        restore_tile<C::KIND, C::RESTORERS>(sm + C::RAW_RING + raw_stage(st, k) * C::RAW_TILE,
-                                            sm + C::RING + kv_stage(st, k) * C::TILE, w, lane);
+        restore_tile<C::KIND, kKeys / C::SPLIT, C::RESTORERS>(
+            sm + C::RAW_RING + raw_stage(st, u) * C::RAW_TILE,
+            sm + C::RING + kv_stage(st, k) * C::TILE + part * (kKeys / C::SPLIT * 128), w, lane);
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(raw_empty(st, k));
+          mbar_arrive(raw_empty(st, u));
           mbar_arrive(kv_full(st, k));
         }
       }
