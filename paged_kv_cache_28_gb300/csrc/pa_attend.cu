@@ -589,8 +589,8 @@ struct AttendCfg {
   static constexpr int RAW_RING = RING + STAGES * TILE;
   static constexpr int SMEM = RAW_RING + (QUANT ? RAW * RAW_TILE : 0) + 1024;
   // Warps 0-7 softmax.  Then the products (a warp for each row tile, so that one's waits are
-  // filled by the other's products), the pieces, the loads and, for code pools, eight that restore
-  // codes.  XX threads start with 128 registers, dealt anew
+  // filled by the other's products), the pieces and the loads (separate form: both, of a stream
+  // each) and, for code pools, eight that restore codes.  XX threads start with 128 registers, dealt anew
   // by groups of four warps as 256 x 184 + 256 x 72: a softmax thread holds its row's 128 scores.
   static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr int MMA_WARP = 8, PIECE_WARP = 10, LOAD_WARP = 11;
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     for (int st = 0; st < C::STREAMS; ++st)
       for (int k = 0; k < C::PIECES; ++k) {
         mbar_init(pc_full(st, k), 1);
-        mbar_init(pc_empty(st, k), 1 + (C::SHARED ? 2 + 8 : 1 + 4));   // every reader
+        mbar_init(pc_empty(st, k), C::SHARED ? 1 + 2 + 8 : 1 + 4);     // every reader
       }
     if constexpr (C::QUANT) {
       for (int i = 0; i < C::RAW; ++i) {
@@ -1045,108 +1045,80 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       for (uint32_t k = q_used > 0 ? q_used - 1 : 0; k < q_loads; ++k) mbar_wait(q_full(t), k & 1);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OTHER_REGS));
-    if (warp == C::PIECE_WARP) {
-      // ---------------------------------------------------------------- the pieces of the streams
-      // this stream's walker and, in the separate form, the other's; they change places
-      Walker walk = places[0], other = places[C::STREAMS - 1];
-      int4 cut = make_int4(0, 0, 0, 0), other_cut = cut;
-      uint32_t known = 0, other_known = 0;               // pieces published
-      bool over = false, other_over = C::STREAMS == 1;
-      auto swap_streams = [&] {
-        if constexpr (C::STREAMS == 2) {
-          const Walker w = walk;
-          walk = other;
-          other = w;
-          const int4 c4 = cut;
-          cut = other_cut;
-          other_cut = c4;
-          const uint32_t n = known;
-          known = other_known;
-          other_known = n;
-          const bool o = over;
-          over = other_over;
-          other_over = o;
-        }
-      };
-      int st = 0;
-      uint32_t idle = 0;
+    // make a piece known to its stream's readers
+    auto publish = [&](int st, uint32_t k, const Piece &x) {
+      ok = ok && mbar_wait(pc_empty(st, k), pc_parity(k) ^ 1);
+      if (ok && lane == 0) {
+        pieces[st][k % C::PIECES] = x;
+        mbar_arrive(pc_full(st, k));
+      }
+    };
+    auto cut_after = [&](const Piece &x, int rest) {
+      return make_int4(x.row, x.ntok, x.h, (rest - 1) / segment_width + 1);
+    };
+    if (C::SHARED && warp == C::PIECE_WARP) {
+      // ---------------------------------------------------------------- the pieces of the stream
+      Walker walk = places[0];
+      int4 cut = make_int4(0, 0, 0, 0);
+      bool more = true;
 #pragma unroll 1
-      while (!(over && other_over)) {
-        if (!over) {
-          // the shared form may wait for room; the separate one looks at its streams in turn (the
-          // readers of one may need the other's next piece), and sleeps rather than take issue slots
-          // from the softmax
-          const bool room = C::STREAMS == 1
-                                ? mbar_wait(pc_empty(st, known), pc_parity(known) ^ 1)
-                                : mbar_test(pc_empty(st, known), pc_parity(known) ^ 1);
-          if (room) {
-            idle = 0;
-            Piece x;
-            int rest = 0;
-            over = !walk.next(p, S, x, rest);
-            if (lane == 0) {
-              pieces[st][known % C::PIECES] = x;
-              mbar_arrive(pc_full(st, known));
-            }
-            ++known;
-            if (!over && x.starts && !x.ends)
-              cut = make_int4(x.row, x.ntok, x.h, (rest - 1) / segment_width + 1);
-          } else if (C::STREAMS == 1 || ++idle > kWaitSpins / 16) {
-            ok = false;
-            break;
-          } else {
-            __nanosleep(200);
-          }
-        }
-        if (C::STREAMS == 2) {
-          swap_streams();
-          st ^= 1;
-        }
+      for (uint32_t k = 0; more && ok; ++k) {
+        Piece x;
+        int rest = 0;
+        more = walk.next(p, S, x, rest);
+        publish(0, k, x);
+        if (more && x.starts && !x.ends) cut = cut_after(x, rest);
       }
-      if (lane == 0) {
-        p.cut[blockIdx.x * C::STREAMS + st] = cut;
-        if (C::STREAMS == 2) p.cut[blockIdx.x * C::STREAMS + (st ^ 1)] = other_cut;
-      }
-    } else if (warp == C::LOAD_WARP) {
-      // ---------------------------------------------------------------- K and V tiles
+      if (lane == 0) p.cut[blockIdx.x] = cut;
+    } else if (warp == C::LOAD_WARP || (!C::SHARED && warp == C::PIECE_WARP)) {
+      // ---------------------------------------------------------------- K and V tiles of a stream
+      // (separate form: this warp walks its stream's pieces, too)
+      const int st = C::SHARED ? 0 : warp - C::PIECE_WARP;
       // One box per 16 tokens (a page of a tile) and, in bf16 pools, 64 columns.
       constexpr int kBox = C::QUANT ? 16 * C::CODE_ROW : 16 * 128;
-      constexpr int kRing = C::QUANT ? C::RAW_PER : C::PER;
+      constexpr int kRing = C::QUANT ? C::RAW_PER : C::PER, kPages = 8 / C::SPLIT;
       const int outside = p.nblocks * p.bs;              // a row past the pool reads zeros
+      Walker walk;
+      int4 cut = make_int4(0, 0, 0, 0);
+      if (!C::SHARED) walk = places[st];
+      Piece x;
+      x.n = 0;
+      int at = 0;                                        // tiles of x that are fetched
+      uint32_t seen = 0;
+      bool over = false;
+      auto next_piece = [&] {
+        if constexpr (C::SHARED) {
+          return read_piece(st, seen++, x);
+        } else {
+          int rest = 0;
+          const bool more = walk.next(p, S, x, rest);
+          publish(st, seen++, x);
+          if (more && x.starts && !x.ends) cut = cut_after(x, rest);
+          return more && ok;
+        }
+      };
       // Block ids come four tiles (32 runs of 16 tokens, one per lane) at a time, two such chunks
       // ahead of the copies; scales one.
       struct Chunk {
-        int h, tile, n, L, lo;                           // n = 0: none
+        int h, tile, n;                                  // n = 0: none
         int row;                                         // this lane's first pool row; -1: unseen
         float ks, vs;
       };
-      struct Src {
-        Piece x;
-        int at;
-        uint32_t k;
-        bool over;
-        Chunk cur, nxt;
-        int i;
-      } src[C::STREAMS];
-      auto fetch_chunk = [&](int st) {
+      auto fetch_chunk = [&] {
         Chunk c{};
-        Src &z = src[st];
-        if (z.over) return c;
-        if (z.at == z.x.n) {
-          z.over = !read_piece(st, z.k++, z.x);
-          z.at = 0;
-          if (z.over) return c;
+        if (!over && at == x.n) {
+          over = !next_piece();
+          at = 0;
         }
-        c.h = z.x.h;
-        c.tile = z.x.tile + z.at;
-        c.n = min(4, z.x.n - z.at);
-        z.at += c.n;
-        c.L = z.x.L;
-        c.lo = z.x.lo;
+        if (over) return c;
+        c.h = x.h;
+        c.tile = x.tile + at;
+        c.n = min(4, x.n - at);
+        at += c.n;
         c.row = -1;
         const int g = c.tile * kKeys + 16 * lane;
-        if (g < c.L && g + 16 > c.lo && lane < 8 * c.n)
-          c.row = p.block_tables[static_cast<int64_t>(z.x.seq) * p.max_blocks + g / p.bs] & 0x7fffffff;
+        if (g < x.L && g + 16 > x.lo && lane < 8 * c.n)
+          c.row = p.block_tables[static_cast<int64_t>(x.seq) * p.max_blocks + g / p.bs] & 0x7fffffff;
         return c;
       };
       // block id to pool row (and the scales on their way), when it has come
@@ -1166,110 +1138,75 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       };
-      // tile (or part of a tile) u of this warp's ring
-      auto full_bar = [&](int st, uint32_t u) { return C::QUANT ? raw_full(st, u) : kv_full(st, u); };
-      auto room_bar = [&](int st, uint32_t u) { return C::QUANT ? raw_empty(st, u) : kv_empty(st, u); };
-      // rows: the pages' first pool rows, in every lane (-1: unseen); pages [first, first + kPages)
-      constexpr int kPages = 8 / C::SPLIT;
-      auto issue = [&](const CUtensorMap *map, int st, uint32_t u, int h, const int (&rows)[8], int first,
-                       bool zeros) {
-        const uint32_t full = full_bar(st, u);
-        if (elect_one()) {
-          uint32_t boxes = 0;
-#pragma unroll
-          for (int page = 0; page < 8; ++page)
-            boxes += page - first >= 0 && page - first < kPages && (rows[page] >= 0 || zeros);
-          mbar_arrive_expect_tx(full, boxes * kBox * (C::QUANT ? 1 : C::HALVES));
-          const uint32_t dst = C::QUANT ? sm + C::RAW_RING + raw_stage(st, u) * C::RAW_TILE
-                                        : sm + C::RING + kv_stage(st, u) * C::TILE;
-#pragma unroll
-          for (int page = 0; page < 8; ++page) {
-            if (page < first || page >= first + kPages || (rows[page] < 0 && !zeros)) continue;
-            const int row = rows[page] < 0 ? outside : rows[page];
+      // tile (or part of a tile) u of the ring that this warp fills
+      auto full_bar = [&](uint32_t u) { return C::QUANT ? raw_full(st, u) : kv_full(st, u); };
+      const uint32_t all = 2 * C::SPLIT * ring_order(st).n;
+      Chunk cur = fetch_chunk(), nxt = fetch_chunk();
+      resolve(cur);
+      int next = 0, here = 0;                            // the chunk's next tile, and the one at hand
+      uint32_t tiles = 0, u = 0;
+#pragma unroll 1
+      for (; ok && u < all; ++u) {
+        const uint32_t k = u / C::SPLIT;
+        const int first = static_cast<int>(u % C::SPLIT) * kPages;
+        ok = mbar_wait(C::QUANT ? raw_empty(st, u) : kv_empty(st, u), ((u / kRing) & 1) ^ 1);
+        if (!ok) break;
+        const bool v = k & 1;
+        if (!v && first == 0) {
+          if (next == cur.n) {
+            cur = nxt;
+            resolve(cur);
+            nxt = fetch_chunk();
+            next = 0;
+            if (!ok) break;
+          }
+          here = next++;
+          if constexpr (C::QUANT) {
+            float *sc = reinterpret_cast<float *>(scales[st][tiles % C::SCALES]);
+            if ((lane >> 3) == here) {
+              // c times K's scale and log2 of V's, both kept above zero: a zero scale's codes add
+              // nothing, and -inf stays -inf
+              sc[lane & 7] = fmaxf(cur.ks * p.c, 1e-30f);
+              sc[8 + (lane & 7)] = __log2f(fmaxf(cur.vs, 1e-30f));
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sc_full(st, tiles));
+            ++tiles;
+          }
+        }
+        // pages of V that no token sees read zeros (bf16): a weight of 0 times what lies there must
+        // be 0; codes are never infinite or NaN once restored
+        const bool zeros = !C::QUANT && v;
+        const uint32_t seen_pages =
+            (__ballot_sync(0xffffffffu, cur.row >= 0 || zeros) >> (8 * here + first)) & ((1u << kPages) - 1u);
+        const bool leader = elect_one();
+        const uint32_t full = full_bar(u);
+        if (leader)
+          mbar_arrive_expect_tx(full, __popc(seen_pages) * kBox * (C::QUANT ? 1 : C::HALVES));
+        const CUtensorMap *map = v ? &tmV : &tmK;
+        const uint32_t dst = C::QUANT ? sm + C::RAW_RING + raw_stage(st, u) * C::RAW_TILE
+                                      : sm + C::RING + kv_stage(st, u) * C::TILE;
+        const int column = cur.h * (C::QUANT ? C::CODE_ROW : C::D);
+#pragma unroll 4
+        for (int page = 0; page < kPages; ++page) {
+          int row = __shfl_sync(0xffffffffu, cur.row, 8 * here + first + page);
+          if (!(seen_pages >> page & 1)) continue;
+          if (row < 0) row = outside;
+          if (leader) {
 #pragma unroll
             for (int half = 0; half < (C::QUANT ? 1 : C::HALVES); ++half)
-              tma_load_2d(dst + half * (kKeys * 128) + (page - first) * kBox, map,
-                          h * (C::QUANT ? C::CODE_ROW : C::D) + half * 64, row, full);
+              tma_load_2d(dst + half * (kKeys * 128) + page * kBox, map, column + half * 64, row, full);
           }
         }
         __syncwarp();
-      };
-      int head[C::STREAMS] = {}, rows[C::STREAMS][8] = {};
-      uint32_t next[C::STREAMS] = {}, all[C::STREAMS];   // tiles (parts) issued, and in all
-      uint32_t tiles[C::STREAMS] = {};
-#pragma unroll
-      for (int st = 0; st < C::STREAMS; ++st) {
-        all[st] = 2 * C::SPLIT * ring_order(st).n;
-        Src &z = src[st];
-        z.x.n = z.at = z.i = 0;
-        z.k = 0;
-        z.over = false;
-        z.cur = fetch_chunk(st);
-        z.nxt = fetch_chunk(st);
-        resolve(z.cur);
       }
-      auto next_tile = [&](int st, int &h, int (&to)[8]) {
-        Src &z = src[st];
-        if (z.i == z.cur.n) {
-          z.cur = z.nxt;
-          resolve(z.cur);
-          z.nxt = fetch_chunk(st);
-          z.i = 0;
-        }
-        h = z.cur.h;
-#pragma unroll
-        for (int page = 0; page < 8; ++page)
-          to[page] = __shfl_sync(0xffffffffu, z.cur.row, z.i * 8 + page);
-        if constexpr (C::QUANT) {
-          const uint32_t n = tiles[st]++;
-          float *sc = reinterpret_cast<float *>(scales[st][n % C::SCALES]);
-          if ((lane >> 3) == z.i) {
-            // c times K's scale and log2 of V's, both kept above zero: a zero scale's codes add
-            // nothing, and -inf stays -inf
-            sc[lane & 7] = fmaxf(z.cur.ks * p.c, 1e-30f);
-            sc[8 + (lane & 7)] = __log2f(fmaxf(z.cur.vs, 1e-30f));
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sc_full(st, n));
-        }
-        ++z.i;
-      };
-      uint32_t idle = 0;
-      for (bool more = true; more && ok;) {
-        more = false;
-#pragma unroll
-        for (int st = 0; st < C::STREAMS; ++st) {
-          const uint32_t u = next[st], k = u / C::SPLIT;
-          const int first = static_cast<int>(u % C::SPLIT) * kPages;
-          if (!ok || u == all[st]) continue;
-          more = true;
-          // one stream: wait for room; two: see which has some
-          const uint32_t parity = ((u / kRing) & 1) ^ 1;
-          if (C::STREAMS == 1) {
-            ok = mbar_wait(room_bar(st, u), parity);
-          } else if (!mbar_test(room_bar(st, u), parity)) {
-            ok = ++idle < 4 * kWaitSpins;
-            continue;
-          }
-          if (!ok) break;
-          idle = 0;
-          if (k & 1) {
-            // pages of V that no token sees read zeros (bf16): a weight of 0 times what lies there
-            // must be 0; codes are never infinite or NaN once restored
-            issue(&tmV, st, u, head[st], rows[st], first, !C::QUANT);
-          } else {
-            if (first == 0) next_tile(st, head[st], rows[st]);
-            if (!ok) break;
-            issue(&tmK, st, u, head[st], rows[st], first, false);
-          }
-          next[st] = u + 1;
-        }
+      if (!C::SHARED) {
+        while (ok && !over) fetch_chunk();               // the end mark
+        if (lane == 0) p.cut[2 * blockIdx.x + st] = cut;
       }
       // after a wait that gave up, the copies in flight must have landed before the CTA's memory goes
       if (!ok)
-        for (int st = 0; st < C::STREAMS; ++st)
-          for (uint32_t u = next[st] > kRing ? next[st] - kRing : 0; u < next[st]; ++u)
-            mbar_wait(full_bar(st, u), (u / kRing) & 1);
+        for (uint32_t i = u > kRing ? u - kRing : 0; i < u; ++i) mbar_wait(full_bar(i), (i / kRing) & 1);
     } else if (C::QUANT && warp >= C::CODE_WARP) {
       // ---------------------------------------------------------------- codes to bf16 tiles
       const int st = (warp - C::CODE_WARP) / C::RESTORERS, w = (warp - C::CODE_WARP) % C::RESTORERS;
