@@ -8,6 +8,7 @@ present: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -308,6 +309,11 @@ def pa_quest_select(shape: pa_shape, q, key_summaries, block_tables, seq_lens, t
         int(topk), _ptr(page_scores), _ptr(selected_pages), _ptr(err_flag), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=256)
+def _rope(rotary_dim, interleaved, num_positions, q_stride, k_stride, v_stride) -> pa_rope:
+    return pa_rope(rotary_dim, interleaved, num_positions, q_stride, k_stride, v_stride)
+
+
 def pa_rope_and_cache(shape: pa_shape, cos_sin, positions, q_out, q, k_new, v_new, k_pool, v_pool,
                       k_scale, v_scale, slot_mapping, err_flag=None, stream=None,
                       interleaved: bool = False) -> None:
@@ -316,7 +322,7 @@ def pa_rope_and_cache(shape: pa_shape, cos_sin, positions, q_out, q, k_new, v_ne
     lib = load()
     (qp, qs), (kp, ks), (vp, vs) = _token_ptr(q), _token_ptr(k_new), _token_ptr(v_new)
     rows, width = cos_sin.shape
-    rope = pa_rope(int(width), int(bool(interleaved)), int(rows), qs, ks, vs)
+    rope = _rope(width, bool(interleaved), rows, qs, ks, vs)
     _check("pa_rope_and_cache", lib.pa_rope_and_cache(
         ctypes.byref(shape), ctypes.byref(rope), _ptr(cos_sin), _ptr(positions), _ptr(q_out), qp,
         kp, vp, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
