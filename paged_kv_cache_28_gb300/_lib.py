@@ -138,15 +138,17 @@ def status_string(status: int) -> str:
 
 def _ptr(t):
     """Device pointer of a CUDA tensor (None -> NULL).  Plain ints pass through."""
-    if t is None or t.__class__ is int:
-        return t
-    if isinstance(t, int):
-        return t
-    if not t.is_cuda:
-        raise ValueError("libpa takes CUDA tensors only")
-    if not t.is_contiguous():
-        raise ValueError("libpa takes contiguous tensors only")
-    return t.data_ptr()
+    if t is None:
+        return None
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
+    raise ValueError("libpa takes contiguous tensors only" if t.is_cuda else
+                     "libpa takes CUDA tensors only")
 
 
 def _token_ptr(t):
@@ -171,9 +173,10 @@ def _find_current_stream():
     one: building a torch.cuda.Stream costs as much as the launch (6 of 16 us of a small call)."""
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None:
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
         return lambda: torch.cuda.current_stream().cuda_stream
-    device = torch.cuda.current_device
+    torch.cuda.init()
     return lambda: raw(device())
 
 
