@@ -351,6 +351,98 @@ def test_device_errors():
         assert (out[7:] == -3).all()
 
 
+def test_output_and_queries_on_a_16_byte_boundary():
+    """16-byte aligned tensors, not 32: the narrow stores."""
+    for n, L in (([40, 3], [300, 5000]), ([300], [300])):
+        b = Batch(n, L, 2, 4, seed=25)
+        k = b.T * b.Hq * b.D
+        b.q = torch.cat([b.q.new_zeros(8), b.q.flatten()])[8:].view(b.q.shape)
+        out = torch.full((k + 8,), -3.0, dtype=torch.bfloat16, device="cuda")[8:].view(b.q.shape)
+        assert b.q.data_ptr() % 32 == 16 and out.data_ptr() % 32 == 16
+        b.check(b.run(out))
+        assert (out[sum(n):] == -3.0).all()
+
+
+def test_sequences_that_share_blocks():
+    b = Batch([5, 70, 1], [900, 900, 900], 2, 4, seed=26, causal=False)
+    b.block_tables[:] = b.block_tables[0]
+    b.check()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+@pytest.mark.parametrize("n", [[3, 1], [200]])
+def test_zero_scales_restore_to_zero(kind, n):
+    """A block whose scale is 0 scores 0 and adds nothing, whatever its codes are."""
+    b = Batch(n, [600] * len(n), 2, 4, kind=kind, seed=27)
+    b.k_scale[::3] = 0
+    b.v_scale[::2] = 0
+    b.check()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+def test_scales_over_six_decades(kind):
+    """Pages with large V scales among small ones; scores stay within a few units."""
+    b = Batch([40, 5], [700, 900], 2, 4, kind=kind, seed=28)
+    g = torch.Generator(device="cuda").manual_seed(28)
+    b.v_scale *= 10.0 ** torch.randint(-3, 4, b.v_scale.shape, generator=g, device="cuda")
+    b.check()
+
+
+def test_the_most_kv_heads():
+    Batch([3, 1], [40, 300], 2048, 1, 64, seed=29).check()
+
+
+@pytest.mark.parametrize("most", [3, 200])
+def test_thousands_of_sequences(most):
+    """More than 32 groups of 32 sequences: the places of the segments are found in two steps."""
+    r = np.random.default_rng(30)
+    n = [int(x) for x in r.integers(0, most, 2500)]
+    counting(Batch(n, [a + int(x) for a, x in zip(n, r.integers(1, 60, 2500))], 1, 4, 64, seed=30))
+
+
+def test_rows_past_4_gib_of_a_pool():
+    """Blocks at the end of a 5 GB pool, written by pa_rope_and_cache and read by pa_extend."""
+    b = Batch([50, 2], [400, 90], 8, 2, seed=31)
+    blocks = 5 * 2 ** 30 // (16 * 8 * 128 * 2)
+    far = torch.arange(blocks - b.nblocks, blocks, device="cuda", dtype=torch.int32)
+    pools = []
+    for x in (b.k, b.v):
+        pool = torch.empty(blocks, 16, 8, 128, dtype=torch.bfloat16, device="cuda")
+        pool[far.long()] = x
+        pools.append(pool)
+    want = b.run().clone()
+    b.block_tables = torch.where(b.block_tables >= 0, far[b.block_tables.clamp(min=0).long()], -7)
+    b.k, b.v = pools
+    b.shape = pa.make_shape(b.B, b.Hq, 8, 128, 16, blocks, b.max_blocks, KINDS["bf16"])
+    assert torch.equal(b.run(), want)
+    a = Append(20, 8, 8, nblocks=8, seed=31)
+    small = [x.clone() for x in a.pools]
+    a.run()
+    lift = torch.where(a.slots >= 0, a.slots + (blocks - 8) * 16, -1)
+    for pool, x in zip(pools, small):
+        pool[-8:] = x
+    pa.pa_rope_and_cache(pa.make_shape(20, 8, 8, 128, 16, blocks, 1, KINDS["bf16"]), a.cos_sin, a.pos, a.q_out, a.q,
+                         a.k, a.v, *pools, None, None, lift, a.err)
+    for pool, x in zip(pools, a.pools):
+        assert torch.equal(pool[-8:], x)
+    assert pa.pa_read_error_flag(a.err) == 0
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    r = np.random.default_rng(100 + seed)
+    kind = ["bf16", "fp8", "int4"][seed % 3]
+    D = 128 if kind != "bf16" or seed % 2 else 64
+    B = int(r.integers(1, 9))
+    top = int(r.choice([6, 60, 400]))
+    n = [int(x) for x in r.integers(0, top, B)]
+    L = [a + int(x) for a, x in zip(n, r.integers(0, 1500, B))]
+    causal = bool(r.integers(0, 3))
+    window = int(r.choice([0, 0, 1, 50, 700, 2 ** 31 - 1])) if causal else 0
+    Batch(n, L if causal else L[::-1], int(r.choice([1, 2, 5])), int(r.choice([1, 2, 3, 4, 6, 7, 8, 12, 16])), D,
+          int(r.choice([16, 32])), kind, window=window, causal=causal, seed=seed).check()
+
+
 def test_refuses_a_short_workspace():
     b = Batch([4], [20], 1, 2, seed=17)
     b.ws = b.ws[:-256]
