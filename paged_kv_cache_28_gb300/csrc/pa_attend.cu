@@ -1000,40 +1000,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       o_phase ^= 1;
       tc_fence_after();
       if (warp_live) {
-        if (x.starts && x.ends) {
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-          uint16_t *dst = p.out + (static_cast<int64_t>(x.row + tok0 + my_tok) * p.Hq +
-                                   x.h * p.G + (row - my_tok * p.G)) * C::D;
+        const bool whole = x.starts && x.ends;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint16_t *dst = p.out + (static_cast<int64_t>(x.row + tok0 + my_tok) * p.Hq + x.h * p.G +
+                                 (row - my_tok * p.G)) * C::D;
+        const int64_t r = (2 * static_cast<int64_t>(blockIdx.x * C::STREAMS + st) + x.starts) * p.rows +
+                          (C::SHARED ? t * kRows : 0) + row;
+        float *part = p.part_o + r * C::D;
+        if (!whole && live) p.part_ml[r] = make_float2(m, l);
+        constexpr int kCols = C::QUANT ? 64 : C::D;      // columns on their way at once
 #pragma unroll
-          for (int j = 0; j < C::D; j += 32) {
-            uint32_t o[32];
-            tc_ld32(o, tO + j);
-            tc_wait_ld32(o);
-            uint32_t v[16];
+        for (int j0 = 0; j0 < C::D; j0 += kCols) {
+          uint32_t o[kCols];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              v[e] = l > 0.f ? pack_bf16(__uint_as_float(o[2 * e]) * inv,
-                                         __uint_as_float(o[2 * e + 1]) * inv)
+          for (int j = 0; j < kCols; j += 32) tc_ld32(o + j, tO + j0 + j);
+          tc_wait_ld32(o);
+#pragma unroll
+          for (int j = 32; j < kCols; j += 32) tc_use32(o + j);
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < kCols / 2; ++e)
+              o[e] = l > 0.f ? pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
                              : 0u;
             if (live) {
-              store32(dst + j, v, p.wide);
-              store32(dst + j + 16, v + 8, p.wide);
-            }
-          }
-        } else {
-          const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x * C::STREAMS + st) + x.starts;
-          const int64_t r = slot * p.rows + (C::SHARED ? t * kRows : 0) + row;
-          if (live) p.part_ml[r] = make_float2(m, l);
-          float *dst = p.part_o + r * C::D;
 #pragma unroll
-          for (int j = 0; j < C::D; j += 32) {
-            uint32_t o[32];
-            tc_ld32(o, tO + j);
-            tc_wait_ld32(o);
-            if (live) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) store32(dst + j + 8 * e, o + 8 * e, true);
+              for (int e = 0; e < kCols / 16; ++e) store32(dst + j0 + 16 * e, o + 8 * e, p.wide);
             }
+          } else if (live) {
+#pragma unroll
+            for (int e = 0; e < kCols / 8; ++e) store32(part + j0 + 8 * e, o + 8 * e, true);
           }
         }
       }
@@ -1502,7 +1497,7 @@ pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t 
   p.causal = causal;
   p.tok = plan.tok;
   p.workers = plan.workers;
-  p.unit_cost = plan.shared ? 2 : 2;
+  p.unit_cost = plan.shared ? 2 : 1;
   p.over_workers = ~uint64_t(0) / plan.workers + 1;       // exact for totals below 2^55
   p.rows = plan.rows;
   // c > 0 keeps a masked score's c s at -inf; 1e-30 scores every key alike, as 0 does

@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
                               threadIdx.x == 0 && blockIdx.y == 0);
 }
 
-// Quantised pools (D = 128).  `cache_ctas` CTAs write the cache, `tokens` tokens each; as in
+// Quantised pools (D = 128).  `cache_ctas` CTAs write the cache, a share of `tokens` tokens each; as in
 // pa_reshape_and_cache, the first token of the call in a block (its leader) stands for every
 // token of the call in that block, applied in token order.  A warp takes (KV head, K or V) jobs,
 // a lane four consecutive channels.  The codes of a job's rows stay in shared memory while its
@@ -196,7 +196,8 @@ __global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
 // divides: the two differ by one unit in the last place at most); codes are x / scale, rounded,
 // in both.
 template <class Codec, bool kInterleaved>
-__global__ void __launch_bounds__(256, 4) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens) {
+__global__ void __launch_bounds__(256, 4) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens,
+                                                            int shares) {
   using Word = typename Codec::Word;
   constexpr int D = 128, kWarps = 8, kBatch = 8;
   extern __shared__ uint32_t smem[];                     // [kWarps][bs][32] words: a job's rows
@@ -209,12 +210,13 @@ __global__ void __launch_bounds__(256, 4) rope_quant_kernel(const RopeParams p, 
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the two kinds of CTA alternate, so that the writers' arithmetic runs beside the queries' traffic
-  const int period = gridDim.x / cache_ctas, nth = blockIdx.x / period;
-  if (blockIdx.x % period != 0 || nth >= cache_ctas) {
-    const int t = blockIdx.x - min(nth + 1, cache_ctas);
+  const int period = gridDim.x / cache_ctas, writer = blockIdx.x / period;
+  if (blockIdx.x % period != 0 || writer >= cache_ctas) {
+    const int t = blockIdx.x - min(writer + 1, cache_ctas);
     rope_queries<kInterleaved>(p, t, tid % 8, tid / 8, 32);
     return;
   }
+  const int nth = writer / shares, share = writer % shares;
   Word *codes = reinterpret_cast<Word *>(smem) + warp * p.bs * 32 + lane;    // row r: codes[32 r]
   for (int t = nth * tokens; t < min(p.T, (nth + 1) * tokens); ++t) {
     const int64_t slot = p.slots[t];
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(256, 4) rope_quant_kernel(const RopeParams p, 
         if (atomicOr(&offsets_seen, 1u << off) & (1u << off)) set_err(p.err, PA_DEVERR_FP8_CONFLICT);
       }
       __syncthreads();
-      for (int job = warp; job < 2 * p.Hkv; job += kWarps) {
+      for (int job = share * kWarps + warp; job < 2 * p.Hkv; job += shares * kWarps) {
         const int h = job >> 1;
         const bool is_v = job & 1;
         uint8_t *pool = is_v ? p.v_pool : p.k_pool;
@@ -378,13 +380,15 @@ template <class Codec, bool I>
 cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
   // a prompt's tokens mostly leave at once, so a CTA looks at several; a batch's stay
   const int tokens = p.T >= 2048 ? 8 : 1;
-  const int cache_ctas = (p.T + tokens - 1) / tokens;
+  // few tokens: their jobs go over several CTAs, each of which finds its block's tokens
+  const int shares = p.T >= 1024 ? 1 : (2 * p.Hkv + 7) / 8;
+  const int cache_ctas = (p.T + tokens - 1) / tokens * shares;
   const size_t smem = 8 * 32 * sizeof(typename Codec::Word) * p.bs;
   const cudaError_t e = cudaFuncSetAttribute(rope_quant_kernel<Codec, I>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * 1024);
   if (e != cudaSuccess) return e;
   return launch_pdl(rope_quant_kernel<Codec, I>, dim3(cache_ctas + (p.q ? p.T : 0)), dim3(256), smem,
-                    stream, p, cache_ctas, tokens);
+                    stream, p, cache_ctas, tokens, shares);
 }
 
 }  // namespace
