@@ -1008,27 +1008,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                           (C::SHARED ? t * kRows : 0) + row;
         float *part = p.part_o + r * C::D;
         if (!whole && live) p.part_ml[r] = make_float2(m, l);
-        constexpr int kCols = C::QUANT ? 64 : C::D;      // columns on their way at once
 #pragma unroll
-        for (int j0 = 0; j0 < C::D; j0 += kCols) {
-          uint32_t o[kCols];
-#pragma unroll
-          for (int j = 0; j < kCols; j += 32) tc_ld32(o + j, tO + j0 + j);
+        for (int j = 0; j < C::D; j += 32) {
+          uint32_t o[32];
+          tc_ld32(o, tO + j);
           tc_wait_ld32(o);
-#pragma unroll
-          for (int j = 32; j < kCols; j += 32) tc_use32(o + j);
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < kCols / 2; ++e)
+            for (int e = 0; e < 16; ++e)
               o[e] = l > 0.f ? pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
                              : 0u;
             if (live) {
-#pragma unroll
-              for (int e = 0; e < kCols / 16; ++e) store32(dst + j0 + 16 * e, o + 8 * e, p.wide);
+              store32(dst + j, o, p.wide);
+              store32(dst + j + 16, o + 8, p.wide);
             }
           } else if (live) {
 #pragma unroll
-            for (int e = 0; e < kCols / 8; ++e) store32(part + j0 + 8 * e, o + 8 * e, true);
+            for (int e = 0; e < 4; ++e) store32(part + j + 8 * e, o + 8 * e, true);
           }
         }
       }
