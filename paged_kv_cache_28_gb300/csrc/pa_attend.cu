@@ -1355,66 +1355,73 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 // Joins the pieces of the unit that worker blockIdx.x left unfinished: its own (the unit's
 // first keys), then those that the next workers began with, in key order.
 //     out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,   M = max_i m_i
+// One warp per row; bound by the latency of its loads, so the first pieces' O are on their way
+// before their weights are known, and eight are at a time.
 template <int D>
 __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p) {
-
   pdl_trigger();
   pdl_wait();
   const int4 cut = p.cut[blockIdx.x];
   if (cut.w == 0) return;
+  constexpr int E = D / 32, kBatch = 8;                  // channels per lane
   const int lane = threadIdx.x & 31;
-  constexpr int E = D / 32;                              // channels per lane
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < p.rows; r += gridDim.y * 8) {
-    const int t = r / kRows, rr = r - t * kRows;
-    const int in_tile = rr / p.G, tok = t * p.tok + in_tile;
-    if (in_tile >= p.tok || tok >= cut.y) continue;
-    auto slot = [&](int i) {
-      const int64_t s = i == 0 ? 2 * static_cast<int64_t>(blockIdx.x) + 1
-                               : 2 * (static_cast<int64_t>(blockIdx.x) + i);
-      return s * p.rows + r;
-    };
-    float M = -INFINITY;
-    for (int i = lane; i <= cut.w; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int t = r / kRows, rr = r - t * kRows;
+  const int in_tile = rr / p.G, tok = t * p.tok + in_tile;
+  if (r >= p.rows || in_tile >= p.tok || tok >= cut.y) return;
+  const int n = cut.w + 1;
+  auto slot = [&](int i) {
+    const int64_t s = i == 0 ? 2 * static_cast<int64_t>(blockIdx.x) + 1
+                             : 2 * (static_cast<int64_t>(blockIdx.x) + i);
+    return s * p.rows + r;
+  };
+  float v[kBatch][E];
+  auto load = [&](int i0) {
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    float l = 0.f, o[E] = {};
-    for (int i0 = 0; i0 <= cut.w; i0 += 32) {            // a piece per lane, then a lane's weight to all
-      float f = 0.f;
-      if (i0 + lane <= cut.w) {
-        const float2 ml = p.part_ml[slot(i0 + lane)];
-        if (ml.y > 0.f) f = ex2(ml.x - M);
-        l += f * ml.y;
-      }
-      const int n = min(32, cut.w + 1 - i0);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float g = __shfl_sync(0xffffffffu, f, i);
+    for (int i = 0; i < kBatch; ++i)
+      if (i0 + i < n) {
         const float *src = p.part_o + slot(i0 + i) * D + lane * E;
-        // a piece without seen keys has all weights zero, and so is its O
-        if constexpr (E == 4) {
-          const float4 v = *reinterpret_cast<const float4 *>(src);
-          o[0] += g * v.x;
-          o[1] += g * v.y;
-          o[2] += g * v.z;
-          o[3] += g * v.w;
-        } else {
-          const float2 v = *reinterpret_cast<const float2 *>(src);
-          o[0] += g * v.x;
-          o[1] += g * v.y;
+        if constexpr (E == 4)
+          *reinterpret_cast<float4 *>(v[i]) = *reinterpret_cast<const float4 *>(src);
+        else
+          *reinterpret_cast<float2 *>(v[i]) = *reinterpret_cast<const float2 *>(src);
+      }
+  };
+  load(0);
+  const float2 none = make_float2(-INFINITY, 0.f);
+  const float2 first = lane < n ? p.part_ml[slot(lane)] : none;
+  float M = first.x;
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, p.part_ml[slot(i)].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+  float l = 0.f, o[E] = {};
+  for (int i0 = 0; i0 < n; i0 += 32) {                   // a piece's weight per lane
+    const float2 ml = i0 == 0 ? first : i0 + lane < n ? p.part_ml[slot(i0 + lane)] : none;
+    // a piece without seen keys has only zero weights, and so is its O
+    const float f = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
+    l += f * ml.y;
+    for (int j = 0; j < 32 && i0 + j < n; j += kBatch) {
+      if (i0 + j > 0) load(i0 + j);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float g = __shfl_sync(0xffffffffu, f, j + i);
+        if (i0 + j + i < n) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += g * v[i][e];
         }
       }
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    uint16_t *dst = p.out + (static_cast<int64_t>(cut.x + tok) * p.Hq + cut.z * p.G +
-                             (rr - in_tile * p.G)) * D + lane * E;
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2 *>(dst) =
-          make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
-    else
-      *reinterpret_cast<uint32_t *>(dst) = pack_bf16(o[0] * inv, o[1] * inv);
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint16_t *dst = p.out + (static_cast<int64_t>(cut.x + tok) * p.Hq + cut.z * p.G + (rr - in_tile * p.G)) * D +
+                  lane * E;
+  if constexpr (E == 4)
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t *>(dst) = pack_bf16(o[0] * inv, o[1] * inv);
 }
 
 // ------------------------------------------------------------------ host side
