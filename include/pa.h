@@ -470,6 +470,7 @@ typedef struct {
  *   q [B, Hq, D], k_new and v_new [B, Hkv, D] bf16, heads dense, tokens `*_stride` apart;
  *   q_out [B, Hq, D] bf16, dense.  q_out may be q (dense) and must not overlap it otherwise.
  *     Both NULL: keys and values only.
+ * Two tokens with the same slot: as in pa_reshape_and_cache.
  * A token with a negative slot is padding: nothing of it is written, q_out neither.  A slot
  * beyond the pool sets PA_DEVERR_SLOT, a position outside the table PA_DEVERR_POSITION; such a
  * token is skipped like padding.
@@ -500,8 +501,10 @@ pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const fl
  * length beyond the block table is clamped, and a sequence with more query than cached tokens
  * gets zeros (PA_DEVERR_SEQ_LEN); a sequence whose offsets fall or leave the rows is skipped
  * (PA_DEVERR_QUERY).
- * Rounding: q K^T and the sums are fp32; the weights enter the second product as bf16.  The
- * result is the same on every call, bit for bit.  Batches of more than 16384 sequences return
+ * Rounding: q K^T, the softmax's maxima and sums and the output before its last rounding are
+ * fp32; the weights (times V's scale) enter the second product as bf16, 2^-8 of each at most.
+ * The scales of code pools are absmax scales, never negative.  The result is the same on every
+ * call, bit for bit.  Batches of more than 16384 sequences return
  * PA_ERR_UNSUPPORTED.
  */
 pa_status pa_extend(const pa_shape *shape, void *out, const void *q, const int32_t *query_offsets,

@@ -6,6 +6,7 @@
 #include <initializer_list>
 
 #include "pa.h"
+#include "pa_extend.h"
 #include "pa_internal.h"
 
 namespace {

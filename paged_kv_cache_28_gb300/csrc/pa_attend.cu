@@ -22,10 +22,32 @@
 //
 // One CTA per SM: Q, K and V tiles in 128-byte-swizzled shared memory (TMA, one box per 16
 // tokens of a page), S and O in TMEM (128 + D columns per row tile), P written over S as
-// bf16 and read from TMEM by the second product.
+// bf16 and read from TMEM by the second product.  Each role has its own warps (AttendCfg), and
+// they meet at mbarriers only.
+//
+// What bounds it (D = 128, measured on a GB300):
+//   Shared form: a 128 x 128 x 128 product takes the tensor core 512 cycles, so a key tile costs
+//   four of them, 2,048; a row tile's softmax takes 870 cycles alone (its 128 exponentials a row
+//   at 5.1 cycles a warp) and about 2,000 beside the other's and the products, which read and
+//   write the same TMEM.  A key tile takes about 3,300 cycles: the chain S -> softmax -> P V of
+//   each row tile, half of it behind the other's.  2,048 tokens after 15,952 cached ones, 64
+//   query and 8 KV heads: 0.80 ms, 1,425 TFLOP/s, 75 % of the measured cuBLAS peak.
+//   Separate form: the loads.  32 tokens after 257,000 cached ones: 0.178 ms, 5.9 TB/s, 87 %
+//   of the measured copy bandwidth.
+//   Code pools: restoring the codes takes issue slots and shared memory from the softmax; a
+//   windowed layer over 4-bit pages runs at 950 TFLOP/s.
+//
+// What made it fast, with the time of the 2,048-token chunk: one warp issuing both row tiles'
+// products, 981 us; a warp each, taking turns, 872; P announced at half of the keys instead of at
+// three quarters, 835; a piece left in shared memory instead of in the softmax's registers and
+// loads issued in a short loop, 800.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "pa_common.cuh"
+#include "pa_extend.h"
 #include "pa_internal.h"
 
 namespace pa {
@@ -590,8 +612,10 @@ struct AttendCfg {
   static constexpr int SMEM = RAW_RING + (QUANT ? RAW * RAW_TILE : 0) + 1024;
   // Warps 0-7 softmax.  Then the products (a warp for each row tile, so that one's waits are
   // filled by the other's products), the pieces and the loads (separate form: both, of a stream
-  // each) and, for code pools, eight that restore codes.  XX threads start with 128 registers, dealt anew
-  // by groups of four warps as 256 x 184 + 256 x 72: a softmax thread holds its row's 128 scores.
+  // each) and, for code pools, eight that restore codes.  Registers are dealt anew by groups of
+  // four warps: 384 threads start with 168, 64,512 in all = 256 x 216 + 128 x 72, and a softmax
+  // thread holds its row's 128 scores; 640 with 96, 61,440 = 256 x 144 + 384 x 64, and it reads
+  // half of them twice.
   static constexpr int THREADS = QUANT ? 640 : 384;
   static constexpr int MMA_WARP = 8, PIECE_WARP = 10, LOAD_WARP = 11;
   static constexpr int CODE_WARP = 12, CODE_WARPS = 8;  // code pools
@@ -1426,7 +1450,33 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p)
 
 // ------------------------------------------------------------------ host side
 
-// Separate key streams while a sequence has at most one row tile of tokens on average.
+// 3D TMA map of query rows [T, Hq, D] bf16: a box is `tok` tokens x the heads of one KV head x 64
+// columns, which land in shared memory as 128-byte swizzled rows (token, head).
+bool make_query_map(CUtensorMap *map, const void *q, const pa_shape &s, int T, int tok) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
+                                                     cudaEnableDefault, &found) == cudaSuccess &&
+                    found == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
+  }();
+  if (!encode) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.D), static_cast<cuuint64_t>(s.Hq),
+                              static_cast<cuuint64_t>(T)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.D) * 2,
+                                 static_cast<cuuint64_t>(s.Hq) * s.D * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(s.Hq / s.Hkv), static_cast<cuuint32_t>(tok)};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
+                steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Separate key streams while a sequence has at most one row tile of tokens on average.  Measured
+// on 8 sequences of 4,000 to 8,000 cached tokens, 64 query and 8 KV heads (16 tokens a row tile):
+// 24 tokens each 59 us shared against 83 separate, 40 tokens 95 against 110; below, the second row
+// tile of the shared form is empty.
 struct Plan {
   bool shared;
   int tok, workers, rows;
@@ -1452,6 +1502,16 @@ template <class C>
 pa_status launch(const AttendParams &p, const CUtensorMap &mq, const CUtensorMap &mk,
                  const CUtensorMap &mv, cudaStream_t stream) {
   auto kernel = attend_kernel<C>;
+  // the registers that the warps ask for must be those that the CTA was launched with: asking for
+  // more would wait for ever
+  static std::atomic<bool> fits{false};
+  if (!fits.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes a;
+    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return PA_ERR_CUDA;
+    if (a.numRegs * C::THREADS < 256 * C::SOFTMAX_REGS + (C::THREADS - 256) * C::OTHER_REGS)
+      return PA_ERR_UNSUPPORTED;
+    fits.store(true, std::memory_order_relaxed);
+  }
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
       cudaSuccess)
     return PA_ERR_CUDA;
@@ -1500,6 +1560,8 @@ pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t 
   p.causal = causal;
   p.tok = plan.tok;
   p.workers = plan.workers;
+  // four ragged prompts, shared form: 488, 449, 439, 444, 453 us with 0 to 4; verification of few
+  // tokens, separate form: 116, 121 and 127 us with 1 to 3
   p.unit_cost = plan.shared ? 2 : 1;
   p.over_workers = ~uint64_t(0) / plan.workers + 1;       // exact for totals below 2^55
   p.rows = plan.rows;

@@ -2297,21 +2297,6 @@ bool make_pool_map(CUtensorMap *map, const void *pool, const pa_shape &s, int he
   return r == CUDA_SUCCESS;
 }
 
-// 3D view of query rows [T, Hq, D] bf16: a box is `tok` tokens x the heads of one KV head x
-// 64 columns, which land in shared memory as 128-byte swizzled rows (token, head).
-bool make_query_map(CUtensorMap *map, const void *q, const pa_shape &s, int T, int tok) {
-  auto fn = encode_fn();
-  if (!fn) return false;
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.D), static_cast<cuuint64_t>(s.Hq),
-                        static_cast<cuuint64_t>(T)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.D) * 2, static_cast<cuuint64_t>(s.Hq) * s.D * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(s.Hq / s.Hkv), static_cast<cuuint32_t>(tok)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Opt the kernel in to the dynamic shared memory it needs (per call: cheap, and
 // correct whichever device is current).
 template <class K>

@@ -80,9 +80,6 @@ __host__ __device__ inline CascadeLayout cascade_layout(int B, int Hq, int D) {
 // `heads` adjacent KV heads): 16-token boxes of up to 128 bytes per unit row.
 bool make_pool_map(CUtensorMap *map, const void *pool, const pa_shape &s, int heads);
 
-// 3D TMA map of query rows [T, Hq, D] for boxes of `tok` tokens x one KV head's query heads.
-bool make_query_map(CUtensorMap *map, const void *q, const pa_shape &s, int T, int tok);
-
 // Cascade (shared-prefix) part of a split decode; arguments validated.  The plan
 // kernel writes the per-sequence cascade info and resets the work counter
 // (programmatic dependent launch on the caller's stream); each cascade launch (`ctas`
@@ -142,19 +139,5 @@ pa_status run_quest_select(const pa_shape &s, const void *q, const void *summari
                            const int32_t *block_tables, const int32_t *seq_lens, int topk,
                            float *page_scores, int32_t *selected, int32_t *err,
                            cudaStream_t stream);
-
-// pa_extend (causal) and pa_cross_attend; `sms`: SMs of the device, as the workspace was sized.
-size_t attend_workspace_bytes(const pa_shape &s, int T, int sms);
-pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t *offsets, int T,
-                     const void *k_pool, const void *v_pool, const float *k_scale,
-                     const float *v_scale, const int32_t *bt, const int32_t *sl, bool causal,
-                     int window, float sm_scale, void *workspace, int sms, int32_t *err,
-                     cudaStream_t stream);
-
-pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const float *cos_sin,
-                             const int32_t *positions, void *q_out, const void *q,
-                             const void *k_new, const void *v_new, void *k_pool, void *v_pool,
-                             float *k_scale, float *v_scale, const int64_t *slot_mapping,
-                             int32_t *err, cudaStream_t stream);
 
 }  // namespace pa

@@ -8,12 +8,18 @@
 // of the written formula), rounded once to bf16.  The rotated keys and the values then go to
 // the cache as pa_reshape_and_cache writes them.
 //
-// Nothing here is reused but the table row of a token, so the kernels are bound by HBM: each
-// vector is read once and written once.
+// Nothing here is reused but the table row of a token, so the bf16 kernel is bound by HBM: each
+// vector is read once and written once.  16,384 tokens of 64 query and 8 KV heads take 112 us, 90 %
+// of the measured copy bandwidth (119 us before the first vectors' loads went ahead of the token's
+// slot and angles).  The quantised writer is bound by its instructions, above all the codes'
+// quotients and what a raised scale encodes anew: 9,485 tokens into an E4M3 cache take 118 us, 47 %.
+// 261 us -> 155 with quotients by the reciprocal and the block index by a shift, 118 with the
+// tokens of a job in a loop and the writers' CTAs among the queries'.
 #include <algorithm>
 
 #include "pa_codec.cuh"
 #include "pa_common.cuh"
+#include "pa_extend.h"
 #include "pa_internal.h"
 
 namespace pa {
