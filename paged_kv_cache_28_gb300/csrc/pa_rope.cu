@@ -9,7 +9,7 @@
 // the cache as pa_reshape_and_cache writes them.
 //
 // Nothing here is reused but the table row of a token, so the bf16 kernel is bound by HBM: each
-// vector is read once and written once.  16,384 tokens of 64 query and 8 KV heads take 112 us, 90 %
+// vector is read once and written once.  16,384 tokens of 64 query and 8 KV heads take 109 us, 92 %
 // of the measured copy bandwidth (119 us before the first vectors' loads went ahead of the token's
 // slot and angles).  The quantised writer is bound by its instructions, above all the codes'
 // quotients and what a raised scale encodes anew: 9,485 tokens into an E4M3 cache take 118 us, 47 %.
@@ -179,9 +179,10 @@ __device__ __forceinline__ void rope_queries(const RopeParams &p, int t, int ite
   }
 }
 
-// BF16 pools: blockIdx.x is the token; blockIdx.y a share of its heads.
+// BF16 pools: blockIdx.x is the token; blockIdx.y a share of its heads.  Six CTAs an SM (80 registers)
+// keep the memory busiest: 112, 111, 109, 136 us for 16,384 tokens with 95 registers, 5, 6 and 8 CTAs.
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(128, 6) rope_bf16_kernel(const RopeParams p) {
   pdl_trigger();
   pdl_wait();
   constexpr int kItems = D / 16, kHeads = 128 / kItems;
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(128) rope_bf16_kernel(const RopeParams p) {
 // divides: the two differ by one unit in the last place at most); codes are x / scale, rounded,
 // in both.
 template <class Codec, bool kInterleaved>
-__global__ void __launch_bounds__(256, 4) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens,
+__global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens,
                                                             int shares) {
   using Word = typename Codec::Word;
   constexpr int D = 128, kWarps = 8, kBatch = 8;
