@@ -504,7 +504,8 @@ pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const fl
  * Rounding: q K^T, the softmax's maxima and sums and the output before its last rounding are
  * fp32; the weights (times V's scale) enter the second product as bf16, 2^-8 of each at most.
  * The scales of code pools are absmax scales, never negative.  The result is the same on every
- * call, bit for bit.  Batches of more than 16384 sequences return
+ * call, bit for bit.  Batches of more than 16384 sequences, and calls whose tiles (128 keys x up to
+ * 256 query rows, if every sequence filled its block table) exceed 2^28 per SM, return
  * PA_ERR_UNSUPPORTED.
  */
 pa_status pa_extend(const pa_shape *shape, void *out, const void *q, const int32_t *query_offsets,
@@ -528,8 +529,8 @@ pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
 
 /*
  * Bytes of pa_extend's and pa_cross_attend's workspace for this shape and number of query rows
- * on a GPU with sm_count SMs; 0 if the arguments are invalid.  It does not depend on the
- * lengths.  Nothing in it needs initialising, and it keeps nothing for a later call.  Host only.
+ * on a GPU with sm_count SMs; 0 if the arguments are invalid or more than a call takes.  It does
+ * not depend on the lengths.  Nothing in it needs initialising, and it keeps nothing for a later call.  Host only.
  */
 size_t pa_attend_workspace_bytes(const pa_shape *shape, int32_t total_queries, int32_t sm_count);
 

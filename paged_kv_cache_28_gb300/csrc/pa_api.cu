@@ -130,8 +130,9 @@ pa_status attend(const pa_shape *shape, void *out, const void *q, const int32_t 
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
   int sms = 0;
   if (current_sm_count(&sms) != PA_OK) return PA_ERR_CUDA;
-  if (workspace_bytes < pa::attend_workspace_bytes(*shape, total_queries, sms))
-    return PA_ERR_INVALID_ARG;
+  const size_t need = pa::attend_workspace_bytes(*shape, total_queries, sms);
+  if (need == 0) return PA_ERR_UNSUPPORTED;
+  if (workspace_bytes < need) return PA_ERR_INVALID_ARG;
   return pa::run_attend(*shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale,
                         v_scale, block_tables, seq_lens, causal, window, sm_scale, workspace, sms,
                         err_flag, reinterpret_cast<cudaStream_t>(stream));

@@ -1528,7 +1528,13 @@ pa_status launch(const AttendParams &p, const CUtensorMap &mq, const CUtensorMap
 
 }  // namespace
 
-size_t attend_workspace_bytes(const pa_shape &s, int T, int sms) { return make_plan(s, T, sms).total; }
+size_t attend_workspace_bytes(const pa_shape &s, int T, int sms) {
+  const Plan plan = make_plan(s, T, sms);
+  // a worker counts its tiles in 32 bits (2^28 of them would take minutes)
+  const int64_t units = (static_cast<int64_t>(T) / plan.tok + s.B) * s.Hkv;
+  const int64_t tiles = static_cast<int64_t>(s.max_blocks) * s.block_size / kKeys + 4;
+  return units * tiles / plan.workers < (int64_t(1) << 28) ? plan.total : 0;
+}
 
 pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t *offsets, int T,
                      const void *k_pool, const void *v_pool, const float *k_scale,

@@ -12,6 +12,7 @@
 namespace pa {
 
 // pa_extend (causal) and pa_cross_attend; `sms`: SMs of the device, as the workspace was sized.
+// 0 bytes: more work than a call takes.
 size_t attend_workspace_bytes(const pa_shape &s, int T, int sms);
 pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t *offsets, int T,
                      const void *k_pool, const void *v_pool, const float *k_scale,

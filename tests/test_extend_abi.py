@@ -68,6 +68,10 @@ def test_attend_workspace(lib):
     many = _lib.pa_attend_workspace_bytes(s, 1000, 152)
     assert 0 <= many - (2 * 152 * 256 * 130 * 4 + 152 * 16) < 1024
     assert _lib.pa_attend_workspace_bytes(s, 10, 0) == 0
+    # a million query tokens, each over a block table of 2^29 positions: too many tiles to count
+    far = shape(Hq=64, Hkv=8, B=1, max_blocks=1 << 25)
+    assert _lib.pa_attend_workspace_bytes(far, 1 << 20, 152) == 0
+    assert _lib.pa_attend_workspace_bytes(far, 1 << 10, 152) > 0
     assert _lib.pa_attend_workspace_bytes(s, -1, 152) == 0
 
 
