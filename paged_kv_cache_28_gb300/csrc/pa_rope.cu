@@ -12,9 +12,10 @@
 // vector is read once and written once.  16,384 tokens of 64 query and 8 KV heads take 109 us, 92 %
 // of the measured copy bandwidth (119 us before the first vectors' loads went ahead of the token's
 // slot and angles).  The quantised writer is bound by its instructions, above all the codes'
-// quotients and what a raised scale encodes anew: 9,485 tokens into an E4M3 cache take 118 us, 47 %.
+// quotients and what a raised scale encodes anew: 9,485 tokens into an E4M3 cache take 111 us, 50 %.
 // 261 us -> 155 with quotients by the reciprocal and the block index by a shift, 118 with the
-// tokens of a job in a loop and the writers' CTAs among the queries'.
+// tokens of a job in a loop and the writers' CTAs among the queries', 111 with a CTA's eight tokens
+// looked at by a warp each.
 #include <algorithm>
 
 #include "pa_codec.cuh"
@@ -213,6 +214,7 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
   __shared__ int warp_count[kWarps];
   __shared__ uint2 vectors[kWarps][kBatch][32];
   __shared__ uint32_t offsets_seen;
+  __shared__ bool first_of_run[kWarps];
   pdl_trigger();
   pdl_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -225,17 +227,29 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
   }
   const int nth = writer / shares, share = writer % shares;
   Word *codes = reinterpret_cast<Word *>(smem) + warp * p.bs * 32 + lane;    // row r: codes[32 r]
-  for (int t = nth * tokens; t < min(p.T, (nth + 1) * tokens); ++t) {
+  // A token right after another of its block (a prompt's tokens fill their blocks in order) has
+  // nothing to do; a warp looks at each of the CTA's.  The others look through the call: an earlier
+  // token of the block leads it, and without a later one past the first 256 tokens one look is enough.
+  auto same_block = [&](int u, int64_t o, int64_t blk0) {
+    return o >= blk0 && o < blk0 + p.bs && token_ok(p, o, p.positions[u], false);
+  };
+  if (warp < tokens && lane == 0) {
+    const int t = nth * tokens + warp;
+    bool first = false;
+    if (t < p.T) {
+      const int64_t slot = p.slots[t], before = t > 0 ? p.slots[t - 1] : -1;
+      first = token_ok(p, slot, p.positions[t], true) &&
+              !(t > 0 && same_block(t - 1, before, slot & ~static_cast<int64_t>(p.bs - 1)));
+    }
+    first_of_run[warp] = first;
+  }
+  __syncthreads();
+  for (int c = 0; c < tokens; ++c) {
+    if (!first_of_run[c]) continue;
+    const int t = nth * tokens + c;
     const int64_t slot = p.slots[t];
-    if (!token_ok(p, slot, p.positions[t], tid == 0)) continue;
     const int64_t blk = slot >> (p.bs == 16 ? 4 : 5), blk0 = blk * p.bs;
-    auto in_block = [&](int u, int64_t o) {
-      return o >= blk0 && o < blk0 + p.bs && token_ok(p, o, p.positions[u], false);
-    };
-    // A token right after another of its block (a prompt's tokens fill their blocks in order)
-    // leaves at once; the others look through the call: an earlier token of the block leads it,
-    // and without a later one past the first 256 tokens one look is enough.
-    if (t > 0 && in_block(t - 1, p.slots[t - 1])) continue;
+    auto in_block = [&](int u, int64_t o) { return same_block(u, o, blk0); };
     int earlier = 0, later = 0;
 #pragma unroll 8
     for (int u = tid; u < t - 1; u += 256) earlier |= in_block(u, p.slots[u]);
@@ -322,13 +336,13 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
               }
             }
             // magnitudes as integers, which order alike: one instruction finds the warp's largest
-            const uint32_t lo = x[i].x & 0x7FFF7FFFu, hi = x[i].y & 0x7FFF7FFFu;
-            const uint32_t most = __vmaxu2(lo, hi);
-            amax[i] = bf16_lo(__reduce_max_sync(0xffffffffu, max(most & 0xFFFFu, most >> 16)));
+            const uint32_t most = max(max(x[i].x & 0x7FFF0000u, (x[i].x << 16) & 0x7FFF0000u),
+                                      max(x[i].y & 0x7FFF0000u, (x[i].y << 16) & 0x7FFF0000u));
+            amax[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
           }
           // lane i: the scale that the batch's token i asks for.  The vectors wait in shared memory,
           // so that the tokens can be taken in a loop: unrolled, this part overflows the
-          // instruction cache (the kernel took 155 us for 9,485 tokens, and 118 in this form).
+          // instruction cache (155 us for 9,485 tokens, against 118 when it was made a loop).
           float want = 0.f;
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
