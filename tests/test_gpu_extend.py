@@ -585,6 +585,31 @@ def test_rope_and_cache(kind, T, Hq, Hkv, bs, order, interleaved, r, fused):
     Append(T, Hq, Hkv, 128, bs, kind, r, interleaved, fused, seed=T + r, order=order).check()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+@pytest.mark.parametrize("T,Hq,Hkv,bs,order", [(1024, 12, 12, 16, "runs"), (2047, 4, 2, 16, "shuffled"),
+                                               (2048, 6, 3, 32, "runs"), (2055, 5, 5, 32, "shuffled"),
+                                               (4100, 2, 2, 16, "shuffled")])
+def test_rope_and_cache_of_long_calls(kind, T, Hq, Hkv, bs, order):
+    """Calls whose CTAs take all heads, and several tokens each: padding and bad tokens among them,
+    a slot that two tokens far apart write, a block's tokens in either order."""
+    a = Append(T, Hq, Hkv, 128, bs, kind, seed=T, order=order)
+    a.slots[100:118] = -1
+    a.slots[9::41] = -1
+    a.pos[9::41] = a.npos + 7
+    a.slots[333] = a.nblocks * a.bs + 5
+    a.pos[700] = -4
+    keep = a.slots >= 0
+    bad = int(keep[700])
+    keep[333] = keep[700] = False
+    quantised = kind != "bf16"
+    if quantised:
+        good = keep.nonzero().flatten()
+        a.slots[good[-1]] = a.slots[good[3]]
+    a.check(keep)
+    assert pa.pa_read_error_flag(a.err) == (pa.PA_DEVERR_SLOT | bad * pa.PA_DEVERR_POSITION
+                                            | quantised * pa.PA_DEVERR_FP8_CONFLICT)
+
+
 @pytest.mark.parametrize("kind", ["fp8", "int4"])
 def test_scales_agree_with_reshape_and_cache(kind):
     """The scales of the two writers are off by one unit in the last place at most."""
