@@ -6,6 +6,8 @@ data and passes pointers; every step of the hot path runs in libpa.so.
 """
 from __future__ import annotations
 
+import contextlib
+
 import numpy as np
 import torch
 
@@ -26,6 +28,18 @@ def rope_table(num_positions: int, rotary_dim: int, base: float = 10000.0,
     f = torch.arange(0, rotary_dim, 2, device=device, dtype=torch.float64) / rotary_dim
     angle = torch.arange(num_positions, device=device, dtype=torch.float64)[:, None] * base ** -f
     return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def on_stream(stream, device=None):
+    """Context in which torch allocates and fills in the order of a call's stream: None, a
+    torch.cuda.Stream or a raw handle, as the binding takes it.  A buffer made on the current
+    stream for a kernel on another one is ordered with neither its fill nor its next owner."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream else
+                  torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
 
 
 class DeviceBatch:
@@ -155,6 +169,8 @@ class DeviceBatch:
             _lib.pa_merge_lse(self.shape, self.out, self.o_part, self.lse, num_splits, stream)
 
     # -- several tokens per sequence ---------------------------------------------
+    # `stream`: the inputs must be ready in its order, and what a call makes belongs to it (a reader
+    # on another stream waits for it first).
 
     def rope_and_cache(self, q, k_new, v_new, positions, slot_mapping, cos_sin, q_out=None,
                        stream=None, interleaved: bool = False) -> torch.Tensor:
@@ -162,7 +178,8 @@ class DeviceBatch:
         returns the rotated queries."""
         b = self.batch
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+            with on_stream(stream, self.device):
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
         shape = _lib.make_shape(q.shape[0], b.Hq, b.Hkv, b.D, b.block_size, b.nblocks,
                                 b.max_blocks, self.shape.kv_dtype)
         _lib.pa_rope_and_cache(shape, cos_sin, positions, q_out, q, k_new, v_new, self.k_pool,
@@ -177,8 +194,11 @@ class DeviceBatch:
         return self._attend_ws
 
     def extend(self, q, query_offsets, out=None, stream=None, window: int = 0) -> torch.Tensor:
-        """pa_extend of ragged query rows q [T, Hq, D] over the batch's cache."""
-        out = torch.zeros_like(q) if out is None else out
+        """pa_extend of ragged query rows q [T, Hq, D] over the batch's cache (a new `out`
+        is zero in the rows of no sequence)."""
+        if out is None:
+            with on_stream(stream, self.device):
+                out = torch.zeros_like(q)
         _lib.pa_extend(self.shape, out, q, query_offsets, self.k_pool, self.v_pool, self.k_scale,
                        self.v_scale, self.block_tables, self.seq_lens, self.batch.sm_scale,
                        self.attend_workspace(q.shape[0]), self.err, stream, window)
@@ -186,7 +206,9 @@ class DeviceBatch:
 
     def cross_attend(self, q, query_offsets, out=None, stream=None) -> torch.Tensor:
         """pa_cross_attend of ragged query rows q [T, Hq, D] over the batch's cache."""
-        out = torch.zeros_like(q) if out is None else out
+        if out is None:
+            with on_stream(stream, self.device):
+                out = torch.zeros_like(q)
         _lib.pa_cross_attend(self.shape, out, q, query_offsets, self.k_pool, self.v_pool,
                              self.k_scale, self.v_scale, self.block_tables, self.seq_lens,
                              self.batch.sm_scale, self.attend_workspace(q.shape[0]), self.err,

@@ -1,0 +1,86 @@
+"""DeviceBatch's calls with several tokens per sequence on streams other than the current one.
+
+The current stream is kept busy ahead of a call on another stream: whatever the call puts on the
+current one comes after its kernels.  Results are compared bit for bit with the same call on the
+current stream, so no tolerance is needed.
+"""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_28_gb300 import workload
+from paged_kv_cache_28_gb300.device import DeviceBatch, rope_table
+
+pytestmark = pytest.mark.gpu
+
+BUSY = 100_000_000          # clock cycles, about 50 ms
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+
+
+def device_batch(lens=(300, 700, 90, 1500), Hq=8, Hkv=2, D=64, seed=1):
+    lens = np.array(lens, dtype=np.int32)
+    return DeviceBatch(workload.build_batch("ragged", lens, Hq=Hq, Hkv=Hkv, D=D, block_size=16, seed=seed))
+
+
+def queries(dev, n, seed):
+    """n query tokens of each sequence, and their offsets."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    b = dev.batch
+    q = torch.randn(n * b.B, b.Hq, b.D, generator=g, device="cuda").bfloat16()
+    return q, torch.arange(0, n * b.B + 1, n, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", ["extend", "cross_attend"])
+def test_a_new_output_is_made_on_the_calls_stream(name, raw):
+    dev = device_batch()
+    q, offsets = queries(dev, 5, 2)
+    call = getattr(dev, name)
+    want = call(q, offsets).clone()
+    assert (want != 0).any(-1).all()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(BUSY)
+        out = call(q, offsets, stream=side.cuda_stream if raw else side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert dev.read_err() == 0
+
+
+def stream_of(t):
+    """The stream whose memory torch gave a tensor."""
+    at = t.data_ptr()
+    return next(x["stream"] for x in torch.cuda.memory_snapshot()
+                if x["address"] <= at < x["address"] + x["total_size"])
+
+
+def test_new_tensors_belong_to_the_calls_stream():
+    """A new tensor's memory goes back to the stream that wrote it, not to one that may hand it out
+    while the kernel still writes."""
+    dev = device_batch()
+    T, b = 64, dev.batch
+    g = torch.Generator(device="cuda").manual_seed(3)
+    qkv = torch.randn(T, b.Hq + 2 * b.Hkv, b.D, generator=g, device="cuda").bfloat16()
+    q, k, v = qkv[:, :b.Hq], qkv[:, b.Hq:b.Hq + b.Hkv], qkv[:, b.Hq + b.Hkv:]
+    args = (q, k, v, torch.arange(T, dtype=torch.int32, device="cuda"),
+            torch.arange(T, dtype=torch.int64, device="cuda"), rope_table(T, b.D))
+    want = dev.rope_and_cache(*args).clone()
+    rows, offsets = queries(dev, 3, 4)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        out = dev.rope_and_cache(*args, stream=stream)
+        assert stream_of(out) == side.cuda_stream
+        side.synchronize()
+        assert torch.equal(out, want)
+        assert stream_of(dev.extend(rows, offsets, stream=stream)) == side.cuda_stream
+    assert stream_of(dev.rope_and_cache(*args)) == torch.cuda.current_stream().cuda_stream
+    assert stream_of(dev.rope_and_cache(*args, stream=0)) == 0
+    torch.cuda.synchronize()
