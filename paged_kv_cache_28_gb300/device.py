@@ -187,32 +187,39 @@ class DeviceBatch:
                                stream, interleaved)
         return q_out
 
-    def attend_workspace(self, total_queries: int) -> torch.Tensor:
+    def attend_workspace(self, total_queries: int, stream=None) -> torch.Tensor:
+        """A new workspace for calls of total_queries query tokens on `stream`.  Calls that may
+        overlap on the GPU, those of two captured graphs among them, need one each."""
         nbytes = _lib.pa_attend_workspace_bytes(self.shape, total_queries, _sm_count(self.device))
-        if getattr(self, "_attend_ws", None) is None or self._attend_ws.numel() < nbytes:
-            self._attend_ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        return self._attend_ws
+        with on_stream(stream, self.device):
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
 
-    def extend(self, q, query_offsets, out=None, stream=None, window: int = 0) -> torch.Tensor:
+    def extend(self, q, query_offsets, out=None, stream=None, window: int = 0,
+               workspace=None) -> torch.Tensor:
         """pa_extend of ragged query rows q [T, Hq, D] over the batch's cache (a new `out`
-        is zero in the rows of no sequence)."""
+        is zero in the rows of no sequence).  workspace: the caller's, or one for this call
+        alone, from memory of the call's stream or captured graph."""
+        if workspace is None:
+            workspace = self.attend_workspace(q.shape[0], stream)
         if out is None:
             with on_stream(stream, self.device):
                 out = torch.zeros_like(q)
         _lib.pa_extend(self.shape, out, q, query_offsets, self.k_pool, self.v_pool, self.k_scale,
                        self.v_scale, self.block_tables, self.seq_lens, self.batch.sm_scale,
-                       self.attend_workspace(q.shape[0]), self.err, stream, window)
+                       workspace, self.err, stream, window)
         return out
 
-    def cross_attend(self, q, query_offsets, out=None, stream=None) -> torch.Tensor:
-        """pa_cross_attend of ragged query rows q [T, Hq, D] over the batch's cache."""
+    def cross_attend(self, q, query_offsets, out=None, stream=None, workspace=None) -> torch.Tensor:
+        """pa_cross_attend of ragged query rows q [T, Hq, D] over the batch's cache (out and
+        workspace as in extend)."""
+        if workspace is None:
+            workspace = self.attend_workspace(q.shape[0], stream)
         if out is None:
             with on_stream(stream, self.device):
                 out = torch.zeros_like(q)
         _lib.pa_cross_attend(self.shape, out, q, query_offsets, self.k_pool, self.v_pool,
                              self.k_scale, self.v_scale, self.block_tables, self.seq_lens,
-                             self.batch.sm_scale, self.attend_workspace(q.shape[0]), self.err,
-                             stream)
+                             self.batch.sm_scale, workspace, self.err, stream)
         return out
 
     # -- Quest page selection ------------------------------------------------------

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 import torch
 
-from paged_kv_cache_28_gb300 import workload
+from paged_kv_cache_28_gb300 import _lib, workload
 from paged_kv_cache_28_gb300.device import DeviceBatch, rope_table
 
 pytestmark = pytest.mark.gpu
@@ -84,3 +84,85 @@ def test_new_tensors_belong_to_the_calls_stream():
     assert stream_of(dev.rope_and_cache(*args)) == torch.cuda.current_stream().cuda_stream
     assert stream_of(dev.rope_and_cache(*args, stream=0)) == 0
     torch.cuda.synchronize()
+
+
+class Spy:
+    """Stands before a binding's call and keeps the workspaces it is given."""
+
+    def __init__(self, monkeypatch, name):
+        self.seen, self.call = [], getattr(_lib, name)
+        monkeypatch.setattr(_lib, name, self)
+
+    def __call__(self, shape, out, q, offsets, k, v, ks, vs, bt, sl, scale, workspace, *rest, **kw):
+        self.seen.append((workspace.data_ptr(), workspace.numel()))
+        return self.call(shape, out, q, offsets, k, v, ks, vs, bt, sl, scale, workspace, *rest, **kw)
+
+
+def apart(a, b):
+    return a[0] + a[1] <= b[0] or b[0] + b[1] <= a[0]
+
+
+@pytest.mark.parametrize("name", ["extend", "cross_attend"])
+def test_calls_that_may_overlap_have_a_workspace_each(name, monkeypatch):
+    dev = device_batch((9000, 7000, 11000))
+    spy = Spy(monkeypatch, "pa_" + name)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    work = [queries(dev, 40, 5), queries(dev, 3, 6)]
+    call = getattr(dev, name)
+    want = [call(q, offsets).clone() for q, offsets in work]
+    torch.cuda.synchronize()
+    spy.seen.clear()
+    outs = [[call(q, offsets, stream=s) for (q, offsets), s in zip(work, sides)] for _ in range(30)]
+    torch.cuda.synchronize()
+    for pair in outs:
+        for out, w in zip(pair, want):
+            assert torch.equal(out, w)
+    first, second = spy.seen[0::2], spy.seen[1::2]
+    assert all(apart(a, b) for a in first for b in second)
+
+
+def test_captured_calls_keep_their_workspaces(monkeypatch):
+    """Two graphs of one DeviceBatch share no workspace with each other nor with later eager calls,
+    larger ones among them."""
+    dev = device_batch((9000, 7000, 11000))
+    spy = Spy(monkeypatch, "pa_extend")
+    work = [queries(dev, 3, 7), queries(dev, 4, 8)]
+    want = [dev.extend(q, offsets).clone() for q, offsets in work]
+    outs = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    spy.seen.clear()
+    graphs = []
+    for (q, offsets), out in zip(work, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            dev.extend(q, offsets, out)
+    large = queries(dev, 200, 9)
+    dev.extend(*large)
+    dev.extend(*work[0])
+    assert apart(*spy.seen[:2])
+    assert all(apart(a, b) for a in spy.seen[:2] for b in spy.seen[2:])
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, sides):
+            with torch.cuda.stream(s):
+                g.replay()
+        dev.extend(*large)
+        torch.cuda.synchronize()
+        for out, w in zip(outs, want):
+            assert torch.equal(out, w)
+
+
+def test_a_workspace_of_the_callers():
+    dev = device_batch()
+    q, offsets = queries(dev, 5, 10)
+    ws = dev.attend_workspace(q.shape[0])
+    ws.fill_(0xFF)
+    for name in ("extend", "cross_attend"):
+        call = getattr(dev, name)
+        assert torch.equal(call(q, offsets, workspace=ws), call(q, offsets))
+    with pytest.raises(_lib.PAError, match="PA_ERR_INVALID_ARG"):
+        dev.extend(q, offsets, workspace=ws[:-256])
