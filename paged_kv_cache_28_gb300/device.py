@@ -239,26 +239,29 @@ class DeviceBatch:
     def quest_build_summaries(self, stream=None):
         b = self.batch
         npages = b.nblocks * b.block_size // 16
-        self.key_summaries = torch.zeros((npages, b.Hkv, 2, b.D), dtype=torch.bfloat16,
-                                         device=self.device)
-        slots = self.quest_summary_slots()
+        with on_stream(stream, self.device):
+            self.key_summaries = torch.zeros((npages, b.Hkv, 2, b.D), dtype=torch.bfloat16,
+                                             device=self.device)
+            slots = self.quest_summary_slots()
         shape = _lib.make_shape(slots.numel(), b.Hq, b.Hkv, b.D, b.block_size, b.nblocks,
                                 b.max_blocks, self.shape.kv_dtype)
         _lib.pa_quest_summarize(shape, self.k_pool, self.k_scale, self.key_summaries, slots,
                                 self.err, stream)
 
-    def quest_buffers(self, topk: int):
-        """page_scores [B, Hkv, pages per block-table row] and selected_pages [B, Hkv, topk]."""
+    def quest_buffers(self, topk: int, stream=None):
+        """page_scores [B, Hkv, pages per block-table row] and selected_pages [B, Hkv, topk], for
+        calls on `stream`."""
         b = self.batch
         max_pages = (b.max_blocks * b.block_size + 15) // 16
-        self.page_scores = torch.zeros((b.B, b.Hkv, max_pages), dtype=torch.float32,
-                                       device=self.device)
-        self.selected_pages = torch.empty((b.B, b.Hkv, topk), dtype=torch.int32,
-                                          device=self.device)
+        with on_stream(stream, self.device):
+            self.page_scores = torch.zeros((b.B, b.Hkv, max_pages), dtype=torch.float32,
+                                           device=self.device)
+            self.selected_pages = torch.empty((b.B, b.Hkv, topk), dtype=torch.int32,
+                                              device=self.device)
 
     def quest_select(self, topk: int, stream=None) -> torch.Tensor:
         if getattr(self, "selected_pages", None) is None or self.selected_pages.shape[2] != topk:
-            self.quest_buffers(topk)
+            self.quest_buffers(topk, stream)
         _lib.pa_quest_select(self.shape, self.q, self.key_summaries, self.block_tables,
                              self.seq_lens, topk, self.page_scores, self.selected_pages,
                              self.err, stream)

@@ -166,3 +166,29 @@ def test_a_workspace_of_the_callers():
         assert torch.equal(call(q, offsets, workspace=ws), call(q, offsets))
     with pytest.raises(_lib.PAError, match="PA_ERR_INVALID_ARG"):
         dev.extend(q, offsets, workspace=ws[:-256])
+
+
+def test_quest_buffers_are_made_on_the_calls_stream():
+    dev = device_batch((3000, 900, 5000))
+    dev.quest_build_summaries()
+    summaries = dev.key_summaries.clone()
+    dev.quest_buffers(9)
+    pages = dev.quest_select(9).clone()
+    assert (summaries != 0).any() and (pages >= 0).any()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        torch.cuda._sleep(BUSY)
+        dev.quest_build_summaries(stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(dev.key_summaries, summaries)
+        del dev.selected_pages
+        scores = dev.page_scores.clone()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(BUSY)
+        got = dev.quest_select(9, stream=side)
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert torch.equal(got, pages) and torch.equal(dev.page_scores, scores)
+    assert dev.read_err() == 0
