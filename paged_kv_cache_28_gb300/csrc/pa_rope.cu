@@ -335,10 +335,13 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
                 }
               }
             }
-            // magnitudes as integers, which order alike: one instruction finds the warp's largest
-            const uint32_t most = max(max(x[i].x & 0x7FFF0000u, (x[i].x << 16) & 0x7FFF0000u),
-                                      max(x[i].y & 0x7FFF0000u, (x[i].y << 16) & 0x7FFF0000u));
-            amax[i] = __uint_as_float(__reduce_max_sync(0xffffffffu, most));
+            // The largest magnitude by integers, which order alike.  A NaN is left out, as by fmaxf in
+            // pa_reshape_and_cache: it costs its own channel, not its block's scale.  A vector of
+            // nothing but NaN has -1 as its largest, a NaN's bits.
+            const float most = fmaxf(fmaxf(fabsf(bf16_lo(x[i].x)), fabsf(bf16_hi(x[i].x))),
+                                     fmaxf(fabsf(bf16_lo(x[i].y)), fabsf(bf16_hi(x[i].y))));
+            const int key = isnan(most) ? -1 : __float_as_int(most);
+            amax[i] = __int_as_float(__reduce_max_sync(0xffffffffu, key));
           }
           // lane i: the scale that the batch's token i asks for.  The vectors wait in shared memory,
           // so that the tokens can be taken in a loop: unrolled, this part overflows the

@@ -742,3 +742,72 @@ def test_prompt_in_chunks_then_decode(kind):
     pa.pa_decode(b.shape, out, b.q, b.k, b.v, b.k_scale, b.v_scale, b.block_tables, b.seq_lens, b.scale, b.err)
     ref, size = b.reference()
     assert ((out.double() - ref).abs() <= (1e-3 if kind == "bf16" else 2e-2) * (1 + ref.abs())).all()
+
+
+def write_codes_nan(x, pool, scale, slots, bs, kind):
+    """write_codes for values with NaN: a maximum leaves NaN out unless a vector holds nothing else, a
+    comparison with NaN is false, and the code of a NaN is E4M3's NaN or the lowest 4-bit code."""
+    top = {"fp8": 448.0, "int4": 7.0}[kind]
+    per_code = np.float32(1.0 / top)
+    code = restore(pool, torch.ones_like(scale), kind).float().cpu().numpy()
+    xs, sc = x.float().cpu().numpy(), scale.cpu().numpy()
+
+    def encode(v, s):
+        with np.errstate(all="ignore"):
+            y = np.where(s == 0, np.float32(0), v / s)
+        if kind == "fp8":
+            return torch.from_numpy(y).clamp(-448, 448).to(torch.float8_e4m3fn).float().numpy()
+        return np.where(np.isnan(y), np.float32(-7), np.clip(np.rint(y), -7, 7))
+
+    for t, slot in enumerate(slots.tolist()):
+        if slot < 0:
+            continue
+        blk, off = divmod(slot, bs)
+        for h in range(xs.shape[1]):
+            v, old = xs[t, h], sc[blk, h]
+            cand = np.fmax.reduce(np.abs(v)) * per_code
+            new = cand if off == 0 or cand > old else old
+            if off and new > old:
+                code[blk, :off, h] = encode(code[blk, :off, h] * old, new)
+            code[blk, off, h] = encode(v, new)
+            sc[blk, h] = new
+    code = torch.from_numpy(code).cuda()
+    if kind == "fp8":
+        pool.copy_(code.to(torch.float8_e4m3fn).view(torch.uint8))
+    else:
+        u = (code + 8).to(torch.uint8)
+        pool.copy_(u[..., 0::2] | (u[..., 1::2] << 4))
+    scale.copy_(torch.from_numpy(sc).cuda())
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+@pytest.mark.parametrize("T,Hkv,order", [(60, 2, "runs"), (2100, 1, "shuffled")])
+def test_rope_leaves_nan_out_of_the_scale(kind, T, Hkv, order):
+    """A NaN channel costs itself alone, at a block's first row and at others, as in
+    pa_reshape_and_cache; only a vector of nothing but NaN sets a NaN scale, and only at offset 0."""
+    a = Append(T, 4, Hkv, kind=kind, seed=T, order=order)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    first = (a.slots % a.bs == 0) & (a.slots >= 0)
+    for x in (a.k, a.v):
+        one = torch.randint(0, 128, (T, Hkv, 1), generator=g, device="cuda")
+        some = (torch.rand(T, Hkv, 1, generator=g, device="cuda") < 0.3) | first[:, None, None]
+        x.masked_fill_((torch.arange(128, device="cuda") == one) & some, float("nan"))
+        x[::17] = float("nan")
+        x[5::23] = -x[5::23].abs() * 8           # raised scales after them
+    assert (a.k[first].isnan().any(-1) & ~a.k[first].isnan().all(-1)).any()
+    k = rotated(a.k, a.cos_sin, a.pos.long(), False).bfloat16()
+    pools, scales = [x.clone() for x in a.pools], [x.clone() for x in a.scales]
+    other, others = [x.clone() for x in a.pools], [x.clone() for x in a.scales]
+    a.run()
+    for x, pool, scale in zip((k, a.v), pools, scales):
+        write_codes_nan(x, pool, scale, a.slots, a.bs, kind)
+    pa.pa_reshape_and_cache(a.shape, k, a.v, *other, *others, a.slots, None)
+    torch.cuda.synchronize()
+    assert pa.pa_read_error_flag(a.err) == 0
+    for mine, plain, theirs in zip(a.scales, scales, others):
+        assert torch.equal(mine.nan_to_num(-1.0), plain.nan_to_num(-1.0))
+        assert torch.equal(mine.isnan(), theirs.isnan())
+        assert ((mine - theirs).abs() <= 2.0 ** -23 * theirs).logical_or(mine.isnan()).all()
+    one_nan = (lambda x: torch.where(x == 0xFF, 0x7F, x)) if kind == "fp8" else (lambda x: x)  # noqa: E731
+    for mine, plain in zip(a.pools, pools):
+        assert torch.equal(one_nan(mine), one_nan(plain))
