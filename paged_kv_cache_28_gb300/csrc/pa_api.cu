@@ -13,8 +13,8 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Checks common to every call.  need_q: Hq matters (decode).
-pa_status check_shape(const pa_shape *s, bool need_q) {
+// Checks common to every call.  need_q: Hq matters.
+pa_status check_sizes(const pa_shape *s, bool need_q) {
   if (!s) return PA_ERR_INVALID_ARG;
   if (s->B < 0 || s->Hkv <= 0 || s->D <= 0 || s->block_size <= 0 || s->nblocks <= 0 ||
       s->max_blocks <= 0)
@@ -29,12 +29,21 @@ pa_status check_shape(const pa_shape *s, bool need_q) {
   if (s->D != 64 && s->D != 128) return PA_ERR_UNSUPPORTED;
   if (s->block_size != 16 && s->block_size != 32) return PA_ERR_UNSUPPORTED;
   if (s->kv_dtype != PA_KV_BF16 && s->D != 128) return PA_ERR_UNSUPPORTED;
-  // every row index and tile count below must fit in int32
+  // every row and scale index must fit in int32
   if (static_cast<int64_t>(s->nblocks) * s->block_size >= (int64_t(1) << 31))
     return PA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(s->B) * s->max_blocks >= (int64_t(1) << 31)) return PA_ERR_INVALID_ARG;
   if (s->kv_dtype != PA_KV_BF16 && static_cast<int64_t>(s->nblocks) * s->Hkv >= (int64_t(1) << 31))
-    return PA_ERR_INVALID_ARG;                          // scale indices
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+// The calls that read B sequences through block tables: table entries and 16-token tiles are
+// counted in int32.  (In the calls that write or summarise slots B counts tokens, and nothing
+// grows with the tables' width.)
+pa_status check_shape(const pa_shape *s) {
+  const pa_status st = check_sizes(s, true);
+  if (st != PA_OK) return st;
+  if (static_cast<int64_t>(s->B) * s->max_blocks >= (int64_t(1) << 31)) return PA_ERR_INVALID_ARG;
   const int64_t max_tiles = (static_cast<int64_t>(s->max_blocks) * s->block_size + 15) / 16;
   if (static_cast<int64_t>(s->B) * s->Hkv * max_tiles >= (int64_t(1) << 31))
     return PA_ERR_INVALID_ARG;
@@ -51,7 +60,7 @@ pa_status check_decode_args(const pa_shape *shape, const float *out, const void 
                             const void *k_pool, const void *v_pool, const float *k_scale,
                             const float *v_scale, const int32_t *bt, const int32_t *sl,
                             const pa_decode_opts *opts) {
-  pa_status st = check_shape(shape, true);
+  pa_status st = check_shape(shape);
   if (st != PA_OK) return st;
   st = check_ptrs({out, q, k_pool, v_pool, bt, sl});
   if (st != PA_OK) return st;
@@ -104,7 +113,7 @@ pa_status current_sm_count(int *sms) {
 }
 
 pa_status check_attend_shape(const pa_shape *s, int32_t total_queries) {
-  const pa_status st = check_shape(s, true);
+  const pa_status st = check_shape(s);
   if (st != PA_OK) return st;
   if (total_queries < 0 || static_cast<int64_t>(total_queries) * s->Hq >= (int64_t(1) << 31))
     return PA_ERR_INVALID_ARG;
@@ -146,7 +155,7 @@ pa_status pa_reshape_and_cache(const pa_shape *shape, const void *k_new, const v
                                void *k_pool, void *v_pool, float *k_scale, float *v_scale,
                                const int64_t *slot_mapping, int32_t *err_flag,
                                pa_stream_t stream) {
-  pa_status st = check_shape(shape, false);
+  pa_status st = check_sizes(shape, false);
   if (st != PA_OK) return st;
   if (shape->B == 0) return PA_OK;
   st = check_ptrs({k_new, v_new, k_pool, v_pool, slot_mapping});
@@ -162,7 +171,7 @@ pa_status pa_decode(const pa_shape *shape, float *out, const void *q, const void
                     const pa_decode_opts *opts, float sm_scale, int32_t *err_flag,
                     pa_stream_t stream) {
   if (!shape) return PA_ERR_INVALID_ARG;
-  if (shape->B == 0) return check_shape(shape, true);
+  if (shape->B == 0) return check_shape(shape);
   pa_status st = check_decode_args(shape, out, q, k_pool, v_pool, k_scale, v_scale,
                                    block_tables, seq_lens, opts);
   if (st != PA_OK) return st;
@@ -189,28 +198,28 @@ pa_status pa_decode(const pa_shape *shape, float *out, const void *q, const void
 }
 
 size_t pa_decode_workspace_bytes(const pa_shape *shape, int32_t num_segments) {
-  if (check_shape(shape, true) != PA_OK || num_segments < 1 || num_segments > kMaxSplits)
+  if (check_shape(shape) != PA_OK || num_segments < 1 || num_segments > kMaxSplits)
     return 0;
   return pa::splitkv_layout(*shape, num_segments).total;
 }
 
 int32_t pa_default_num_segments(const pa_shape *shape, int32_t sm_count) {
-  if (check_shape(shape, true) != PA_OK || sm_count <= 0) return 1;
+  if (check_shape(shape) != PA_OK || sm_count <= 0) return 1;
   return resident_segments(shape, sm_count);
 }
 
 size_t pa_splitkv_workspace_bytes(const pa_shape *shape, int32_t num_splits) {
-  if (check_shape(shape, true) != PA_OK || num_splits < 1 || num_splits > kMaxSplits) return 0;
+  if (check_shape(shape) != PA_OK || num_splits < 1 || num_splits > kMaxSplits) return 0;
   return static_cast<size_t>(shape->B) * shape->Hq * num_splits * (shape->D + 1) * sizeof(float);
 }
 
 size_t pa_cascade_workspace_bytes(const pa_shape *shape) {
-  if (check_shape(shape, true) != PA_OK) return 0;
+  if (check_shape(shape) != PA_OK) return 0;
   return pa::cascade_layout(shape->B, shape->Hq, shape->D).total;
 }
 
 int32_t pa_default_num_splits(const pa_shape *shape, int32_t sm_count) {
-  if (check_shape(shape, true) != PA_OK || sm_count <= 0) return 1;
+  if (check_shape(shape) != PA_OK || sm_count <= 0) return 1;
   // partial slots per query head: as many as 64 MiB of o_part holds, between 2 and 64,
   // and no more than a sequence has 16-token tiles
   const int64_t per_slot = static_cast<int64_t>(shape->B) * shape->Hq * shape->D * 4;
@@ -230,7 +239,7 @@ pa_status pa_decode_splitkv(const pa_shape *shape, float *o_part, float *lse, in
                             pa_stream_t stream) {
   if (!shape) return PA_ERR_INVALID_ARG;
   if (num_splits < 1 || num_splits > kMaxSplits) return PA_ERR_INVALID_ARG;
-  if (shape->B == 0) return check_shape(shape, true);
+  if (shape->B == 0) return check_shape(shape);
   pa_status st = check_decode_args(shape, o_part, q, k_pool, v_pool, k_scale, v_scale,
                                    block_tables, seq_lens, opts);
   if (st != PA_OK) return st;
@@ -247,7 +256,7 @@ pa_status pa_decode_splitkv(const pa_shape *shape, float *o_part, float *lse, in
 
 pa_status pa_merge_lse(const pa_shape *shape, float *out, const float *o_part, const float *lse,
                        int32_t num_splits, pa_stream_t stream) {
-  pa_status st = check_shape(shape, true);
+  pa_status st = check_shape(shape);
   if (st != PA_OK) return st;
   if (num_splits < 1 || num_splits > kMaxSplits) return PA_ERR_INVALID_ARG;
   if (shape->B == 0) return PA_OK;
@@ -260,7 +269,7 @@ pa_status pa_merge_lse(const pa_shape *shape, float *out, const float *o_part, c
 pa_status pa_quest_summarize(const pa_shape *shape, const void *k_pool, const float *k_scale,
                              void *key_summaries, const int64_t *slot_mapping, int32_t *err_flag,
                              pa_stream_t stream) {
-  pa_status st = check_shape(shape, false);
+  pa_status st = check_sizes(shape, false);
   if (st != PA_OK) return st;
   if (shape->B == 0) return PA_OK;
   st = check_ptrs({k_pool, key_summaries, slot_mapping});
@@ -274,7 +283,7 @@ pa_status pa_quest_select(const pa_shape *shape, const void *q, const void *key_
                           const int32_t *block_tables, const int32_t *seq_lens, int32_t topk,
                           float *page_scores, int32_t *selected_pages, int32_t *err_flag,
                           pa_stream_t stream) {
-  pa_status st = check_shape(shape, true);
+  pa_status st = check_shape(shape);
   if (st != PA_OK) return st;
   if (topk < 1) return PA_ERR_INVALID_ARG;
   if (shape->B == 0) return PA_OK;
@@ -295,7 +304,7 @@ pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const fl
                             const void *k_new, const void *v_new, void *k_pool, void *v_pool,
                             float *k_scale, float *v_scale, const int64_t *slot_mapping,
                             int32_t *err_flag, pa_stream_t stream) {
-  pa_status st = check_shape(shape, true);
+  pa_status st = check_sizes(shape, true);
   if (st != PA_OK) return st;
   if (!rope || rope->rotary_dim <= 0 || rope->rotary_dim > shape->D || rope->num_positions <= 0)
     return PA_ERR_INVALID_ARG;

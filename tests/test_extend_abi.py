@@ -109,3 +109,15 @@ def test_binding_takes_slices_of_a_fused_projection():
     with pytest.raises(ValueError, match="CUDA"):
         _lib._token_ptr(x)
     assert _lib._token_ptr(None) == (None, 0)
+
+
+def test_writes_of_many_tokens_beside_a_wide_block_table(lib):
+    """A write's B counts tokens: its size has nothing to do with the block table's width."""
+    for kw in (dict(B=32768, Hkv=8, Hq=64, max_blocks=8192), dict(B=16384, Hkv=16, Hq=16, max_blocks=8192),
+               dict(B=1 << 20, max_blocks=1 << 20)):
+        # (a rotation that is not built is found after the shape, before any CUDA call)
+        assert rope(lib, shape(**kw), r=24) == NOT_BUILT, kw
+        # the same shape as a batch of sequences has too many tiles to count
+        assert attend(lib, shape(**kw)) in (BAD, NOT_BUILT)
+        assert _lib.pa_attend_workspace_bytes(shape(**kw), 10, 152) == 0
+    assert rope(lib, shape(B=32768, max_blocks=0), r=24) == BAD

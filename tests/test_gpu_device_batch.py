@@ -192,3 +192,35 @@ def test_quest_buffers_are_made_on_the_calls_stream():
         torch.cuda.synchronize()
         assert torch.equal(got, pages) and torch.equal(dev.page_scores, scores)
     assert dev.read_err() == 0
+
+
+def test_long_prompt_beside_a_wide_block_table():
+    """32,768 tokens in one call, with a block table of 131,072 positions: the same bytes as in two calls
+    of half as many."""
+    T, D, Hkv = 32768, 64, 8
+    batch = workload.build_batch("long", [T], Hq=8, Hkv=Hkv, D=D, block_size=16, max_blocks=8192, seed=11,
+                                 with_pools=False)
+    g = torch.Generator(device="cuda").manual_seed(12)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    pools = [rand(batch.nblocks, 16, Hkv, D) for _ in range(2)]
+    whole = DeviceBatch(batch, pools=[x.clone() for x in pools] + [None, None])
+    half = DeviceBatch(batch, pools=[x.clone() for x in pools] + [None, None])
+    q, k, v = rand(T, 8, D), rand(T, Hkv, D), rand(T, Hkv, D)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = whole.block_tables[0, (pos // 16).long()].long() * 16 + pos.long() % 16
+    table = rope_table(T, D)
+    out = whole.rope_and_cache(q, k, v, pos, slots, table)
+    outs = [half.rope_and_cache(q[i:i + T // 2], k[i:i + T // 2], v[i:i + T // 2], pos[i:i + T // 2],
+                                slots[i:i + T // 2], table) for i in (0, T // 2)]
+    assert torch.equal(out, torch.cat(outs))
+    assert torch.equal(whole.k_pool, half.k_pool) and torch.equal(whole.v_pool, half.v_pool)
+    # the plain write and the page summaries of as many tokens
+    shape = _lib.make_shape(T, 8, Hkv, D, 16, batch.nblocks, 8192, _lib.PA_KV_BF16)
+    _lib.pa_reshape_and_cache(shape, k, v, whole.k_pool, whole.v_pool, None, None, slots, whole.err)
+    assert torch.equal(whole.k_pool.view(-1, Hkv, D)[slots], k)
+    assert torch.equal(whole.v_pool.view(-1, Hkv, D)[slots], v)
+    summaries = torch.zeros(batch.nblocks, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+    _lib.pa_quest_summarize(shape, whole.k_pool, None, summaries, slots, whole.err)
+    page = k.view(T // 16, 16, Hkv, D)
+    assert torch.equal(summaries[slots[::16] // 16], torch.stack([page.amin(1), page.amax(1)], 2))
+    assert whole.read_err() == 0 and half.read_err() == 0
