@@ -1132,8 +1132,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         at += c.n;
         c.row = -1;
         const int g = c.tile * kKeys + 16 * lane;
-        if (g < x.L && g + 16 > x.lo && lane < 8 * c.n)
-          c.row = p.block_tables[static_cast<int64_t>(x.seq) * p.max_blocks + g / p.bs] & 0x7fffffff;
+        if (g < x.L && g + 16 > x.lo && lane < 8 * c.n) {
+          // (as unsigned, a negative id is past every pool)
+          const uint32_t id = p.block_tables[static_cast<int64_t>(x.seq) * p.max_blocks + g / p.bs];
+          c.row = static_cast<int>(min(id, 0x7fffffffu));
+        }
         return c;
       };
       // block id to pool row (and the scales on their way), when it has come

@@ -811,3 +811,26 @@ def test_rope_leaves_nan_out_of_the_scale(kind, T, Hkv, order):
     one_nan = (lambda x: torch.where(x == 0xFF, 0x7F, x)) if kind == "fp8" else (lambda x: x)  # noqa: E731
     for mine, plain in zip(a.pools, pools):
         assert torch.equal(one_nan(mine), one_nan(plain))
+
+
+@pytest.mark.parametrize("bad", ["nblocks", "far", 2 ** 31 - 1, -1, -2 ** 31, -2 ** 31 + 2])
+@pytest.mark.parametrize("kind,n,L,causal", [("bf16", [3, 1], [400, 90], True), ("bf16", [200], [500], True),
+                                             ("bf16", [1, 2], [300, 20], False), ("fp8", [3, 1], [400, 90], True),
+                                             ("fp8", [200], [500], True), ("int4", [3, 1], [400, 90], True),
+                                             ("int4", [200], [500], False)])
+def test_blocks_outside_the_pool_read_zeros(kind, n, L, causal, bad):
+    """Keys of a block id outside the pool, of either sign, score 0 and count in the softmax's sum, and
+    their values add nothing: the same result as for a block of zeros."""
+    b = Batch(n, L, 2, 4, kind=kind, causal=causal, seed=32)
+    used = set(b.block_tables.flatten().tolist())
+    zero = next(i for i in range(b.nblocks) if i not in used)
+    for x in (b.k, b.v):
+        x[zero] = 0x88 if kind == "int4" else 0
+    b.seen.view(b.nblocks, b.bs)[zero] = True
+    b.block_tables[0, 1] = zero
+    b.check()                                    # with the block of zeros
+    ref, size = b.reference()
+    b.block_tables[0, 1] = {"nblocks": b.nblocks, "far": b.nblocks + 5}.get(bad, bad)
+    out = b.run()
+    assert pa.pa_read_error_flag(b.err) == pa.PA_DEVERR_BLOCK_ID
+    assert ((out.double() - ref).abs() <= U * ref.abs() + size).all()
