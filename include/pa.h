@@ -496,7 +496,8 @@ pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const fl
  *                  that may overlap on the GPU need one each
  * Cached values must be finite at the positions [seq_lens[b] - n_b - window + 1, seq_lens[b])
  * that some token of the call sees; other rows, and blocks wholly outside them, may hold
- * anything.  Block-table entries of blocks before every token's window are not read.
+ * anything.  Block-table entries of blocks before every token's window are not read.  A query
+ * head with a NaN gives NaN (zeros if it sees no key), and no other row feels it.
  * Errors found on the device: a block id outside the pool reads zeros (PA_DEVERR_BLOCK_ID); a
  * length beyond the block table is clamped, and a sequence with more query than cached tokens
  * gets zeros (PA_DEVERR_SEQ_LEN); a sequence whose offsets fall or leave the rows is skipped

@@ -1025,7 +1025,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       tc_fence_after();
       if (warp_live) {
         const bool whole = x.starts && x.ends;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        // a row without keys has l = 0 and gives zeros; a NaN in its query gives NaN
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         uint16_t *dst = p.out + (static_cast<int64_t>(x.row + tok0 + my_tok) * p.Hq + x.h * p.G +
                                  (row - my_tok * p.G)) * C::D;
         const int64_t r = (2 * static_cast<int64_t>(blockIdx.x * C::STREAMS + st) + x.starts) * p.rows +
@@ -1040,8 +1041,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (whole) {
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              o[e] = l > 0.f ? pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv)
-                             : 0u;
+              o[e] = l == 0.f ? 0u
+                              : pack_bf16(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
             if (live) {
               store32(dst + j, o, p.wide);
               store32(dst + j + 16, o + 8, p.wide);
@@ -1425,7 +1426,7 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p)
   for (int i0 = 0; i0 < n; i0 += 32) {                   // a piece's weight per lane
     const float2 ml = i0 == 0 ? first : i0 + lane < n ? p.part_ml[slot(i0 + lane)] : none;
     // a piece without seen keys has only zero weights, and so is its O
-    const float f = ml.y > 0.f ? ex2(ml.x - M) : 0.f;
+    const float f = ml.y == 0.f ? 0.f : ex2(ml.x - M);
     l += f * ml.y;
     for (int j = 0; j < 32 && i0 + j < n; j += kBatch) {
       if (i0 + j > 0) load(i0 + j);
@@ -1441,7 +1442,7 @@ __global__ void __launch_bounds__(256) attend_merge_kernel(const AttendParams p)
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint16_t *dst = p.out + (static_cast<int64_t>(cut.x + tok) * p.Hq + cut.z * p.G + (rr - in_tile * p.G)) * D +
                   lane * E;
   if constexpr (E == 4)

@@ -834,3 +834,28 @@ def test_blocks_outside_the_pool_read_zeros(kind, n, L, causal, bad):
     out = b.run()
     assert pa.pa_read_error_flag(b.err) == pa.PA_DEVERR_BLOCK_ID
     assert ((out.double() - ref).abs() <= U * ref.abs() + size).all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("kind,n,L", [("bf16", [3, 2], [400, 9000]), ("bf16", [200, 3], [700, 4000]),
+                                      ("fp8", [3, 2], [400, 9000]), ("int4", [200, 3], [700, 4000]),
+                                      ("bf16", [3, 2] * 150, [100, 128] * 150),
+                                      ("bf16", [40, 60] * 60, [90, 120] * 60),
+                                      ("fp8", [3, 2] * 150, [100, 128] * 150),
+                                      ("int4", [40, 60] * 60, [90, 120] * 60)])
+def test_a_nan_in_a_query_shows(kind, n, L, causal):
+    """A query head with a NaN has no weights: its output is NaN, whether its unit was cut or not, and
+    every other row is what it was."""
+    b = Batch(n, L, 2, 4, kind=kind, causal=causal, seed=33)
+    want = b.run().clone()
+    hit = torch.zeros(b.T, b.Hq, dtype=torch.bool, device="cuda")
+    for row, head, d in ((0, 0, 0), (1, 5, 127), (n[0] - 1, 2, 64), (n[0], 7, 3), (sum(n) - 1, 4, 31)):
+        b.q[row, head, d] = float("nan")
+        hit[row, head] = True
+    out = b.run()
+    assert pa.pa_read_error_flag(b.err) == 0
+    assert out[hit].isnan().all()
+    assert torch.equal(out[~hit], want[~hit])
+    b.seq_lens.zero_()                           # nothing to see: zeros all the same
+    b.err.zero_()
+    assert (b.run()[:sum(n)] == 0).all()
