@@ -839,13 +839,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const int all_lo = p.causal && p.window > 0 ? x.pos + tok0 + ntok - p.window : 0;
       float m = -INFINITY;                               // reference maximum, times c
       float l = 0.f;
+      // A barrier's parity tells its phase only from the ones next to it, and a row tile has not
+      // followed the scales of pieces that it had no part in.  Once S of a piece's first tile is
+      // there its scales are the last ones stored in their place, and they stay until the tile's
+      // weights are out (see SCALES); from then on this row tile keeps up.
+      if constexpr (C::QUANT && C::SHARED) ok = mbar_wait(s_full(t), s_phase);
       for (int i = 0; i < n_tiles; ++i) {
         const int key0 = (tile_0 + i) * kKeys;
         // code pools: the scales of the tile's pages, K's then V's
         [[maybe_unused]] uint32_t sc = 0;
         if constexpr (C::QUANT) {
           const uint32_t n = tile0 + i;
-          ok = mbar_wait(sc_full(st, n), sc_parity(n));
+          ok = ok && mbar_wait(sc_full(st, n), sc_parity(n));
           sc = smem_u32(scales[st][n % C::SCALES]);
         }
         ok = ok && mbar_wait(s_full(t), s_phase);

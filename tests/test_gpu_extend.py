@@ -859,3 +859,13 @@ def test_a_nan_in_a_query_shows(kind, n, L, causal):
     b.seq_lens.zero_()                           # nothing to see: zeros all the same
     b.err.zero_()
     assert (b.run()[:sum(n)] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "int4"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_half_empty_units_between_full_ones(kind, causal):
+    """Shared form: units whose second row tile has no tokens lie between full ones, with more key tiles
+    than the scales of a stream are held for."""
+    n = [65, 1, 100, 10, 128, 70, 2, 97] * 3
+    L = [1500, 2900, 1400, 700, 2300, 900, 5000, 1111] * 3
+    Batch(n, L, 2, 8, kind=kind, causal=causal, seed=34).check()
