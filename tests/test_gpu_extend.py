@@ -869,3 +869,22 @@ def test_half_empty_units_between_full_ones(kind, causal):
     n = [65, 1, 100, 10, 128, 70, 2, 97] * 3
     L = [1500, 2900, 1400, 700, 2300, 900, 5000, 1111] * 3
     Batch(n, L, 2, 8, kind=kind, causal=causal, seed=34).check()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "subnormal", "int4"])
+@pytest.mark.parametrize("n", [[3, 1], [200]])
+def test_every_code(kind, n):
+    """All finite E4M3 codes, its subnormal ones and zeros by themselves, and all 4-bit codes, in K and V."""
+    b = Batch(n, [600] * len(n), 2, 4, kind="fp8" if kind == "subnormal" else kind, seed=35)
+    for m, (x, scale) in enumerate(((b.k, b.k_scale), (b.v, b.v_scale))):
+        i = torch.arange(x.numel(), device="cuda").view(x.shape) * 7919 + m
+        sign = (i // 13 % 2 * 128).to(torch.uint8)
+        if kind == "subnormal":                  # up to 7 / 512
+            x.copy_((i % 8).to(torch.uint8) | sign)
+            scale.fill_(64.0)
+        elif kind == "fp8":
+            x.copy_((i % 127).to(torch.uint8) | sign)
+            scale.fill_(2.0 ** -7)
+        else:
+            x.copy_((i % 256).to(torch.uint8))
+    b.check()
