@@ -519,7 +519,8 @@ pa_status pa_extend(const pa_shape *shape, void *out, const void *q, const int32
  * pa_cross_attend -- the same attention without order: every query token of sequence b sees all
  * seq_lens[b] cached tokens (an encoder's states, written by pa_reshape_and_cache; their number
  * has nothing to do with n_b).  seq_lens[b] = 0 gives zeros.  Several sequences may name the
- * same blocks.
+ * same blocks.  (For one token per sequence pa_decode computes the same, into fp32; with a
+ * workspace it is the faster of the two for short states.)
  */
 pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
                           const int32_t *query_offsets, int32_t total_queries,

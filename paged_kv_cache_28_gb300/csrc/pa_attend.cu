@@ -31,7 +31,7 @@
 //   at 5.1 cycles a warp) and about 2,000 beside the other's and the products, which read and
 //   write the same TMEM.  A key tile takes about 3,300 cycles: the chain S -> softmax -> P V of
 //   each row tile, half of it behind the other's.  2,048 tokens after 15,952 cached ones, 64
-//   query and 8 KV heads: 0.80 ms, 1,425 TFLOP/s, 75 % of the measured cuBLAS peak.
+//   query and 8 KV heads: 0.80-0.82 ms, 1,390-1,431 TFLOP/s, 73-75 % of the measured cuBLAS peak.
 //   Separate form: the loads.  32 tokens after 257,000 cached ones: 0.178 ms, 5.9 TB/s, 87 %
 //   of the measured copy bandwidth.
 //   Code pools: restoring the codes takes issue slots and shared memory from the softmax; a
@@ -591,7 +591,7 @@ struct RingOrder {
 };
 
 // kKind: the pools' pa_kv_dtype.  Codes (D = 128) are restored to bf16 tiles, without their scale,
-// by four warps of their own: K's scale multiplies the scores of a page, V's its weights.
+// by eight warps of their own: K's scale multiplies the scores of a page, V's its weights.
 template <int kD, int kKind, bool kShared>
 struct AttendCfg {
   static constexpr int D = kD, KIND = kKind;

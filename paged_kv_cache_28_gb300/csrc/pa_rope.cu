@@ -11,8 +11,9 @@
 // Nothing here is reused but the table row of a token, so the bf16 kernel is bound by HBM: each
 // vector is read once and written once.  16,384 tokens of 64 query and 8 KV heads take 109 us, 92 %
 // of the measured copy bandwidth (119 us before the first vectors' loads went ahead of the token's
-// slot and angles).  The quantised writer is bound by its instructions, above all the codes'
-// quotients and what a raised scale encodes anew: 9,485 tokens into an E4M3 cache take 111 us, 50 %.
+// slot and angles).  9,485 tokens into an E4M3 cache take 111 us, 50 % of it: the writers alone take
+// 74, the queries (by the bf16 kernel, with four KV heads) 60, and beside each other they hide
+// little.  What bounds the writers by themselves has not been measured.
 // 261 us -> 155 with quotients by the reciprocal and the block index by a shift, 118 with the
 // tokens of a job in a loop and the writers' CTAs among the queries', 111 with a CTA's eight tokens
 // looked at by a warp each.
