@@ -536,6 +536,55 @@ pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
  */
 size_t pa_attend_workspace_bytes(const pa_shape *shape, int32_t total_queries, int32_t sm_count);
 
+/*
+ * Positions with several axes, and reading the cache back.
+ */
+
+#define PA_MAX_AXES 4
+
+/* Which of a token's positions each pair of channels turns by (host memory, read by the call). */
+typedef struct {
+    int32_t num_axes;          /* 1 .. PA_MAX_AXES (time, height and width of a video: 3)   */
+    uint8_t pair_axis[64];     /* pair j < rotary_dim / 2 turns by axis pair_axis[j] < num_axes;
+                                  the rest is not looked at */
+} pa_rope_axes;
+
+/*
+ * pa_rope_axes_and_cache -- pa_rope_and_cache for tokens whose position has several axes (the time,
+ * row and column of an image's or a video's patch): pair j of token t turns by
+ *     c, s = cos_sin[positions[pair_axis[j]][t]][j], [rotary_dim / 2 + j]
+ * positions [num_axes, shape->B] int32.  Everything else is as in pa_rope_and_cache; a token with
+ * any of its num_axes positions outside the table sets PA_DEVERR_POSITION and is skipped.
+ */
+pa_status pa_rope_axes_and_cache(const pa_shape *shape, const pa_rope *rope,
+                                 const pa_rope_axes *axes, const float *cos_sin,
+                                 const int32_t *positions, void *q_out, const void *q,
+                                 const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                                 float *k_scale, float *v_scale, const int64_t *slot_mapping,
+                                 int32_t *err_flag, pa_stream_t stream);
+
+/*
+ * pa_read_cache -- cached rows as dense bf16 tensors (to send a sequence elsewhere, to move it to a
+ * pool of another kind, or for a call that takes dense keys and values).  Rows offsets[b] ..
+ * offsets[b + 1) of k_out and v_out are sequence b's positions starts[b], starts[b] + 1, ...:
+ *     k_out[offsets[b] + i][h][:] = K_b[starts[b] + i][h][:]
+ * with K_b gathered through the block table; a bf16 pool's rows are copied bit for bit, codes are
+ * restored as the fp32 product code * scale[block][h], rounded to bf16.
+ *   k_out, v_out  [total_tokens, Hkv, D] bf16; either may be NULL (with its pool and scale)
+ *   offsets       [B + 1] int32, not falling, within [0, total_tokens]; rows before the first and
+ *                 from the last offset on are left as they were
+ *   starts        [B] int32, or NULL: all start at position 0
+ * shape->Hq is ignored.  Errors found on the device: a block id outside the pool gives zeros
+ * (PA_DEVERR_BLOCK_ID); positions outside [0, seq_lens[b]) give zeros, as do those past the block
+ * table, and set PA_DEVERR_SEQ_LEN; a sequence whose offsets fall or leave the rows is skipped
+ * (PA_DEVERR_QUERY).
+ */
+pa_status pa_read_cache(const pa_shape *shape, void *k_out, void *v_out, const void *k_pool,
+                        const void *v_pool, const float *k_scale, const float *v_scale,
+                        const int32_t *block_tables, const int32_t *seq_lens,
+                        const int32_t *offsets, int32_t total_tokens, const int32_t *starts,
+                        int32_t *err_flag, pa_stream_t stream);
+
 /* Human-readable name of a status. */
 const char *pa_status_string(pa_status status);
 

@@ -25,7 +25,7 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode", "pa_splitkv_workspace_bytes",
             "pa_read_error_flag", "pa_decode_splitkv_noalloc", "pa_quest_summarize",
             "pa_quest_select", "pa_cascade_workspace_bytes", "pa_decode_workspace_bytes",
             "pa_default_num_segments", "pa_rope_and_cache", "pa_extend", "pa_cross_attend",
-            "pa_attend_workspace_bytes")
+            "pa_attend_workspace_bytes", "pa_rope_axes_and_cache", "pa_read_cache")
 PA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -40,6 +40,10 @@ class pa_rope(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
                 ("num_positions", ctypes.c_int32), ("q_stride", ctypes.c_int64),
                 ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class pa_rope_axes(ctypes.Structure):
+    _fields_ = [("num_axes", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * 64)]
 
 
 class pa_decode_opts(ctypes.Structure):
@@ -118,6 +122,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                 P]),
             "pa_cross_attend": (I32, [S, P, P, P, I32, P, P, P, P, P, P, F, P, ctypes.c_size_t, P,
                                       P]),
+            "pa_rope_axes_and_cache": (I32, [S, ctypes.POINTER(pa_rope),
+                                             ctypes.POINTER(pa_rope_axes)] + [P] * 13),
+            "pa_read_cache": (I32, [S, P, P, P, P, P, P, P, P, P, I32, P, P, P]),
             "pa_attend_workspace_bytes": (ctypes.c_size_t, [S, I32, I32]),
         }
         for name, (res, args) in sig.items():
@@ -329,6 +336,44 @@ def pa_rope_and_cache(shape: pa_shape, cos_sin, positions, q_out, q, k_new, v_ne
     _check("pa_rope_and_cache", lib.pa_rope_and_cache(
         ctypes.byref(shape), ctypes.byref(rope), _ptr(cos_sin), _ptr(positions), _ptr(q_out), qp,
         kp, vp, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
+        _ptr(err_flag), _stream(stream)))
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_axes(num_axes: int, pair_axis: bytes) -> pa_rope_axes:
+    return pa_rope_axes(num_axes, (ctypes.c_uint8 * 64).from_buffer_copy(pair_axis.ljust(64, b"\0")))
+
+
+def pa_rope_axes_and_cache(shape: pa_shape, pair_axis, cos_sin, positions, q_out, q, k_new, v_new,
+                           k_pool, v_pool, k_scale, v_scale, slot_mapping, err_flag=None, stream=None,
+                           interleaved: bool = False) -> None:
+    """As pa_rope_and_cache with positions [num_axes, T] int32; pair_axis: the axis that each of the
+    rotary_dim / 2 pairs turns by (a sequence of small ints, or bytes)."""
+    lib = load()
+    (qp, qs), (kp, ks), (vp, vs) = _token_ptr(q), _token_ptr(k_new), _token_ptr(v_new)
+    rows, width = cos_sin.shape
+    pair_axis = bytes(pair_axis)
+    if len(pair_axis) != width // 2 or positions.dim() != 2 or positions.shape[1] != shape.B:
+        raise ValueError("pair_axis has rotary_dim / 2 entries, positions is [num_axes, tokens]")
+    rope = _rope(width, bool(interleaved), rows, qs, ks, vs)
+    axes = _rope_axes(int(positions.shape[0]), pair_axis)
+    _check("pa_rope_axes_and_cache", lib.pa_rope_axes_and_cache(
+        ctypes.byref(shape), ctypes.byref(rope), ctypes.byref(axes), _ptr(cos_sin), _ptr(positions),
+        _ptr(q_out), qp, kp, vp, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
+        _ptr(slot_mapping), _ptr(err_flag), _stream(stream)))
+
+
+def pa_read_cache(shape: pa_shape, k_out, v_out, k_pool, v_pool, k_scale, v_scale, block_tables,
+                  seq_lens, offsets, starts=None, err_flag=None, stream=None) -> None:
+    """k_out, v_out: [total_tokens, Hkv, D] bf16 (either may be None); offsets: [B + 1] int32;
+    starts: [B] int32, None: position 0."""
+    out = v_out if k_out is None else k_out
+    tokens = 0 if out is None else int(out.shape[0])
+    if k_out is not None and v_out is not None and int(v_out.shape[0]) != tokens:
+        raise ValueError("k_out and v_out have the same number of rows")
+    _check("pa_read_cache", load().pa_read_cache(
+        ctypes.byref(shape), _ptr(k_out), _ptr(v_out), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
+        _ptr(v_scale), _ptr(block_tables), _ptr(seq_lens), _ptr(offsets), tokens, _ptr(starts),
         _ptr(err_flag), _stream(stream)))
 
 

@@ -147,6 +147,42 @@ pa_status attend(const pa_shape *shape, void *out, const void *q, const int32_t 
                         err_flag, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// pa_rope_and_cache and, given axes, pa_rope_axes_and_cache.
+pa_status rope_and_cache(const pa_shape *shape, const pa_rope *rope, const pa_rope_axes *axes,
+                         const float *cos_sin, const int32_t *positions, void *q_out, const void *q,
+                         const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                         float *k_scale, float *v_scale, const int64_t *slot_mapping,
+                         int32_t *err_flag, pa_stream_t stream) {
+  pa_status st = check_sizes(shape, true);
+  if (st != PA_OK) return st;
+  if (!rope || rope->rotary_dim <= 0 || rope->rotary_dim > shape->D || rope->num_positions <= 0)
+    return PA_ERR_INVALID_ARG;
+  if (rope->rotary_dim % 16) return PA_ERR_UNSUPPORTED;
+  if (axes) {
+    if (axes->num_axes < 1 || axes->num_axes > PA_MAX_AXES) return PA_ERR_INVALID_ARG;
+    for (int j = 0; j < rope->rotary_dim / 2; ++j)
+      if (axes->pair_axis[j] >= axes->num_axes) return PA_ERR_INVALID_ARG;
+  }
+  auto bad_stride = [&](int64_t stride, int heads) {
+    return stride != 0 && (stride < static_cast<int64_t>(heads) * shape->D || stride % 8);
+  };
+  if (bad_stride(rope->q_stride, shape->Hq) || bad_stride(rope->k_stride, shape->Hkv) ||
+      bad_stride(rope->v_stride, shape->Hkv))
+    return PA_ERR_INVALID_ARG;
+  if (shape->B == 0) return PA_OK;
+  st = check_ptrs({cos_sin, positions, k_new, v_new, k_pool, v_pool, slot_mapping});
+  if (st != PA_OK) return st;
+  if ((q != nullptr) != (q_out != nullptr) || !aligned16(q) || !aligned16(q_out))
+    return PA_ERR_INVALID_ARG;
+  if (q && q == q_out && rope->q_stride != 0 &&
+      rope->q_stride != static_cast<int64_t>(shape->Hq) * shape->D)
+    return PA_ERR_INVALID_ARG;
+  if (shape->kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  return pa::run_rope_and_cache(*shape, *rope, axes, cos_sin, positions, q_out, q, k_new, v_new,
+                                k_pool, v_pool, k_scale, v_scale, slot_mapping, err_flag,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -304,29 +340,43 @@ pa_status pa_rope_and_cache(const pa_shape *shape, const pa_rope *rope, const fl
                             const void *k_new, const void *v_new, void *k_pool, void *v_pool,
                             float *k_scale, float *v_scale, const int64_t *slot_mapping,
                             int32_t *err_flag, pa_stream_t stream) {
-  pa_status st = check_sizes(shape, true);
+  return rope_and_cache(shape, rope, nullptr, cos_sin, positions, q_out, q, k_new, v_new, k_pool, v_pool,
+                        k_scale, v_scale, slot_mapping, err_flag, stream);
+}
+
+pa_status pa_rope_axes_and_cache(const pa_shape *shape, const pa_rope *rope,
+                                 const pa_rope_axes *axes, const float *cos_sin,
+                                 const int32_t *positions, void *q_out, const void *q,
+                                 const void *k_new, const void *v_new, void *k_pool, void *v_pool,
+                                 float *k_scale, float *v_scale, const int64_t *slot_mapping,
+                                 int32_t *err_flag, pa_stream_t stream) {
+  if (!axes) return PA_ERR_INVALID_ARG;
+  return rope_and_cache(shape, rope, axes, cos_sin, positions, q_out, q, k_new, v_new, k_pool, v_pool,
+                        k_scale, v_scale, slot_mapping, err_flag, stream);
+}
+
+pa_status pa_read_cache(const pa_shape *shape, void *k_out, void *v_out, const void *k_pool,
+                        const void *v_pool, const float *k_scale, const float *v_scale,
+                        const int32_t *block_tables, const int32_t *seq_lens,
+                        const int32_t *offsets, int32_t total_tokens, const int32_t *starts,
+                        int32_t *err_flag, pa_stream_t stream) {
+  pa_status st = check_sizes(shape, false);
   if (st != PA_OK) return st;
-  if (!rope || rope->rotary_dim <= 0 || rope->rotary_dim > shape->D || rope->num_positions <= 0)
+  if (total_tokens < 0 || static_cast<int64_t>(shape->B) * shape->max_blocks >= (int64_t(1) << 31))
     return PA_ERR_INVALID_ARG;
-  if (rope->rotary_dim % 16) return PA_ERR_UNSUPPORTED;
-  auto bad_stride = [&](int64_t stride, int heads) {
-    return stride != 0 && (stride < static_cast<int64_t>(heads) * shape->D || stride % 8);
+  if (shape->B > pa::kMaxSplitBatch) return PA_ERR_UNSUPPORTED;
+  if (shape->B == 0 || total_tokens == 0 || (!k_out && !v_out)) return PA_OK;
+  st = check_ptrs({block_tables, seq_lens, offsets});
+  if (st != PA_OK) return st;
+  if (starts && !aligned16(starts)) return PA_ERR_INVALID_ARG;
+  const bool codes = shape->kv_dtype != PA_KV_BF16;
+  auto bad = [&](const void *out, const void *pool, const float *scale) {
+    return out && (!aligned16(out) || !pool || !aligned16(pool) || (codes && !scale));
   };
-  if (bad_stride(rope->q_stride, shape->Hq) || bad_stride(rope->k_stride, shape->Hkv) ||
-      bad_stride(rope->v_stride, shape->Hkv))
-    return PA_ERR_INVALID_ARG;
-  if (shape->B == 0) return PA_OK;
-  st = check_ptrs({cos_sin, positions, k_new, v_new, k_pool, v_pool, slot_mapping});
-  if (st != PA_OK) return st;
-  if ((q != nullptr) != (q_out != nullptr) || !aligned16(q) || !aligned16(q_out))
-    return PA_ERR_INVALID_ARG;
-  if (q && q == q_out && rope->q_stride != 0 &&
-      rope->q_stride != static_cast<int64_t>(shape->Hq) * shape->D)
-    return PA_ERR_INVALID_ARG;
-  if (shape->kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
-  return pa::run_rope_and_cache(*shape, *rope, cos_sin, positions, q_out, q, k_new, v_new, k_pool,
-                                v_pool, k_scale, v_scale, slot_mapping, err_flag,
-                                reinterpret_cast<cudaStream_t>(stream));
+  if (bad(k_out, k_pool, k_scale) || bad(v_out, v_pool, v_scale)) return PA_ERR_INVALID_ARG;
+  return pa::run_read_cache(*shape, k_out, v_out, k_pool, v_pool, k_scale, v_scale, block_tables,
+                            seq_lens, offsets, total_tokens, starts, err_flag,
+                            reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t pa_attend_workspace_bytes(const pa_shape *shape, int32_t total_queries, int32_t sm_count) {

@@ -1,6 +1,6 @@
 // pa_extend.h -- host-side interfaces between the C ABI (pa_api.cu) and the kernels of the
-// calls with several new tokens per sequence (pa_rope.cu, pa_attend.cu).  Arguments reaching
-// these functions are already validated.
+// calls with several new tokens per sequence (pa_rope.cu, pa_attend.cu) and of reading the cache
+// back (pa_read.cu).  Arguments reaching these functions are already validated.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -20,10 +20,18 @@ pa_status run_attend(const pa_shape &s, void *out, const void *q, const int32_t 
                      int window, float sm_scale, void *workspace, int sms, int32_t *err,
                      cudaStream_t stream);
 
-pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const float *cos_sin,
+// axes: which position each pair turns by (pa_rope_axes_and_cache), or null
+pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const pa_rope_axes *axes,
+                             const float *cos_sin,
                              const int32_t *positions, void *q_out, const void *q,
                              const void *k_new, const void *v_new, void *k_pool, void *v_pool,
                              float *k_scale, float *v_scale, const int64_t *slot_mapping,
                              int32_t *err, cudaStream_t stream);
+
+// k_out or v_out may be null
+pa_status run_read_cache(const pa_shape &s, void *k_out, void *v_out, const void *k_pool,
+                         const void *v_pool, const float *k_scale, const float *v_scale,
+                         const int32_t *bt, const int32_t *sl, const int32_t *offsets, int T,
+                         const int32_t *starts, int32_t *err, cudaStream_t stream);
 
 }  // namespace pa

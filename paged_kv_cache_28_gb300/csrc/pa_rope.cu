@@ -1,5 +1,5 @@
 // pa_rope.cu -- the position rotation of a call's queries and keys, and the slot-mapped write
-// of the rotated keys and the values (pa_rope_and_cache), in one pass.
+// of the rotated keys and the values (pa_rope_and_cache, pa_rope_axes_and_cache), in one pass.
 //
 // Pair j of a head's first `rotary_dim` channels turns by the angle whose cosine and sine the
 // caller's table holds for the token's position:
@@ -18,6 +18,7 @@
 // tokens of a job in a loop and the writers' CTAs among the queries', 111 with a CTA's eight tokens
 // looked at by a warp each.
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_codec.cuh"
 #include "pa_common.cuh"
@@ -38,7 +39,33 @@ struct RopeParams {
   float *k_scale, *v_scale;
   int32_t *err;
   int T, Hq, Hkv, r, num_positions, bs, nblocks;
+  int num_axes;            // several axes: positions [num_axes, T], and pair j's axis in bits 2 j ..
+  uint32_t axes[4];
 };
+
+// The rows of the table that a token's pairs turn by: one, or one for each axis.
+struct AxisRows {
+  int pos[PA_MAX_AXES];
+};
+template <bool kAxes>
+using Place = std::conditional_t<kAxes, AxisRows, int>;
+
+template <bool kAxes>
+__device__ __forceinline__ Place<kAxes> load_place(const RopeParams &p, int t) {
+  if constexpr (kAxes) {
+    AxisRows x;
+#pragma unroll
+    for (int a = 0; a < PA_MAX_AXES; ++a)
+      x.pos[a] = p.positions[static_cast<int64_t>(a < p.num_axes ? a : 0) * p.T + t];
+    return x;
+  } else {
+    return p.positions[t];
+  }
+}
+
+__device__ __forceinline__ int axis_of(const RopeParams &p, int pair) {
+  return (p.axes[pair >> 4] >> (2 * (pair & 15))) & 3;
+}
 
 // (a, b) turned by (c, s)
 __device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
@@ -46,12 +73,22 @@ __device__ __forceinline__ float2 turn(float a, float b, float c, float s) {
                      __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)));
 }
 
-// Whether a token is written: a slot in the pool and a position in the table.
-__device__ __forceinline__ bool token_ok(const RopeParams &p, int64_t slot, int pos, bool report) {
+// Whether a token is written: a slot in the pool and its positions in the table.
+__device__ __forceinline__ bool in_table(const RopeParams &p, int pos) {
+  return pos >= 0 && pos < p.num_positions;
+}
+__device__ __forceinline__ bool in_table(const RopeParams &p, const AxisRows &at) {
+  bool in = true;
+#pragma unroll
+  for (int pos : at.pos) in = in && in_table(p, pos);
+  return in;
+}
+template <class At>
+__device__ __forceinline__ bool token_ok(const RopeParams &p, int64_t slot, const At &at, bool report) {
   if (slot < 0) return false;                            // padding
   int bits = 0;
   if (slot >= static_cast<int64_t>(p.nblocks) * p.bs) bits |= PA_DEVERR_SLOT;
-  if (pos < 0 || pos >= p.num_positions) bits |= PA_DEVERR_POSITION;
+  if (!in_table(p, at)) bits |= PA_DEVERR_POSITION;
   if (bits && report) set_err(p.err, bits);
   return bits == 0;
 }
@@ -63,7 +100,26 @@ struct Item {
   float cos[8], sin[8];
 };
 
-template <bool kInterleaved>
+// The angles of pairs j .. j + 3 (j a multiple of 4) of a token whose pair j turns by table row
+// row_of(j): together where the four share their axis.
+template <class RowOf>
+__device__ __forceinline__ void load_angles(const RopeParams &p, int j, const RowOf &row_of, float *cos,
+                                            float *sin) {
+  const uint32_t four = (p.axes[j >> 4] >> (2 * (j & 15))) & 0xFFu;
+  if (four == (four & 3u) * 0x55u) {
+    const float *row = p.cos_sin + static_cast<int64_t>(row_of(j)) * p.r + j;
+    *reinterpret_cast<float4 *>(cos) = __ldg(reinterpret_cast<const float4 *>(row));
+    *reinterpret_cast<float4 *>(sin) = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float *row = p.cos_sin + static_cast<int64_t>(row_of(j + e)) * p.r + j + e;
+      cos[e] = __ldg(row);
+      sin[e] = __ldg(row + p.r / 2);
+    }
+  }
+}
+
 __device__ __forceinline__ void load_item(const RopeParams &p, int item, int pos, Item &x) {
   x.rotates = item < p.r / 16;
   if (!x.rotates) return;
@@ -75,6 +131,19 @@ __device__ __forceinline__ void load_item(const RopeParams &p, int item, int pos
     *reinterpret_cast<float4 *>(x.cos + 4 * i) = __ldg(row + i);
     *reinterpret_cast<float4 *>(x.sin + 4 * i) = __ldg(sin_row + i);
   }
+}
+__device__ __forceinline__ void load_item(const RopeParams &p, int item, const AxisRows &at, Item &x) {
+  x.rotates = item < p.r / 16;
+  if (!x.rotates) return;
+  auto row_of = [&](int j) {
+    const int a = axis_of(p, j);
+    int pos = at.pos[0];
+#pragma unroll
+    for (int i = 1; i < PA_MAX_AXES; ++i) pos = a == i ? at.pos[i] : pos;
+    return pos;
+  };
+#pragma unroll
+  for (int i = 0; i < 2; ++i) load_angles(p, 8 * item + 4 * i, row_of, x.cos + 4 * i, x.sin + 4 * i);
 }
 
 template <bool kInterleaved>
@@ -99,7 +168,7 @@ __device__ __forceinline__ void rotate_item(const Item &x, uint4 &a, uint4 &b) {
 // Heads first, first + step, ... < last of token t, counted through the queries, then (bf16
 // pools) the keys and the values; this thread's item of each.  Four heads' loads are in flight
 // at once, the first four's before the token's slot, position and angles are there.
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kAxes>
 __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int item, int first, int step,
                                            int last, bool report) {
   constexpr int U = 4;
@@ -120,10 +189,10 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int item,
   };
   load(first);
   const int64_t slot = p.slots[t];
-  const int pos = p.positions[t];
-  if (!token_ok(p, slot, pos, report)) return;
+  const Place<kAxes> at = load_place<kAxes>(p, t);
+  if (!token_ok(p, slot, at, report)) return;
   Item x;
-  load_item<kInterleaved>(p, item, pos, x);
+  load_item(p, item, at, x);
   for (int h0 = first; h0 < last; h0 += step * U) {
     if (h0 > first) load(h0);
 #pragma unroll
@@ -143,7 +212,7 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int item,
 }
 
 // The queries alone: heads first, first + step, ... of token t (D = 128), two at a time.
-template <bool kInterleaved>
+template <bool kInterleaved, bool kAxes>
 __device__ __forceinline__ void rope_queries(const RopeParams &p, int t, int item, int first, int step) {
   constexpr int D = 128, U = 2;
   const bool split = !kInterleaved && item < p.r / 16;
@@ -162,10 +231,10 @@ __device__ __forceinline__ void rope_queries(const RopeParams &p, int t, int ite
   };
   load(first);
   const int64_t slot = p.slots[t];
-  const int pos = p.positions[t];
-  if (!token_ok(p, slot, pos, false)) return;
+  const Place<kAxes> at = load_place<kAxes>(p, t);
+  if (!token_ok(p, slot, at, false)) return;
   Item x;
-  load_item<kInterleaved>(p, item, pos, x);
+  load_item(p, item, at, x);
 #pragma unroll 1
   for (int h = first; h < p.Hq; h += U * step) {
 #pragma unroll
@@ -183,15 +252,15 @@ __device__ __forceinline__ void rope_queries(const RopeParams &p, int t, int ite
 
 // BF16 pools: blockIdx.x is the token; blockIdx.y a share of its heads.  Six CTAs an SM (80 registers)
 // keep the memory busiest: 112, 111, 109, 136 us for 16,384 tokens with 95 registers, 5, 6 and 8 CTAs.
-template <int D, bool kInterleaved>
+template <int D, bool kInterleaved, bool kAxes>
 __global__ void __launch_bounds__(128, 6) rope_bf16_kernel(const RopeParams p) {
   pdl_trigger();
   pdl_wait();
   constexpr int kItems = D / 16, kHeads = 128 / kItems;
-  rope_heads<D, kInterleaved>(p, blockIdx.x, threadIdx.x % kItems,
-                              (p.q ? 0 : p.Hq) + blockIdx.y * kHeads + threadIdx.x / kItems,
-                              gridDim.y * kHeads, p.Hq + 2 * p.Hkv,
-                              threadIdx.x == 0 && blockIdx.y == 0);
+  rope_heads<D, kInterleaved, kAxes>(p, blockIdx.x, threadIdx.x % kItems,
+                                     (p.q ? 0 : p.Hq) + blockIdx.y * kHeads + threadIdx.x / kItems,
+                                     gridDim.y * kHeads, p.Hq + 2 * p.Hkv,
+                                     threadIdx.x == 0 && blockIdx.y == 0);
 }
 
 // Quantised pools (D = 128).  `cache_ctas` CTAs write the cache, a share of `tokens` tokens each; as in
@@ -204,7 +273,7 @@ __global__ void __launch_bounds__(128, 6) rope_bf16_kernel(const RopeParams p) {
 // The scale is absmax times the fp32 reciprocal of the largest code (pa_reshape_and_cache
 // divides: the two differ by one unit in the last place at most); codes are x / scale, rounded,
 // in both.
-template <class Codec, bool kInterleaved>
+template <class Codec, bool kInterleaved, bool kAxes>
 __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens,
                                                             int shares) {
   using Word = typename Codec::Word;
@@ -223,7 +292,7 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
   const int period = gridDim.x / cache_ctas, writer = blockIdx.x / period;
   if (blockIdx.x % period != 0 || writer >= cache_ctas) {
     const int t = blockIdx.x - min(writer + 1, cache_ctas);
-    rope_queries<kInterleaved>(p, t, tid % 8, tid / 8, 32);
+    rope_queries<kInterleaved, kAxes>(p, t, tid % 8, tid / 8, 32);
     return;
   }
   const int nth = writer / shares, share = writer % shares;
@@ -232,14 +301,14 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
   // nothing to do; a warp looks at each of the CTA's.  The others look through the call: an earlier
   // token of the block leads it, and without a later one past the first 256 tokens one look is enough.
   auto same_block = [&](int u, int64_t o, int64_t blk0) {
-    return o >= blk0 && o < blk0 + p.bs && token_ok(p, o, p.positions[u], false);
+    return o >= blk0 && o < blk0 + p.bs && token_ok(p, o, load_place<kAxes>(p, u), false);
   };
   if (warp < tokens && lane == 0) {
     const int t = nth * tokens + warp;
     bool first = false;
     if (t < p.T) {
       const int64_t slot = p.slots[t], before = t > 0 ? p.slots[t - 1] : -1;
-      first = token_ok(p, slot, p.positions[t], true) &&
+      first = token_ok(p, slot, load_place<kAxes>(p, t), true) &&
               !(t > 0 && same_block(t - 1, before, slot & ~static_cast<int64_t>(p.bs - 1)));
     }
     first_of_run[warp] = first;
@@ -312,11 +381,25 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
             if (i0 + i >= n) break;
             if (!is_v) {
               const float v[4] = {bf16_lo(x[i].x), bf16_hi(x[i].x), bf16_lo(x[i].y), bf16_hi(x[i].y)};
-              const float *row = p.cos_sin + static_cast<int64_t>(p.positions[members[i0 + i]]) * p.r + j;
+              // the table row of pair a, and its place from pair j on
+              auto row_of = [&](int a) {
+                if constexpr (kAxes)
+                  return p.positions[static_cast<int64_t>(axis_of(p, a)) * p.T + members[i0 + i]];
+                else
+                  return p.positions[members[i0 + i]];
+              };
+              const float *row = p.cos_sin + static_cast<int64_t>(row_of(kAxes && !turns ? 0 : j)) * p.r + j;
               if constexpr (kInterleaved) {
                 if (turns) {
-                  const float2 c = __ldg(reinterpret_cast<const float2 *>(row));
-                  const float2 sn = __ldg(reinterpret_cast<const float2 *>(row + p.r / 2));
+                  float2 c, sn;
+                  if (!kAxes || axis_of(p, j) == axis_of(p, j + 1)) {
+                    c = __ldg(reinterpret_cast<const float2 *>(row));
+                    sn = __ldg(reinterpret_cast<const float2 *>(row + p.r / 2));
+                  } else {
+                    const float *next = p.cos_sin + static_cast<int64_t>(row_of(j + 1)) * p.r + j + 1;
+                    c = make_float2(__ldg(row), __ldg(next));
+                    sn = make_float2(__ldg(row + p.r / 2), __ldg(next + p.r / 2));
+                  }
                   const float2 y = turn(v[0], v[1], c.x, sn.x), z = turn(v[2], v[3], c.y, sn.y);
                   x[i] = make_uint2(pack_bf16(y.x, y.y), pack_bf16(z.x, z.y));
                 }
@@ -325,9 +408,15 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
                 const uint32_t w1 = __shfl_sync(0xffffffffu, x[i].y, peer);
                 const float w[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
                 if (turns) {
-                  const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
-                  const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
-                  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+                  alignas(16) float cc[4], ss[4];
+                  if constexpr (kAxes) {
+                    load_angles(p, j, row_of, cc, ss);
+                  } else {
+                    const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
+                    const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
+                    cc[0] = c.x, cc[1] = c.y, cc[2] = c.z, cc[3] = c.w;
+                    ss[0] = sn.x, ss[1] = sn.y, ss[2] = sn.z, ss[3] = sn.w;
+                  }
                   float y[4];                            // a cos - b sin, or b cos + a sin
 #pragma unroll
                   for (int e = 0; e < 4; ++e)
@@ -392,16 +481,16 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
   }
 }
 
-template <int D, bool I>
+template <int D, bool I, bool A>
 cudaError_t launch_bf16(const RopeParams &p, cudaStream_t stream) {
   // few tokens: their heads go over several CTAs, about two per SM
   constexpr int kHeads = 128 / (D / 16);
   const int heads = p.Hq + 2 * p.Hkv;
   const int shares = std::max(1, std::min((heads + kHeads - 1) / kHeads, 304 / p.T));
-  return launch_pdl(rope_bf16_kernel<D, I>, dim3(p.T, shares), dim3(128), 0, stream, p);
+  return launch_pdl(rope_bf16_kernel<D, I, A>, dim3(p.T, shares), dim3(128), 0, stream, p);
 }
 
-template <class Codec, bool I>
+template <class Codec, bool I, bool A>
 cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
   // a prompt's tokens mostly leave at once, so a CTA looks at several; a batch's stay
   const int tokens = p.T >= 2048 ? 8 : 1;
@@ -409,16 +498,24 @@ cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
   const int shares = p.T >= 1024 ? 1 : (2 * p.Hkv + 7) / 8;
   const int cache_ctas = (p.T + tokens - 1) / tokens * shares;
   const size_t smem = 8 * 32 * sizeof(typename Codec::Word) * p.bs;
-  const cudaError_t e = cudaFuncSetAttribute(rope_quant_kernel<Codec, I>,
+  const cudaError_t e = cudaFuncSetAttribute(rope_quant_kernel<Codec, I, A>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, 32 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_pdl(rope_quant_kernel<Codec, I>, dim3(cache_ctas + (p.q ? p.T : 0)), dim3(256), smem,
+  return launch_pdl(rope_quant_kernel<Codec, I, A>, dim3(cache_ctas + (p.q ? p.T : 0)), dim3(256), smem,
                     stream, p, cache_ctas, tokens, shares);
+}
+
+template <bool I, bool A>
+cudaError_t launch_kind(const pa_shape &s, const RopeParams &p, cudaStream_t stream) {
+  if (s.kv_dtype == PA_KV_FP8_E4M3) return launch_quant<Fp8Codec, I, A>(p, stream);
+  if (s.kv_dtype == PA_KV_INT4) return launch_quant<Int4Codec, I, A>(p, stream);
+  return s.D == 128 ? launch_bf16<128, I, A>(p, stream) : launch_bf16<64, I, A>(p, stream);
 }
 
 }  // namespace
 
-pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const float *cos_sin,
+pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const pa_rope_axes *axes,
+                             const float *cos_sin,
                              const int32_t *positions, void *q_out, const void *q,
                              const void *k_new, const void *v_new, void *k_pool, void *v_pool,
                              float *k_scale, float *v_scale, const int64_t *slot_mapping,
@@ -448,14 +545,14 @@ pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const float
   p.nblocks = s.nblocks;
   const bool i = rope.interleaved;
   cudaError_t e;
-  if (s.kv_dtype == PA_KV_FP8_E4M3)
-    e = i ? launch_quant<Fp8Codec, true>(p, stream) : launch_quant<Fp8Codec, false>(p, stream);
-  else if (s.kv_dtype == PA_KV_INT4)
-    e = i ? launch_quant<Int4Codec, true>(p, stream) : launch_quant<Int4Codec, false>(p, stream);
-  else if (s.D == 128)
-    e = i ? launch_bf16<128, true>(p, stream) : launch_bf16<128, false>(p, stream);
-  else
-    e = i ? launch_bf16<64, true>(p, stream) : launch_bf16<64, false>(p, stream);
+  if (axes) {
+    p.num_axes = axes->num_axes;
+    for (int j = 0; j < rope.rotary_dim / 2; ++j)
+      p.axes[j / 16] |= static_cast<uint32_t>(axes->pair_axis[j]) << (2 * (j % 16));
+    e = i ? launch_kind<true, true>(s, p, stream) : launch_kind<false, true>(s, p, stream);
+  } else {
+    e = i ? launch_kind<true, false>(s, p, stream) : launch_kind<false, false>(s, p, stream);
+  }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
