@@ -537,8 +537,65 @@ pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
 size_t pa_attend_workspace_bytes(const pa_shape *shape, int32_t total_queries, int32_t sm_count);
 
 /*
- * Positions with several axes, and reading the cache back.
+ * Attention whose scores are changed before their softmax, positions with several axes, and the
+ * cache read back.
  */
+
+/*
+ * The score of a query at position p with a key at position j is
+ *     a = sm_scale <q, K[j]>;   softcap > 0: a = softcap tanh(a / softcap);
+ *     slopes: a = a - slopes[h] |p - j|
+ * in this order, in fp32.
+ *   softcap  in [1e-10, 1e10]: scores stay within +-softcap.  0: none
+ *   slopes   [Hq] fp32 device array or NULL: a bias that falls with distance, for query head h.
+ *            Finite; any sign.
+ *   prefix_lens  [B] int32 device array or NULL (pa_extend_scored): the first prefix_lens[b]
+ *            positions of sequence b see one another whatever their order (an image, an
+ *            instruction): a token at position p sees j <= max(p, prefix_lens[b] - 1), as far as
+ *            the cache holds them: a prefix whose tokens are appended by several calls is whole
+ *            for the last of them only.  At most 0: none.  (The last token of a sequence sees no
+ *            more for it: pa_decode_scored does not look at it.)
+ */
+typedef struct {
+    float softcap;
+    const float *slopes;
+    const int32_t *prefix_lens;
+} pa_score;
+
+/*
+ * pa_extend_scored -- pa_extend with changed scores:
+ *     out[row][h][:] = sum_j softmax_j(a) V_b[j]
+ * over the j that the row sees; a window bounds them below as in pa_extend (p - window < j).  What
+ * pa_extend says of its arguments, workspace (pa_attend_workspace_bytes), cached values, errors,
+ * rounding and limits holds here; the capped score is off by 2^-20 of itself at most.  A score with
+ * neither cap, slopes nor prefix gives pa_extend's result.
+ */
+pa_status pa_extend_scored(const pa_shape *shape, void *out, const void *q,
+                           const int32_t *query_offsets, int32_t total_queries,
+                           const void *k_pool, const void *v_pool, const float *k_scale,
+                           const float *v_scale, const int32_t *block_tables,
+                           const int32_t *seq_lens, int32_t window, const pa_score *score,
+                           float sm_scale, void *workspace, size_t workspace_bytes,
+                           int32_t *err_flag, pa_stream_t stream);
+
+/*
+ * pa_decode_scored -- the same for one token per sequence, the last of its seq_lens[b] cached ones
+ * (p = seq_lens[b] - 1): pa_decode's load-balanced split decode and merge with changed scores and
+ * a bf16 output.
+ *   q, out     [B, Hq, D] bf16 (out must not overlap q)
+ *   window     > 0: the last `window` positions only, as in pa_decode_opts
+ *   workspace  device memory of pa_decode_workspace_bytes(shape, n) bytes, 256-byte aligned, n =
+ *              num_segments, or pa_default_num_segments for this GPU when num_segments is 0; calls
+ *              that may overlap on the GPU need one each
+ * seq_lens[b] = 0 gives zeros.  The result is the same on every call, bit for bit.  Batches of more
+ * than 16384 sequences return PA_ERR_UNSUPPORTED.
+ */
+pa_status pa_decode_scored(const pa_shape *shape, void *out, const void *q, const void *k_pool,
+                           const void *v_pool, const float *k_scale, const float *v_scale,
+                           const int32_t *block_tables, const int32_t *seq_lens, int32_t window,
+                           const pa_score *score, float sm_scale, void *workspace,
+                           size_t workspace_bytes, int32_t num_segments, int32_t *err_flag,
+                           pa_stream_t stream);
 
 #define PA_MAX_AXES 4
 

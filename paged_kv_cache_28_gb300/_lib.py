@@ -25,7 +25,8 @@ EXPORTED = ("pa_reshape_and_cache", "pa_decode", "pa_splitkv_workspace_bytes",
             "pa_read_error_flag", "pa_decode_splitkv_noalloc", "pa_quest_summarize",
             "pa_quest_select", "pa_cascade_workspace_bytes", "pa_decode_workspace_bytes",
             "pa_default_num_segments", "pa_rope_and_cache", "pa_extend", "pa_cross_attend",
-            "pa_attend_workspace_bytes", "pa_rope_axes_and_cache", "pa_read_cache")
+            "pa_attend_workspace_bytes", "pa_extend_scored", "pa_decode_scored",
+            "pa_rope_axes_and_cache", "pa_read_cache")
 PA_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -44,6 +45,11 @@ class pa_rope(ctypes.Structure):
 
 class pa_rope_axes(ctypes.Structure):
     _fields_ = [("num_axes", ctypes.c_int32), ("pair_axis", ctypes.c_uint8 * 64)]
+
+
+class pa_score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
 
 
 class pa_decode_opts(ctypes.Structure):
@@ -101,7 +107,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                               "`python -m paged_kv_cache_28_gb300.build` (needs nvcc)")
         lib = ctypes.CDLL(path)
         P, I32, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float
-        S = ctypes.POINTER(pa_shape)
+        S, C = ctypes.POINTER(pa_shape), ctypes.POINTER(pa_score)
         sig = {
             "pa_reshape_and_cache": (I32, [S, P, P, P, P, P, P, P, P, P]),
             "pa_decode": (I32, [S, P, P, P, P, P, P, P, P, P, F, P, P]),
@@ -122,6 +128,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                 P]),
             "pa_cross_attend": (I32, [S, P, P, P, I32, P, P, P, P, P, P, F, P, ctypes.c_size_t, P,
                                       P]),
+            "pa_extend_scored": (I32, [S, P, P, P, I32, P, P, P, P, P, P, I32, C, F, P,
+                                       ctypes.c_size_t, P, P]),
+            "pa_decode_scored": (I32, [S, P, P, P, P, P, P, P, P, I32, C, F, P, ctypes.c_size_t, I32,
+                                       P, P]),
             "pa_rope_axes_and_cache": (I32, [S, ctypes.POINTER(pa_rope),
                                              ctypes.POINTER(pa_rope_axes)] + [P] * 13),
             "pa_read_cache": (I32, [S, P, P, P, P, P, P, P, P, P, I32, P, P, P]),
@@ -337,6 +347,33 @@ def pa_rope_and_cache(shape: pa_shape, cos_sin, positions, q_out, q, k_new, v_ne
         ctypes.byref(shape), ctypes.byref(rope), _ptr(cos_sin), _ptr(positions), _ptr(q_out), qp,
         kp, vp, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(slot_mapping),
         _ptr(err_flag), _stream(stream)))
+
+
+def pa_extend_scored(shape: pa_shape, out, q, query_offsets, k_pool, v_pool, k_scale, v_scale,
+                     block_tables, seq_lens, sm_scale: float, workspace, err_flag=None, stream=None,
+                     window: int = 0, softcap: float = 0.0, slopes=None, prefix_lens=None) -> None:
+    """pa_extend with scores capped by softcap (0: not), a bias that falls with distance (slopes
+    [Hq] fp32) and prefixes that see all of themselves (prefix_lens [B] int32)."""
+    score = pa_score(float(softcap), _ptr(slopes), _ptr(prefix_lens))
+    _check("pa_extend_scored", load().pa_extend_scored(
+        ctypes.byref(shape), _ptr(out), _ptr(q), _ptr(query_offsets), int(q.shape[0]),
+        _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
+        _ptr(seq_lens), int(window), ctypes.byref(score), float(sm_scale), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+
+
+def pa_decode_scored(shape: pa_shape, out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
+                     seq_lens, sm_scale: float, workspace, err_flag=None, stream=None,
+                     window: int = 0, softcap: float = 0.0, slopes=None,
+                     num_segments: int = 0) -> None:
+    """One token per sequence with changed scores: q, out [B, Hq, D] bf16; workspace: uint8 tensor
+    of pa_decode_workspace_bytes(shape, num_segments or pa_default_num_segments)."""
+    score = pa_score(float(softcap), _ptr(slopes), None)
+    _check("pa_decode_scored", load().pa_decode_scored(
+        ctypes.byref(shape), _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
+        _ptr(v_scale), _ptr(block_tables), _ptr(seq_lens), int(window), ctypes.byref(score),
+        float(sm_scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        int(num_segments), _ptr(err_flag), _stream(stream)))
 
 
 @functools.lru_cache(maxsize=64)

@@ -123,15 +123,23 @@ pa_status check_attend_shape(const pa_shape *s, int32_t total_queries) {
   return s->B > pa::kMaxSplitBatch ? PA_ERR_UNSUPPORTED : PA_OK;
 }
 
-// pa_extend (causal) and pa_cross_attend.
+bool bad_score(const pa_score &s) {
+  auto unaligned = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+  // (a NaN is neither)
+  return !(s.softcap == 0.f || (s.softcap >= 1e-10f && s.softcap <= 1e10f)) || unaligned(s.slopes) ||
+         unaligned(s.prefix_lens);
+}
+
+// pa_extend (causal), pa_cross_attend and, given a score, pa_extend_scored.
 pa_status attend(const pa_shape *shape, void *out, const void *q, const int32_t *query_offsets,
                  int32_t total_queries, const void *k_pool, const void *v_pool,
                  const float *k_scale, const float *v_scale, const int32_t *block_tables,
-                 const int32_t *seq_lens, bool causal, int32_t window, float sm_scale,
-                 void *workspace, size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream) {
+                 const int32_t *seq_lens, bool causal, int32_t window, const pa_score *score,
+                 float sm_scale, void *workspace, size_t workspace_bytes, int32_t *err_flag,
+                 pa_stream_t stream) {
   pa_status st = check_attend_shape(shape, total_queries);
   if (st != PA_OK) return st;
-  if (window < 0) return PA_ERR_INVALID_ARG;
+  if (window < 0 || (score && bad_score(*score))) return PA_ERR_INVALID_ARG;
   if (shape->B == 0 || total_queries == 0) return PA_OK;
   st = check_ptrs({out, q, query_offsets, k_pool, v_pool, block_tables, seq_lens, workspace});
   if (st != PA_OK) return st;
@@ -142,6 +150,16 @@ pa_status attend(const pa_shape *shape, void *out, const void *q, const int32_t 
   const size_t need = pa::attend_workspace_bytes(*shape, total_queries, sms);
   if (need == 0) return PA_ERR_UNSUPPORTED;
   if (workspace_bytes < need) return PA_ERR_INVALID_ARG;
+  if (score && (score->softcap > 0.f || score->slopes || score->prefix_lens)) {
+    const pa::ScoredCall call{*shape,  out,          q,        query_offsets, total_queries, k_pool,
+                              v_pool,  k_scale,      v_scale,  block_tables,  seq_lens,      window,
+                              *score,  sm_scale,     workspace, sms,          err_flag,
+                              reinterpret_cast<cudaStream_t>(stream)};
+    if (score->softcap > 0.f)
+      return score->slopes ? pa::run_attend_scored<pa::kCap | pa::kBias>(call)
+                           : pa::run_attend_scored<pa::kCap>(call);
+    return score->slopes ? pa::run_attend_scored<pa::kBias>(call) : pa::run_attend_scored<0>(call);
+  }
   return pa::run_attend(*shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale,
                         v_scale, block_tables, seq_lens, causal, window, sm_scale, workspace, sms,
                         err_flag, reinterpret_cast<cudaStream_t>(stream));
@@ -391,8 +409,49 @@ pa_status pa_extend(const pa_shape *shape, void *out, const void *q, const int32
                     const int32_t *seq_lens, int32_t window, float sm_scale, void *workspace,
                     size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream) {
   return attend(shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale, v_scale,
-                block_tables, seq_lens, true, window, sm_scale, workspace, workspace_bytes,
+                block_tables, seq_lens, true, window, nullptr, sm_scale, workspace, workspace_bytes,
                 err_flag, stream);
+}
+
+pa_status pa_extend_scored(const pa_shape *shape, void *out, const void *q,
+                           const int32_t *query_offsets, int32_t total_queries,
+                           const void *k_pool, const void *v_pool, const float *k_scale,
+                           const float *v_scale, const int32_t *block_tables,
+                           const int32_t *seq_lens, int32_t window, const pa_score *score,
+                           float sm_scale, void *workspace, size_t workspace_bytes,
+                           int32_t *err_flag, pa_stream_t stream) {
+  if (!score) return PA_ERR_INVALID_ARG;
+  return attend(shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale, v_scale,
+                block_tables, seq_lens, true, window, score, sm_scale, workspace, workspace_bytes,
+                err_flag, stream);
+}
+
+pa_status pa_decode_scored(const pa_shape *shape, void *out, const void *q, const void *k_pool,
+                           const void *v_pool, const float *k_scale, const float *v_scale,
+                           const int32_t *block_tables, const int32_t *seq_lens, int32_t window,
+                           const pa_score *score, float sm_scale, void *workspace,
+                           size_t workspace_bytes, int32_t num_segments, int32_t *err_flag,
+                           pa_stream_t stream) {
+  pa_status st = check_shape(shape);
+  if (st != PA_OK) return st;
+  if (!score || bad_score(*score) || window < 0 || num_segments < 0 || num_segments > kMaxSplits)
+    return PA_ERR_INVALID_ARG;
+  if (shape->B > pa::kMaxSplitBatch) return PA_ERR_UNSUPPORTED;
+  if (shape->B == 0) return PA_OK;
+  st = check_ptrs({out, q, k_pool, v_pool, block_tables, seq_lens, workspace});
+  if (st != PA_OK) return st;
+  if (shape->kv_dtype != PA_KV_BF16 && (!k_scale || !v_scale)) return PA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return PA_ERR_INVALID_ARG;
+  int segments = num_segments;
+  if (segments == 0) {
+    int sms = 0;
+    if (current_sm_count(&sms) != PA_OK) return PA_ERR_CUDA;
+    segments = resident_segments(shape, sms);
+  }
+  if (workspace_bytes < pa::splitkv_layout(*shape, segments).total) return PA_ERR_INVALID_ARG;
+  return pa::run_decode_scored(*shape, out, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens,
+                               window, *score, sm_scale, workspace, segments, err_flag,
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
@@ -402,8 +461,8 @@ pa_status pa_cross_attend(const pa_shape *shape, void *out, const void *q,
                           const int32_t *seq_lens, float sm_scale, void *workspace,
                           size_t workspace_bytes, int32_t *err_flag, pa_stream_t stream) {
   return attend(shape, out, q, query_offsets, total_queries, k_pool, v_pool, k_scale, v_scale,
-                block_tables, seq_lens, false, 0, sm_scale, workspace, workspace_bytes, err_flag,
-                stream);
+                block_tables, seq_lens, false, 0, nullptr, sm_scale, workspace, workspace_bytes,
+                err_flag, stream);
 }
 
 const char *pa_status_string(pa_status status) {
