@@ -49,6 +49,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "pa_common.cuh"
 #include "pa_extend.h"
@@ -82,6 +83,7 @@ struct AttendParams {
   const float *slopes;                  // [Hq], with kBias
   const int32_t *prefix_lens;           // [B], or null
   float cap2;                           // cap log2(e), with kCap
+  float2 near[6];                       // cap2 times tanh's coefficients within 1
 };
 
 // ------------------------------------------------------------------ units of work
@@ -422,6 +424,17 @@ __device__ __forceinline__ void tc_ld32(uint32_t *r, uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tc_ld16(uint32_t *r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : PA_R8(r, 0), PA_R8(r, 8)
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld16(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : PA_W8(r, 0), PA_W8(r, 8)::"memory");
+}
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
@@ -628,6 +641,12 @@ struct RingOrder {
 
 // kKind: the pools' pa_kv_dtype.  Codes (D = 128) are restored to bf16 tiles, without their scale,
 // by eight warps of their own: K's scale multiplies the scores of a page, V's its weights.
+// What a row's registers hold when its weights are computed: scores, scores to be capped, or the
+// weights' exponents but for the reference.
+constexpr int kScores = 0, kCapped = 1, kExponents = 2;
+template <int k>
+using Kind = std::integral_constant<int, k>;
+
 // kScore: what changes the scores (kCap, kBias).
 template <int kD, int kKind, bool kShared, int kScore = 0>
 struct AttendCfg {
@@ -635,6 +654,9 @@ struct AttendCfg {
   static constexpr bool SHARED = kShared, QUANT = kKind != PA_KV_BF16;
   static constexpr bool CAP = kScore & kCap, BIAS = kScore & kBias;
   static constexpr bool CHANGED = kScore != 0;
+  // A piece's key tiles last to first: where scores fall with distance the first tile then holds the
+  // largest, and the reference maximum hardly ever moves again.
+  static constexpr bool REVERSE = BIAS;
   static constexpr int HALVES = D / 64;                 // 128-byte column chunks of a bf16 row
   static constexpr int TILE = kKeys * D * 2;            // bytes of a Q, K or V tile
   static constexpr int CODE_ROW = KIND == PA_KV_INT4 ? 64 : 128;
@@ -887,7 +909,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       // weights are out (see SCALES); from then on this row tile keeps up.
       if constexpr (C::QUANT && C::SHARED) ok = mbar_wait(s_full(t), s_phase);
       for (int i = 0; i < n_tiles; ++i) {
-        const int key0 = (tile_0 + i) * kKeys;
+        const int key0 = (tile_0 + (C::REVERSE ? n_tiles - 1 - i : i)) * kKeys;
         // code pools: the scales of the tile's pages, K's then V's
         [[maybe_unused]] uint32_t sc = 0;
         if constexpr (C::QUANT) {
@@ -916,47 +938,87 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const bool edge = key0 < all_lo || key0 + kKeys > all_hi;
           const int first = lo - key0;                   // columns [first, first + seen) count
           const unsigned seen = static_cast<unsigned>(max(0, hi - lo));
-          auto hide = [&](uint32_t *s, int j0) {         // columns [j0, j0 + 32) of the row
+          auto hide = [&](uint32_t *s, int j0, float hidden = -INFINITY) {   // columns [j0, j0 + 32) of the row
             if (edge) {
 #pragma unroll
               for (int j = 0; j < 32; ++j)
-                if (static_cast<unsigned>(j0 + j - first) >= seen) s[j] = __float_as_uint(-INFINITY);
+                if (static_cast<unsigned>(j0 + j - first) >= seen) s[j] = __float_as_uint(hidden);
             }
           };
           // what the scores of a block's two pages are multiplied by
           auto k_factors = [&](int block) {
             return C::QUANT ? lds_f32x2(sc + 8 * block) : make_float2(p.c, p.c);
           };
-          // Changed scores: columns [j0, j0 + 32) become the weights' exponents before the maximum
-          // is taken from them.
-          [[maybe_unused]] auto change = [&](uint32_t *s, int j0, float2 f) {
-            if constexpr (C::CAP) {
-              bool far = false;
+          // A capped tile whose scores pass the cap has their exponents in TMEM in their place.
+          [[maybe_unused]] bool far = false;
+          [[maybe_unused]] float hidden = -INFINITY;     // what makes a score's weight 0
+          [[maybe_unused]] float peak = 0.f;             // the largest |score| over the cap
+          [[maybe_unused]] auto look = [&](const uint32_t *s, float2 f) {
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                const float g = j < 16 ? f.x : f.y;
-                const float2 t = mul2(make_float2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), make_float2(g, g));
-                s[j] = __float_as_uint(t.x);
-                s[j + 1] = __float_as_uint(t.y);
-                far |= fmaxf(fabsf(t.x), fabsf(t.y)) > 1.f;
+            for (int j = 0; j < 32; j += 16) {
+              float y[2] = {0.f, 0.f};
+#pragma unroll
+              for (int e = j; e < j + 16; e += 4) {
+                y[0] = fmaxf(y[0], fmaxf(fabsf(__uint_as_float(s[e])), fabsf(__uint_as_float(s[e + 1]))));
+                y[1] = fmaxf(y[1], fmaxf(fabsf(__uint_as_float(s[e + 2])), fabsf(__uint_as_float(s[e + 3]))));
               }
-              if (__any_sync(0xffffffffu, far && live)) {
+              peak = fmaxf(peak, fmaxf(y[0], y[1]) * (j ? f.y : f.x));
+            }
+          };
+          // Exponents of block j's columns, past the cap, in TMEM.
+          [[maybe_unused]] auto cap_far = [&](int block, float2 f) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+              const float g = half ? f.y : f.x;
+              uint32_t o[16];
+              tc_ld16(o, tS + 32 * block + 16 * half);
+              tc_wait_ld16(o);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(p.cap2 * tanh_any(__uint_as_float(s[j])));
-              } else {
+              for (int e = 0; e < 16; ++e)
+                o[e] = __float_as_uint(p.cap2 * tanh_any(__uint_as_float(o[e]) * g));
+              tc_st16(tS + 32 * block + 16 * half, o);
+            }
+          };
+          [[maybe_unused]] auto is_far = [&] { return __any_sync(0xffffffffu, live && peak > 1.f); };
+          // Two capped scores, times log2(e), plus shift (not those of a far tile).  A score of +inf
+          // gives -inf, the sign of the last coefficient.
+          [[maybe_unused]] auto capped = [&](float2 s, float g, float2 shift) {
+            const float2 t = mul2(s, make_float2(g, g)), u = mul2(t, t);
+            float2 y = fma2(u, p.near[5], p.near[4]);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = __float_as_uint(p.cap2 * tanh_within_1(__uint_as_float(s[j])));
+            for (int i = 3; i >= 0; --i) y = fma2(u, y, p.near[i]);
+            return fma2(t, y, shift);
+          };
+          // Scores that fall with distance: columns [j0, j0 + 32) become exponents in place.
+          [[maybe_unused]] auto biased = [&](uint32_t *s, int j0, float2 f) {
+            if constexpr (C::CAP) {
+              if (!far) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  const float2 y = capped(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
+                                          e < 16 ? f.x : f.y, make_float2(0.f, 0.f));
+                  s[e] = __float_as_uint(y.x);
+                  s[e + 1] = __float_as_uint(y.y);
+                }
               }
             }
-            if constexpr (C::BIAS) {
-              const float d = static_cast<float>(key0 + j0 - pos);
-              const bool ahead = key0 + j0 + 31 > x.pos + tok0 && x.prefix > 0;   // some key after its query
+            const float d = static_cast<float>(key0 + j0 - pos);
+            float2 r = make_float2(slope * d, slope * (d + 1.f));
+            const float2 step = make_float2(2.f * slope, 2.f * slope);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float a = C::CAP ? __uint_as_float(s[j]) : __uint_as_float(s[j]) * (j < 16 ? f.x : f.y);
-                const float at = d + static_cast<float>(j);
-                s[j] = __float_as_uint(fmaf(slope, ahead ? -fabsf(at) : at, a));
-              }
+            for (int e = 0; e < 32; e += 2) {
+              const float g = C::CAP ? 1.f : e < 16 ? f.x : f.y;
+              const float2 y = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+              const float2 x = C::CAP ? add2(y, r) : fma2(y, make_float2(g, g), r);
+              s[e] = __float_as_uint(x.x);
+              s[e + 1] = __float_as_uint(x.y);
+              r = add2(r, step);
+            }
+            // keys ahead of their query (in a prefix): the distance counts the other way
+            if (key0 + j0 + 31 > x.pos + tok0 && x.prefix > 0) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                s[e] = __float_as_uint(fmaf(-2.f * slope, fmaxf(d + static_cast<float>(e), 0.f), __uint_as_float(s[e])));
             }
           };
           float mx[2] = {-INFINITY, -INFINITY};
@@ -970,12 +1032,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 y[1] = fmaxf(y[1], fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
               }
               const float page = fmaxf(y[0], y[1]);
-              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT && !C::CHANGED ? page * (j ? f.y : f.x) : page);
+              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT && !C::BIAS ? page * (j ? f.y : f.x) : page);
             }
           };
           // A block of 32 columns is on its way while another is worked on.  bf16 pools: the row's
           // scores stay in registers; code pools, whose threads have fewer, read half of them twice.
           uint32_t s[C::QUANT ? 64 : kKeys];
+          [[maybe_unused]] bool far_2 = false;           // the tile's second half
           if constexpr (C::QUANT) {
 #pragma unroll 1
             for (int j = 2; j >= 0; j -= 2) {            // blocks j and j + 1
@@ -984,9 +1047,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
               tc_wait_ld32(s);
               tc_use32(s + 32);
-              if constexpr (C::CHANGED) {
-                change(s, 32 * j, f0);
-                change(s + 32, 32 * j + 32, f1);
+              if constexpr (C::CAP) {
+                look(s, f0);
+                look(s + 32, f1);
+                if constexpr (C::BIAS) {                 // each half of the tile by itself
+                  far = is_far();
+                  if (far) {
+                    cap_far(j, f0);
+                    cap_far(j + 1, f1);
+                    tc_wait_st();
+                    tc_ld32(s, tS + 32 * j);
+                    tc_ld32(s + 32, tS + 32 * j + 32);
+                    tc_wait_ld32(s);
+                    tc_use32(s + 32);
+                  }
+                  if (j > 0) far_2 = far;
+                  peak = 0.f;
+                }
+              }
+              if constexpr (C::BIAS) {
+                biased(s, 32 * j, f0);
+                biased(s + 32, 32 * j + 32, f1);
               }
               hide(s, 32 * j);
               maximum(s, f0);
@@ -1004,15 +1085,51 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_ld32(s + 64, tS + 64);
                 tc_ld32(s + 96, tS + 96);
               }
+              if constexpr (C::CAP && C::BIAS) {         // each half of the tile by itself
+                peak = 0.f;
+                look(s + 64 * half, make_float2(p.c, p.c));
+                look(s + 64 * half + 32, make_float2(p.c, p.c));
+                far = is_far();
+                if (far) {
+                  tc_wait_ld32(s + 64);                  // (the other half's loads are still on their way)
+                  tc_use32(s + 96);
+                  cap_far(2 * half, make_float2(p.c, p.c));
+                  cap_far(2 * half + 1, make_float2(p.c, p.c));
+                  tc_wait_st();
+                  tc_ld32(s + 64 * half, tS + 64 * half);
+                  tc_ld32(s + 64 * half + 32, tS + 64 * half + 32);
+                  tc_wait_ld32(s + 64 * half);
+                  tc_use32(s + 64 * half + 32);
+                }
+              }
 #pragma unroll
               for (int j = 64 * half; j < 64 * half + 64; j += 32) {
-                if constexpr (C::CHANGED) change(s + j, j, make_float2(p.c, p.c));
+                if constexpr (C::CAP && !C::BIAS) look(s + j, make_float2(p.c, p.c));
+                if constexpr (C::BIAS) biased(s + j, j, make_float2(p.c, p.c));
                 hide(s + j, j);
                 maximum(s + j, make_float2(1.f, 1.f));
               }
             }
           }
-          const float top = fmaxf(mx[0], mx[1]) * (C::QUANT || C::CHANGED ? 1.f : p.c);
+          float top = fmaxf(mx[0], mx[1]) * (C::QUANT || C::BIAS ? 1.f : p.c);
+          if constexpr (C::CAP && !C::BIAS) {
+            // the cap rises with the score, so the largest capped score is the largest score's
+            top = top == -INFINITY ? top : p.cap2 * tanh_any(top);
+            far = is_far();
+            if (far) {
+#pragma unroll 1
+              for (int j = 0; j < 4; ++j) cap_far(j, k_factors(j));
+              tc_wait_st();
+#pragma unroll
+              for (int j = 0; j < (C::QUANT ? 64 : kKeys); j += 32) tc_ld32(s + j, tS + j);
+              tc_wait_ld32(s);
+#pragma unroll
+              for (int j = 32; j < (C::QUANT ? 64 : kKeys); j += 32) tc_use32(s + j);
+            }
+            hidden = far ? -INFINITY : INFINITY;
+#pragma unroll
+            for (int j = 0; j < (C::QUANT ? 64 : kKeys); j += 32) hide(s + j, j, hidden);
+          }
           if (m == -INFINITY) m = top;                   // O and l are zero so far
           // the reference moves only past kMaxJump octaves: weights stay below 2^8, far
           // inside bf16 and fp32, and O is seldom rescaled
@@ -1035,7 +1152,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           // The weights of block j, over columns that are already read.  Code pools: V's scale enters
           // in the exponent, and leaves the sums of its page again.
           float2 sum[2] = {};
-          auto weights = [&](const uint32_t *s, int j, float2 f) {
+          auto weights = [&](const uint32_t *s, int j, float2 f, auto kind) {
+            constexpr int kKind = decltype(kind)::value;
             float2 v = make_float2(0.f, 0.f);
             if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
             uint32_t packed[16];
@@ -1048,10 +1166,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
               for (int e = 8 * half; e < 8 * half + 8; ++e) {
                 float2 y = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                if constexpr (C::CHANGED)
-                  y = add2(y, shift);
-                else
+                if constexpr (kKind == kScores)
                   y = fma2(y, make_float2(c1, c1), shift);
+                else if constexpr (kKind == kCapped)
+                  y = capped(y, c1, shift);
+                else
+                  y = add2(y, shift);
                 y.x = ex2(y.x);
                 y.y = ex2(y.y);
                 float2 &to = C::QUANT ? page[e & 1] : sum[e & 1];
@@ -1079,21 +1199,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               if (j > 0) {
                 tc_wait_ld32(s);
                 tc_use32(s + 32);
-                if constexpr (C::CHANGED) {
-                  change(s, 64, f0);
-                  change(s + 32, 96, f1);
+                if constexpr (C::BIAS) {
+                  far = far_2;
+                  biased(s, 64, f0);
+                  biased(s + 32, 96, f1);
                 }
-                hide(s, 64);
-                hide(s + 32, 96);
+                hide(s, 64, hidden);
+                hide(s + 32, 96, hidden);
               }
-              weights(s, j, f0);
+              auto of_block = [&](const uint32_t *s, int j, float2 f) {
+                if constexpr (!C::CHANGED)
+                  weights(s, j, f, Kind<kScores>{});
+                else if (C::BIAS || far)
+                  weights(s, j, f, Kind<kExponents>{});
+                else
+                  weights(s, j, f, Kind<kCapped>{});
+              };
+              of_block(s, j, f0);
               if (j == 0) tc_ld32(s, tS + 64);           // columns that are not written over yet
-              weights(s + 32, j + 1, f1);
+              of_block(s + 32, j + 1, f1);
               if (j == 0) tc_ld32(s + 32, tS + 96);
             }
           } else {
+            auto all = [&](auto kind) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) weights(s + 32 * j, j, make_float2(p.c, p.c));
+              for (int j = 0; j < 4; ++j) weights(s + 32 * j, j, make_float2(p.c, p.c), kind);
+            };
+            if constexpr (!C::CHANGED)
+              all(Kind<kScores>{});
+            else if (C::BIAS || far)
+              all(Kind<kExponents>{});
+            else
+              all(Kind<kCapped>{});
           }
           tc_wait_st();
           tc_fence_before();
@@ -1220,8 +1357,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         if (over) return c;
         c.h = x.h;
-        c.tile = x.tile + at;
         c.n = min(4, x.n - at);
+        c.tile = x.tile + (C::REVERSE ? x.n - at - c.n : at);
         at += c.n;
         c.row = -1;
         const int g = c.tile * kKeys + 16 * lane;
@@ -1271,7 +1408,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             next = 0;
             if (!ok) break;
           }
-          here = next++;
+          here = C::REVERSE ? cur.n - 1 - next : next;
+          ++next;
           if constexpr (C::QUANT) {
             float *sc = reinterpret_cast<float *>(scales[st][tiles % C::SCALES]);
             if ((lane >> 3) == here) {
@@ -1399,8 +1537,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           y.mine = !C::SHARED || t == 0 || y.x.ntok > p.tok;
           y.first = y.i == 0;
           y.last = y.i == y.x.n - 1;
-          y.lo = y.x.lo - (y.x.tile + y.i) * kKeys;
-          y.hi = y.x.L - (y.x.tile + y.i) * kKeys;
+          const int tile = y.x.tile + (C::REVERSE ? y.x.n - 1 - y.i : y.i);
+          y.lo = y.x.lo - tile * kKeys;
+          y.hi = y.x.L - tile * kKeys;
           ++y.i;
           ok = ok && mbar_spin(kv_full(st, k_at), kv_parity(k_at));
           if (y.mine && y.first) {

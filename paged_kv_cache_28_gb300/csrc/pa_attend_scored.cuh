@@ -17,6 +17,8 @@ pa_status run_attend_scored(const ScoredCall &x) {
   if (kScore & kCap) {
     p.c = fmaxf(fabsf(x.sm_scale / x.score.softcap), 1e-30f);
     p.cap2 = x.score.softcap * kLog2e;
+    const float tanh[6] = {kTanh0, kTanh1, kTanh2, kTanh3, kTanh4, kTanh5};
+    for (int i = 0; i < 6; ++i) p.near[i] = make_float2(p.cap2 * tanh[i], p.cap2 * tanh[i]);
   }
   CUtensorMap maps[3];
   if (!make_maps(x.s, plan, x.q, x.T, x.k_pool, x.v_pool, maps)) return PA_ERR_CUDA;
