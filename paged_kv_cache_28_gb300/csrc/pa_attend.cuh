@@ -83,7 +83,10 @@ struct AttendParams {
   const float *slopes;                  // [Hq], with kBias
   const int32_t *prefix_lens;           // [B], or null
   float cap2;                           // cap log2(e), with kCap
-  float2 near[6];                       // cap2 times tanh's coefficients within 1
+  // A capped score times log2(e) as an odd polynomial of the score (bf16 pools) or of c times it, where
+  // c |score| is at most `reach`.
+  float2 tanh[6];
+  float reach;
 };
 
 // ------------------------------------------------------------------ units of work
@@ -432,6 +435,10 @@ __device__ __forceinline__ void tc_ld16(uint32_t *r, uint32_t addr) {
       : "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void tc_st8(uint32_t addr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::PA_I8(r, 0), "r"(addr)
+               : "memory");
+}
 __device__ __forceinline__ void tc_wait_ld16(uint32_t *r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : PA_W8(r, 0), PA_W8(r, 8)::"memory");
 }
@@ -641,12 +648,6 @@ struct RingOrder {
 
 // kKind: the pools' pa_kv_dtype.  Codes (D = 128) are restored to bf16 tiles, without their scale,
 // by eight warps of their own: K's scale multiplies the scores of a page, V's its weights.
-// What a row's registers hold when its weights are computed: scores, scores to be capped, or the
-// weights' exponents but for the reference.
-constexpr int kScores = 0, kCapped = 1, kExponents = 2;
-template <int k>
-using Kind = std::integral_constant<int, k>;
-
 // kScore: what changes the scores (kCap, kBias).
 template <int kD, int kKind, bool kShared, int kScore = 0>
 struct AttendCfg {
@@ -938,299 +939,325 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           const bool edge = key0 < all_lo || key0 + kKeys > all_hi;
           const int first = lo - key0;                   // columns [first, first + seen) count
           const unsigned seen = static_cast<unsigned>(max(0, hi - lo));
-          auto hide = [&](uint32_t *s, int j0, float hidden = -INFINITY) {   // columns [j0, j0 + 32) of the row
-            if (edge) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (static_cast<unsigned>(j0 + j - first) >= seen) s[j] = __float_as_uint(hidden);
-            }
-          };
           // what the scores of a block's two pages are multiplied by
           auto k_factors = [&](int block) {
             return C::QUANT ? lds_f32x2(sc + 8 * block) : make_float2(p.c, p.c);
           };
-          // A capped tile whose scores pass the cap has their exponents in TMEM in their place.
-          [[maybe_unused]] bool far = false;
-          [[maybe_unused]] float hidden = -INFINITY;     // what makes a score's weight 0
-          [[maybe_unused]] float peak = 0.f;             // the largest |score| over the cap
-          [[maybe_unused]] auto look = [&](const uint32_t *s, float2 f) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              float y[2] = {0.f, 0.f};
-#pragma unroll
-              for (int e = j; e < j + 16; e += 4) {
-                y[0] = fmaxf(y[0], fmaxf(fabsf(__uint_as_float(s[e])), fabsf(__uint_as_float(s[e + 1]))));
-                y[1] = fmaxf(y[1], fmaxf(fabsf(__uint_as_float(s[e + 2])), fabsf(__uint_as_float(s[e + 3]))));
-              }
-              peak = fmaxf(peak, fmaxf(y[0], y[1]) * (j ? f.y : f.x));
-            }
-          };
-          // Exponents of block j's columns, past the cap, in TMEM.
-          [[maybe_unused]] auto cap_far = [&](int block, float2 f) {
+          // Takes a tile's maximum into the row's reference; what its exponents are shifted by.
+          auto refer_to = [&](float top) {
+            if (m == -INFINITY) m = top;                   // O and l are zero so far
+            // the reference moves only past kMaxJump octaves: weights stay below 2^8, far
+            // inside bf16 and fp32, and O is seldom rescaled
+            const bool jump = live && l > 0.f && top > m + kMaxJump;
+            if (__any_sync(0xffffffffu, jump)) {
+              const float g = jump ? ex2(m - top) : 1.f;
+              if (jump) m = top;
+              l *= g;
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
-              const float g = half ? f.y : f.x;
-              uint32_t o[16];
-              tc_ld16(o, tS + 32 * block + 16 * half);
-              tc_wait_ld16(o);
+              for (int j = 0; j < C::D; j += 32) {
+                uint32_t o[32];
+                tc_ld32(o, tO + j);
+                tc_wait_ld32(o);
 #pragma unroll
-              for (int e = 0; e < 16; ++e)
-                o[e] = __float_as_uint(p.cap2 * tanh_any(__uint_as_float(o[e]) * g));
-              tc_st16(tS + 32 * block + 16 * half, o);
+                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
+                tc_st32(tO + j, o);
+              }
             }
+            return m == -INFINITY ? 0.f : -m;
           };
-          [[maybe_unused]] auto is_far = [&] { return __any_sync(0xffffffffu, live && peak > 1.f); };
-          // Two capped scores, times log2(e), plus shift (not those of a far tile).  A score of +inf
-          // gives -inf, the sign of the last coefficient.
-          [[maybe_unused]] auto capped = [&](float2 s, float g, float2 shift) {
-            const float2 t = mul2(s, make_float2(g, g)), u = mul2(t, t);
-            float2 y = fma2(u, p.near[5], p.near[4]);
+          float2 sum[2] = {};
+          if constexpr (!C::CHANGED) {
+            auto hide = [&](uint32_t *s, int j0) {         // columns [j0, j0 + 32) of the row
+              if (edge) {
 #pragma unroll
-            for (int i = 3; i >= 0; --i) y = fma2(u, y, p.near[i]);
-            return fma2(t, y, shift);
-          };
-          // Scores that fall with distance: columns [j0, j0 + 32) become exponents in place.
-          [[maybe_unused]] auto biased = [&](uint32_t *s, int j0, float2 f) {
-            if constexpr (C::CAP) {
-              if (!far) {
+                for (int j = 0; j < 32; ++j)
+                  if (static_cast<unsigned>(j0 + j - first) >= seen) s[j] = __float_as_uint(-INFINITY);
+              }
+            };
+            float mx[2] = {-INFINITY, -INFINITY};
+            auto maximum = [&](const uint32_t *s, float2 f) {   // of a block of 32 columns
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  const float2 y = capped(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])),
-                                          e < 16 ? f.x : f.y, make_float2(0.f, 0.f));
-                  s[e] = __float_as_uint(y.x);
-                  s[e + 1] = __float_as_uint(y.y);
+              for (int j = 0; j < 32; j += 16) {
+                float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int e = j; e < j + 16; e += 4) {
+                  y[0] = fmaxf(y[0], fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
+                  y[1] = fmaxf(y[1], fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
+                }
+                const float page = fmaxf(y[0], y[1]);
+                mx[j / 16] = fmaxf(mx[j / 16], C::QUANT ? page * (j ? f.y : f.x) : page);
+              }
+            };
+            // A block of 32 columns is on its way while another is worked on.  bf16 pools: the row's
+            // scores stay in registers; code pools, whose threads have fewer, read half of them twice.
+            uint32_t s[C::QUANT ? 64 : kKeys];
+            if constexpr (C::QUANT) {
+#pragma unroll 1
+              for (int j = 2; j >= 0; j -= 2) {            // blocks j and j + 1
+                tc_ld32(s, tS + 32 * j);
+                tc_ld32(s + 32, tS + 32 * j + 32);
+                const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
+                tc_wait_ld32(s);
+                tc_use32(s + 32);
+                hide(s, 32 * j);
+                maximum(s, f0);
+                hide(s + 32, 32 * j + 32);
+                maximum(s + 32, f1);
+              }
+            } else {
+              tc_ld32(s, tS);
+              tc_ld32(s + 32, tS + 32);
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                tc_wait_ld32(s + 64 * half);
+                tc_use32(s + 64 * half + 32);
+                if (half == 0) {
+                  tc_ld32(s + 64, tS + 64);
+                  tc_ld32(s + 96, tS + 96);
+                }
+#pragma unroll
+                for (int j = 64 * half; j < 64 * half + 64; j += 32) {
+                  hide(s + j, j);
+                  maximum(s + j, make_float2(1.f, 1.f));
                 }
               }
             }
-            const float d = static_cast<float>(key0 + j0 - pos);
-            float2 r = make_float2(slope * d, slope * (d + 1.f));
-            const float2 step = make_float2(2.f * slope, 2.f * slope);
+            const float top = fmaxf(mx[0], mx[1]) * (C::QUANT ? 1.f : p.c);
+            const float neg = refer_to(top);
+            // The weights of block j, over columns that are already read.  Code pools: V's scale enters
+            // in the exponent, and leaves the sums of its page again.
+            auto weights = [&](const uint32_t *s, int j, float2 f) {
+              float2 v = make_float2(0.f, 0.f);
+              if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
+              uint32_t packed[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float g = C::CAP ? 1.f : e < 16 ? f.x : f.y;
-              const float2 y = make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
-              const float2 x = C::CAP ? add2(y, r) : fma2(y, make_float2(g, g), r);
-              s[e] = __float_as_uint(x.x);
-              s[e + 1] = __float_as_uint(x.y);
-              r = add2(r, step);
-            }
-            // keys ahead of their query (in a prefix): the distance counts the other way
-            if (key0 + j0 + 31 > x.pos + tok0 && x.prefix > 0) {
+              for (int half = 0; half < 2; ++half) {
+                const float c1 = half ? f.y : f.x, lv = half ? v.y : v.x;
+                const float2 shift = make_float2(neg + lv, neg + lv);
+                float2 page[2] = {};
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[e] = __float_as_uint(fmaf(-2.f * slope, fmaxf(d + static_cast<float>(e), 0.f), __uint_as_float(s[e])));
-            }
-          };
-          float mx[2] = {-INFINITY, -INFINITY};
-          auto maximum = [&](const uint32_t *s, float2 f) {   // of a block of 32 columns
-#pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              float y[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-              for (int e = j; e < j + 16; e += 4) {
-                y[0] = fmaxf(y[0], fmaxf(__uint_as_float(s[e]), __uint_as_float(s[e + 1])));
-                y[1] = fmaxf(y[1], fmaxf(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])));
-              }
-              const float page = fmaxf(y[0], y[1]);
-              mx[j / 16] = fmaxf(mx[j / 16], C::QUANT && !C::BIAS ? page * (j ? f.y : f.x) : page);
-            }
-          };
-          // A block of 32 columns is on its way while another is worked on.  bf16 pools: the row's
-          // scores stay in registers; code pools, whose threads have fewer, read half of them twice.
-          uint32_t s[C::QUANT ? 64 : kKeys];
-          [[maybe_unused]] bool far_2 = false;           // the tile's second half
-          if constexpr (C::QUANT) {
-#pragma unroll 1
-            for (int j = 2; j >= 0; j -= 2) {            // blocks j and j + 1
-              tc_ld32(s, tS + 32 * j);
-              tc_ld32(s + 32, tS + 32 * j + 32);
-              const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
-              tc_wait_ld32(s);
-              tc_use32(s + 32);
-              if constexpr (C::CAP) {
-                look(s, f0);
-                look(s + 32, f1);
-                if constexpr (C::BIAS) {                 // each half of the tile by itself
-                  far = is_far();
-                  if (far) {
-                    cap_far(j, f0);
-                    cap_far(j + 1, f1);
-                    tc_wait_st();
-                    tc_ld32(s, tS + 32 * j);
-                    tc_ld32(s + 32, tS + 32 * j + 32);
-                    tc_wait_ld32(s);
-                    tc_use32(s + 32);
-                  }
-                  if (j > 0) far_2 = far;
-                  peak = 0.f;
+                for (int e = 8 * half; e < 8 * half + 8; ++e) {
+                  float2 y = fma2(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])),
+                                  make_float2(c1, c1), shift);
+                  y.x = ex2(y.x);
+                  y.y = ex2(y.y);
+                  float2 &to = C::QUANT ? page[e & 1] : sum[e & 1];
+                  to = add2(to, y);
+                  packed[e] = pack_bf16(y.x, y.y);
+                }
+                if constexpr (C::QUANT) {
+                  const float back = ex2(-lv);
+                  sum[half] = fma2(add2(page[0], page[1]), make_float2(back, back), sum[half]);
                 }
               }
-              if constexpr (C::BIAS) {
-                biased(s, 32 * j, f0);
-                biased(s + 32, 32 * j + 32, f1);
+              tc_st16(tS + 16 * j, packed);
+              if (j == kEarly / 32 - 1) {
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_early(t));    // the second product may begin
               }
-              hide(s, 32 * j);
-              maximum(s, f0);
-              hide(s + 32, 32 * j + 32);
-              maximum(s + 32, f1);
+            };
+            if constexpr (C::QUANT) {
+              // (the separate form in a loop: its few tiles a CTA wait for instructions first of all)
+#pragma unroll(C::SHARED ? 2 : 1)
+              for (int j = 0; j < 4; j += 2) {
+                const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
+                if (j > 0) {
+                  tc_wait_ld32(s);
+                  tc_use32(s + 32);
+                  hide(s, 64);
+                  hide(s + 32, 96);
+                }
+                weights(s, j, f0);
+                if (j == 0) tc_ld32(s, tS + 64);           // columns that are not written over yet
+                weights(s + 32, j + 1, f1);
+                if (j == 0) tc_ld32(s + 32, tS + 96);
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) weights(s + 32 * j, j, make_float2(p.c, p.c));
             }
           } else {
-            tc_ld32(s, tS);
-            tc_ld32(s + 32, tS + 32);
+            // Changed scores.  A tile takes a fast form, where the maximum is taken from the scores and
+            // the change is part of the exponents' arithmetic, or a slow one, which first writes the
+            // exponents over the scores.  Slow are tiles that some row does not see whole, those with a
+            // score past the cap, with a bias and keys ahead of their query (in a prefix), or with so
+            // steep a bias that the fast form's bound on the maximum could be too far from it.  Both are
+            // loops that read the scores twice: unrolled over the tile, with the plain softmax's
+            // registers, the instructions did not come fast enough.
+            auto as_pair = [](const uint32_t *s, int e) {
+              return make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
+            };
+            bool slow = edge;
+            if constexpr (C::BIAS)
+              slow = slow || (x.prefix > 0 && key0 + kKeys - 1 > x.pos + tok0) ||
+                     __any_sync(0xffffffffu, fabsf(slope) > 2.f);
+            float top = -INFINITY;
+            uint32_t s[64];
+            if (!slow) {
+              float peak = 0.f;                          // the largest |score|, over the cap
+              auto scan = [&](const uint32_t *s, int b, float2 f) {       // block b, columns [32 b, 32 b + 32)
+                float mx[2];
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              tc_wait_ld32(s + 64 * half);
-              tc_use32(s + 64 * half + 32);
-              if (half == 0) {
-                tc_ld32(s + 64, tS + 64);
-                tc_ld32(s + 96, tS + 96);
-              }
-              if constexpr (C::CAP && C::BIAS) {         // each half of the tile by itself
-                peak = 0.f;
-                look(s + 64 * half, make_float2(p.c, p.c));
-                look(s + 64 * half + 32, make_float2(p.c, p.c));
-                far = is_far();
-                if (far) {
-                  tc_wait_ld32(s + 64);                  // (the other half's loads are still on their way)
-                  tc_use32(s + 96);
-                  cap_far(2 * half, make_float2(p.c, p.c));
-                  cap_far(2 * half + 1, make_float2(p.c, p.c));
-                  tc_wait_st();
-                  tc_ld32(s + 64 * half, tS + 64 * half);
-                  tc_ld32(s + 64 * half + 32, tS + 64 * half + 32);
-                  tc_wait_ld32(s + 64 * half);
-                  tc_use32(s + 64 * half + 32);
+                for (int j = 0; j < 32; j += 16) {
+                  float y[2] = {-INFINITY, -INFINITY}, a[2] = {0.f, 0.f};
+#pragma unroll
+                  for (int e = j; e < j + 16; e += 4) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                      const float2 v = as_pair(s, e + 2 * i);
+                      y[i] = fmaxf(y[i], fmaxf(v.x, v.y));
+                      if constexpr (C::CAP) a[i] = fmaxf(a[i], fmaxf(fabsf(v.x), fabsf(v.y)));
+                    }
+                  }
+                  mx[j / 16] = fmaxf(y[0], y[1]) * (j ? f.y : f.x);
+                  if constexpr (C::CAP) peak = fmaxf(peak, fmaxf(a[0], a[1]) * (j ? f.y : f.x));
                 }
-              }
-#pragma unroll
-              for (int j = 64 * half; j < 64 * half + 64; j += 32) {
-                if constexpr (C::CAP && !C::BIAS) look(s + j, make_float2(p.c, p.c));
-                if constexpr (C::BIAS) biased(s + j, j, make_float2(p.c, p.c));
-                hide(s + j, j);
-                maximum(s + j, make_float2(1.f, 1.f));
-              }
-            }
-          }
-          float top = fmaxf(mx[0], mx[1]) * (C::QUANT || C::BIAS ? 1.f : p.c);
-          if constexpr (C::CAP && !C::BIAS) {
-            // the cap rises with the score, so the largest capped score is the largest score's
-            top = top == -INFINITY ? top : p.cap2 * tanh_any(top);
-            far = is_far();
-            if (far) {
+                float y = fmaxf(mx[0], mx[1]);
+                if constexpr (C::BIAS) {                 // no more than the largest bias on top
+                  if constexpr (C::CAP) y = p.cap2 * tanh_within_1(y);
+                  const int ahead = key0 + 32 * b - pos, behind = -31 - ahead;       // of the nearest key
+                  const int d = slope >= 0.f ? max(0, max(ahead, behind)) : 31 + max(ahead, behind);
+                  y = fmaf(-slope, static_cast<float>(d), y);
+                }
+                top = fmaxf(top, y);
+              };
 #pragma unroll 1
-              for (int j = 0; j < 4; ++j) cap_far(j, k_factors(j));
+              for (int j = 2; j >= 0; j -= 2) {          // blocks j and j + 1
+                tc_ld32(s, tS + 32 * j);
+                tc_ld32(s + 32, tS + 32 * j + 32);
+                const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
+                tc_wait_ld32(s);
+                tc_use32(s + 32);
+                scan(s, j, f0);
+                scan(s + 32, j + 1, f1);
+              }
+              // the cap rises with the score, so the largest capped score is the largest score's
+              if constexpr (C::CAP && !C::BIAS) top = p.cap2 * tanh_within_1(top);
+              if constexpr (C::CAP) slow = __any_sync(0xffffffffu, live && peak > p.reach);
+            }
+            auto of_page = [&](uint32_t at, float other) {
+              return C::QUANT ? __uint_as_float(lds_u32(at)) : other;
+            };
+            if (slow) {
+              top = -INFINITY;
+#pragma unroll 1
+              for (int page = 0; page < 8; ++page) {
+                uint32_t o[16];
+                tc_ld16(o, tS + 16 * page);
+                const float g = of_page(sc + 4 * page, p.c);
+                tc_wait_ld16(o);
+                const int from = first - 16 * page;      // columns [from, from + seen) of the page count
+                auto in = [&](int e) { return static_cast<unsigned>(e - from) < seen; };
+                float y[16], peak = 0.f;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  y[e] = in(e) ? __uint_as_float(o[e]) * g : 0.f;
+                  peak = fmaxf(peak, fabsf(y[e]));
+                }
+                if constexpr (C::CAP) {
+                  const bool far = __any_sync(0xffffffffu, peak > 1.f);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) y[e] = p.cap2 * (far ? tanh_any(y[e]) : tanh_within_1(y[e]));
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  if constexpr (C::BIAS)
+                    y[e] = fmaf(-slope, fabsf(static_cast<float>(key0 + 16 * page + e - pos)), y[e]);
+                  y[e] = in(e) ? y[e] : -INFINITY;
+                  top = fmaxf(top, y[e]);
+                  o[e] = __float_as_uint(y[e]);
+                }
+                tc_st16(tS + 16 * page, o);
+              }
               tc_wait_st();
-#pragma unroll
-              for (int j = 0; j < (C::QUANT ? 64 : kKeys); j += 32) tc_ld32(s + j, tS + j);
-              tc_wait_ld32(s);
-#pragma unroll
-              for (int j = 32; j < (C::QUANT ? 64 : kKeys); j += 32) tc_use32(s + j);
             }
-            hidden = far ? -INFINITY : INFINITY;
-#pragma unroll
-            for (int j = 0; j < (C::QUANT ? 64 : kKeys); j += 32) hide(s + j, j, hidden);
-          }
-          if (m == -INFINITY) m = top;                   // O and l are zero so far
-          // the reference moves only past kMaxJump octaves: weights stay below 2^8, far
-          // inside bf16 and fp32, and O is seldom rescaled
-          const bool jump = live && l > 0.f && top > m + kMaxJump;
-          if (__any_sync(0xffffffffu, jump)) {
-            const float g = jump ? ex2(m - top) : 1.f;
-            if (jump) m = top;
-            l *= g;
-#pragma unroll 1
-            for (int j = 0; j < C::D; j += 32) {
-              uint32_t o[32];
-              tc_ld32(o, tO + j);
-              tc_wait_ld32(o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * g);
-              tc_st32(tO + j, o);
-            }
-          }
-          const float neg = m == -INFINITY ? 0.f : -m;
-          // The weights of block j, over columns that are already read.  Code pools: V's scale enters
-          // in the exponent, and leaves the sums of its page again.
-          float2 sum[2] = {};
-          auto weights = [&](const uint32_t *s, int j, float2 f, auto kind) {
-            constexpr int kKind = decltype(kind)::value;
-            float2 v = make_float2(0.f, 0.f);
-            if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
-            uint32_t packed[16];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              [[maybe_unused]] const float c1 = half ? f.y : f.x;
-              const float lv = half ? v.y : v.x;
-              const float2 shift = make_float2(neg + lv, neg + lv);
-              float2 page[2] = {};
-#pragma unroll
-              for (int e = 8 * half; e < 8 * half + 8; ++e) {
-                float2 y = make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-                if constexpr (kKind == kScores)
-                  y = fma2(y, make_float2(c1, c1), shift);
-                else if constexpr (kKind == kCapped)
-                  y = capped(y, c1, shift);
-                else
-                  y = add2(y, shift);
-                y.x = ex2(y.x);
-                y.y = ex2(y.y);
-                float2 &to = C::QUANT ? page[e & 1] : sum[e & 1];
-                to = add2(to, y);
-                packed[e] = pack_bf16(y.x, y.y);
-              }
-              if constexpr (C::QUANT) {
-                const float back = ex2(-lv);
-                sum[half] = fma2(add2(page[0], page[1]), make_float2(back, back), sum[half]);
-              }
-            }
-            tc_st16(tS + 16 * j, packed);
-            if (j == kEarly / 32 - 1) {
+            const float neg = refer_to(top);
+            auto announce_early = [&] {
               tc_wait_st();
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(p_early(t));    // the second product may begin
-            }
-          };
-          if constexpr (C::QUANT) {
-            // (the separate form in a loop: its few tiles a CTA wait for instructions first of all)
-#pragma unroll(C::SHARED ? 2 : 1)
-            for (int j = 0; j < 4; j += 2) {
-              const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
-              if (j > 0) {
-                tc_wait_ld32(s);
-                tc_use32(s + 32);
-                if constexpr (C::BIAS) {
-                  far = far_2;
-                  biased(s, 64, f0);
-                  biased(s + 32, 96, f1);
-                }
-                hide(s, 64, hidden);
-                hide(s + 32, 96, hidden);
-              }
-              auto of_block = [&](const uint32_t *s, int j, float2 f) {
-                if constexpr (!C::CHANGED)
-                  weights(s, j, f, Kind<kScores>{});
-                else if (C::BIAS || far)
-                  weights(s, j, f, Kind<kExponents>{});
-                else
-                  weights(s, j, f, Kind<kCapped>{});
-              };
-              of_block(s, j, f0);
-              if (j == 0) tc_ld32(s, tS + 64);           // columns that are not written over yet
-              of_block(s + 32, j + 1, f1);
-              if (j == 0) tc_ld32(s + 32, tS + 96);
-            }
-          } else {
-            auto all = [&](auto kind) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) weights(s + 32 * j, j, make_float2(p.c, p.c), kind);
             };
-            if constexpr (!C::CHANGED)
-              all(Kind<kScores>{});
-            else if (C::BIAS || far)
-              all(Kind<kExponents>{});
-            else
-              all(Kind<kCapped>{});
+            // Code pools: V's scale enters in the exponent, and leaves the sums of its page again.
+            if (slow) {
+#pragma unroll 1
+              for (int page = 0; page < 8; ++page) {
+                uint32_t o[16], packed[8];
+                tc_ld16(o, tS + 16 * page);
+                const float lv = of_page(sc + 32 + 4 * page, 0.f);
+                const float2 shift = make_float2(neg + lv, neg + lv);
+                float2 mine = make_float2(0.f, 0.f);
+                tc_wait_ld16(o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  float2 y = add2(as_pair(o, 2 * e), shift);
+                  y.x = ex2(y.x);
+                  y.y = ex2(y.y);
+                  mine = add2(mine, y);
+                  packed[e] = pack_bf16(y.x, y.y);
+                }
+                const float back = C::QUANT ? ex2(-lv) : 1.f;
+                sum[0] = fma2(mine, make_float2(back, back), sum[0]);
+                tc_st8(tS + 8 * page, packed);           // over columns that are already read
+                if (page == kEarly / 16 - 1) announce_early();
+              }
+            } else {
+              auto weights = [&](const uint32_t *s, int j, float2 f) {    // of block j
+                float2 v = make_float2(0.f, 0.f);
+                if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
+                uint32_t packed[16];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const float c1 = half ? f.y : f.x, lv = half ? v.y : v.x;
+                  const float base = neg + lv;
+                  float2 shift = make_float2(base, base);
+                  if constexpr (C::BIAS) {
+                    const float d = static_cast<float>(key0 + 32 * j + 16 * half - pos);
+                    shift = make_float2(fmaf(slope, d, base), fmaf(slope, d + 1.f, base));
+                  }
+                  const float2 step = make_float2(2.f * slope, 2.f * slope);
+                  float2 page[2] = {};
+#pragma unroll
+                  for (int e = 8 * half; e < 8 * half + 8; ++e) {
+                    float2 y = as_pair(s, 2 * e);
+                    if constexpr (C::CAP) {
+                      const float2 t = C::QUANT ? mul2(y, make_float2(c1, c1)) : y, u = mul2(t, t);
+                      y = fma2(u, p.tanh[5], p.tanh[4]);
+#pragma unroll
+                      for (int i = 3; i >= 0; --i) y = fma2(u, y, p.tanh[i]);
+                      y = fma2(t, y, shift);
+                    } else {
+                      y = fma2(y, make_float2(c1, c1), shift);
+                    }
+                    if constexpr (C::BIAS) shift = add2(shift, step);
+                    y.x = ex2(y.x);
+                    y.y = ex2(y.y);
+                    page[e & 1] = add2(page[e & 1], y);
+                    packed[e] = pack_bf16(y.x, y.y);
+                  }
+                  const float back = C::QUANT ? ex2(-lv) : 1.f;
+                  sum[half] = fma2(add2(page[0], page[1]), make_float2(back, back), sum[half]);
+                }
+                tc_st16(tS + 16 * j, packed);
+              };
+#pragma unroll 1
+              for (int j = 0; j < 4; j += 2) {
+                const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
+                if (j > 0) {
+                  tc_wait_ld32(s);
+                  tc_use32(s + 32);
+                }
+                weights(s, j, f0);
+                if (j == 0) tc_ld32(s, tS + 64);         // columns that are not written over yet
+                weights(s + 32, j + 1, f1);
+                if (j == 0) {
+                  tc_ld32(s + 32, tS + 96);
+                  announce_early();
+                }
+              }
+            }
           }
           tc_wait_st();
           tc_fence_before();

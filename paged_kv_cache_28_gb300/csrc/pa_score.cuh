@@ -11,6 +11,10 @@ namespace pa {
 constexpr float kTanh0 = 0.99999941f, kTanh1 = -0.33329042f, kTanh2 = 0.13281434f,
                 kTanh3 = -0.05160567f, kTanh4 = 0.01674311f, kTanh5 = -0.00306706f;
 
+// On [-1/2, 1/2] four terms come as near (5.5e-7).
+constexpr float kTanhHalf0 = 0.99999946f, kTanhHalf1 = -0.33326318f, kTanhHalf2 = 0.13190297f,
+                kTanhHalf3 = -0.04440223f;
+
 __device__ __forceinline__ float tanh_within_1(float t) {
   const float u = t * t;
   float y = fmaf(u, kTanh5, kTanh4);
