@@ -658,6 +658,8 @@ struct AttendCfg {
   // A piece's key tiles last to first: where scores fall with distance the first tile then holds the
   // largest, and the reference maximum hardly ever moves again.
   static constexpr bool REVERSE = BIAS;
+  // Loops over 32 columns instead of 64.
+  static constexpr bool NARROW = QUANT || !SHARED;
   static constexpr int HALVES = D / 64;                 // 128-byte column chunks of a bf16 row
   static constexpr int TILE = kKeys * D * 2;            // bytes of a Q, K or V tile
   static constexpr int CODE_ROW = KIND == PA_KV_INT4 ? 64 : 128;
@@ -1081,27 +1083,36 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           } else {
             // Changed scores.  A tile takes a fast form, where the maximum is taken from the scores and
             // the change is part of the exponents' arithmetic, or a slow one, which first writes the
-            // exponents over the scores.  Slow are tiles that some row does not see whole, those with a
-            // score past the cap, with a bias and keys ahead of their query (in a prefix), or with so
-            // steep a bias that the fast form's bound on the maximum could be too far from it.  Both are
-            // loops that read the scores twice: unrolled over the tile, with the plain softmax's
-            // registers, the instructions did not come fast enough.
+            // exponents over the scores.  Slow are tiles with a bias and keys ahead of their query (in a
+            // prefix), or with so steep a bias that the fast form's bound on the maximum could be too far
+            // from it.  Both are loops that read the scores twice: unrolled over the tile, with the plain
+            // softmax's registers, the instructions did not come fast enough.
             auto as_pair = [](const uint32_t *s, int e) {
               return make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
             };
-            bool slow = edge;
+            bool slow = false;
             if constexpr (C::BIAS)
-              slow = slow || (x.prefix > 0 && key0 + kKeys - 1 > x.pos + tok0) ||
+              slow = (x.prefix > 0 && key0 + kKeys - 1 > x.pos + tok0) ||
                      __any_sync(0xffffffffu, fabsf(slope) > 2.f);
             float top = -INFINITY;
-            uint32_t s[64];
+            [[maybe_unused]] uint32_t far = 0;           // bit b: block b has scores past the polynomial's reach
+            // whether column e of block b is hidden from this row
+            auto hidden = [&](int b, int e) { return static_cast<unsigned>(32 * b + e - first) >= seen; };
             if (!slow) {
-              float peak = 0.f;                          // the largest |score|, over the cap
-              auto scan = [&](const uint32_t *s, int b, float2 f) {       // block b, columns [32 b, 32 b + 32)
+              // block b: columns [32 b, 32 b + 32).  What is not seen is NaN, which a maximum leaves out
+              // (the form that a tile takes must not depend on what lies beyond a sequence).
+              auto scan = [&](uint32_t *s, int b, float2 f, auto masked) {
+                if constexpr (decltype(masked)::value) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (hidden(b, e)) s[e] = __float_as_uint(NAN);
+                }
                 float mx[2];
+                [[maybe_unused]] float peak = 0.f;       // the largest |score|, over the cap
 #pragma unroll
                 for (int j = 0; j < 32; j += 16) {
-                  float y[2] = {-INFINITY, -INFINITY}, a[2] = {0.f, 0.f};
+                  float y[2] = {-INFINITY, -INFINITY};
+                  [[maybe_unused]] float a[2] = {0.f, 0.f};
 #pragma unroll
                   for (int e = j; e < j + 16; e += 4) {
 #pragma unroll
@@ -1114,28 +1125,47 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                   mx[j / 16] = fmaxf(y[0], y[1]) * (j ? f.y : f.x);
                   if constexpr (C::CAP) peak = fmaxf(peak, fmaxf(a[0], a[1]) * (j ? f.y : f.x));
                 }
+                if constexpr (C::CAP)
+                  far |= __any_sync(0xffffffffu, live && peak > p.reach) ? 1u << b : 0u;
                 float y = fmaxf(mx[0], mx[1]);
                 if constexpr (C::BIAS) {                 // no more than the largest bias on top
-                  if constexpr (C::CAP) y = p.cap2 * tanh_within_1(y);
+                  if constexpr (C::CAP) y = y == -INFINITY ? y : p.cap2 * tanh_any(y);
                   const int ahead = key0 + 32 * b - pos, behind = -31 - ahead;       // of the nearest key
                   const int d = slope >= 0.f ? max(0, max(ahead, behind)) : 31 + max(ahead, behind);
                   y = fmaf(-slope, static_cast<float>(d), y);
                 }
                 top = fmaxf(top, y);
               };
+              // (Tiles that some row does not see whole: a loop of its own shape, whose selections stay out
+              // of the other's way.)
+              auto narrow_loop = [&](auto masked) {
 #pragma unroll 1
-              for (int j = 2; j >= 0; j -= 2) {          // blocks j and j + 1
-                tc_ld32(s, tS + 32 * j);
-                tc_ld32(s + 32, tS + 32 * j + 32);
-                const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
-                tc_wait_ld32(s);
-                tc_use32(s + 32);
-                scan(s, j, f0);
-                scan(s + 32, j + 1, f1);
+                for (int j = 0; j < 4; ++j) {
+                  uint32_t s[32];
+                  tc_ld32(s, tS + 32 * j);
+                  tc_wait_ld32(s);
+                  scan(s, j, k_factors(j), masked);
+                }
+              };
+              if (edge) {
+                narrow_loop(std::true_type{});
+              } else if constexpr (C::NARROW) {
+                narrow_loop(std::false_type{});
+              } else {
+#pragma unroll 1
+                for (int j = 0; j < 4; j += 2) {
+                  uint32_t s[64];
+                  tc_ld32(s, tS + 32 * j);
+                  tc_ld32(s + 32, tS + 32 * j + 32);
+                  const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
+                  tc_wait_ld32(s);
+                  tc_use32(s + 32);
+                  scan(s, j, f0, std::false_type{});
+                  scan(s + 32, j + 1, f1, std::false_type{});
+                }
               }
               // the cap rises with the score, so the largest capped score is the largest score's
-              if constexpr (C::CAP && !C::BIAS) top = p.cap2 * tanh_within_1(top);
-              if constexpr (C::CAP) slow = __any_sync(0xffffffffu, live && peak > p.reach);
+              if constexpr (C::CAP && !C::BIAS) top = top == -INFINITY ? top : p.cap2 * tanh_any(top);
             }
             auto of_page = [&](uint32_t at, float other) {
               return C::QUANT ? __uint_as_float(lds_u32(at)) : other;
@@ -1204,14 +1234,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (page == kEarly / 16 - 1) announce_early();
               }
             } else {
-              auto weights = [&](const uint32_t *s, int j, float2 f) {    // of block j
+              // The weights of block j.
+              auto weights = [&](const uint32_t *s, int j, float2 f, auto masked, auto past_reach) {
                 float2 v = make_float2(0.f, 0.f);
                 if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
                 uint32_t packed[16];
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                  const float c1 = half ? f.y : f.x, lv = half ? v.y : v.x;
-                  const float base = neg + lv;
+                  const float c1 = half ? f.y : f.x, lv = half ? v.y : v.x, base = neg + lv;
                   float2 shift = make_float2(base, base);
                   if constexpr (C::BIAS) {
                     const float d = static_cast<float>(key0 + 32 * j + 16 * half - pos);
@@ -1222,16 +1252,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                   for (int e = 8 * half; e < 8 * half + 8; ++e) {
                     float2 y = as_pair(s, 2 * e);
-                    if constexpr (C::CAP) {
+                    if constexpr (!C::CAP) {
+                      y = fma2(y, make_float2(c1, c1), shift);
+                    } else if constexpr (decltype(past_reach)::value) {
+                      const float2 t = make_float2(tanh_any(y.x * c1), tanh_any(y.y * c1));
+                      y = fma2(t, make_float2(p.cap2, p.cap2), shift);
+                    } else {
                       const float2 t = C::QUANT ? mul2(y, make_float2(c1, c1)) : y, u = mul2(t, t);
                       y = fma2(u, p.tanh[5], p.tanh[4]);
 #pragma unroll
                       for (int i = 3; i >= 0; --i) y = fma2(u, y, p.tanh[i]);
                       y = fma2(t, y, shift);
-                    } else {
-                      y = fma2(y, make_float2(c1, c1), shift);
                     }
                     if constexpr (C::BIAS) shift = add2(shift, step);
+                    if constexpr (decltype(masked)::value) {
+                      if (hidden(j, 2 * e)) y.x = -INFINITY;
+                      if (hidden(j, 2 * e + 1)) y.y = -INFINITY;
+                    }
                     y.x = ex2(y.x);
                     y.y = ex2(y.y);
                     page[e & 1] = add2(page[e & 1], y);
@@ -1242,19 +1279,44 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 tc_st16(tS + 16 * j, packed);
               };
+              auto of_block = [&](const uint32_t *s, int j, float2 f, auto masked) {
+                if (C::CAP && (far >> j & 1))
+                  weights(s, j, f, masked, std::true_type{});
+                else
+                  weights(s, j, f, masked, std::false_type{});
+              };
+              auto narrow_loop = [&](auto masked) {
+                uint32_t s[32];
+                tc_ld32(s, tS);
 #pragma unroll 1
-              for (int j = 0; j < 4; j += 2) {
-                const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
-                if (j > 0) {
+                for (int j = 0; j < 4; ++j) {
+                  const float2 f = k_factors(j);
+                  tc_wait_ld32(s);
+                  of_block(s, j, f, masked);
+                  if (j < 3) tc_ld32(s, tS + 32 * j + 32);       // columns that are not written over yet
+                  if (j == kEarly / 32 - 1) announce_early();
+                }
+              };
+              if (edge) {
+                narrow_loop(std::true_type{});
+              } else if constexpr (C::NARROW) {
+                narrow_loop(std::false_type{});
+              } else {
+                uint32_t s[64];
+                tc_ld32(s, tS);
+                tc_ld32(s + 32, tS + 32);
+#pragma unroll 1
+                for (int j = 0; j < 4; j += 2) {
+                  const float2 f0 = k_factors(j), f1 = k_factors(j + 1);
                   tc_wait_ld32(s);
                   tc_use32(s + 32);
-                }
-                weights(s, j, f0);
-                if (j == 0) tc_ld32(s, tS + 64);         // columns that are not written over yet
-                weights(s + 32, j + 1, f1);
-                if (j == 0) {
-                  tc_ld32(s + 32, tS + 96);
-                  announce_early();
+                  of_block(s, j, f0, std::false_type{});
+                  if (j == 0) tc_ld32(s, tS + 64);       // columns that are not written over yet
+                  of_block(s + 32, j + 1, f1, std::false_type{});
+                  if (j == 0) {
+                    tc_ld32(s + 32, tS + 96);
+                    announce_early();
+                  }
                 }
               }
             }
