@@ -100,26 +100,6 @@ struct Item {
   float cos[8], sin[8];
 };
 
-// The angles of pairs j .. j + 3 (j a multiple of 4) of a token whose pair j turns by table row
-// row_of(j): together where the four share their axis.
-template <class RowOf>
-__device__ __forceinline__ void load_angles(const RopeParams &p, int j, const RowOf &row_of, float *cos,
-                                            float *sin) {
-  const uint32_t four = (p.axes[j >> 4] >> (2 * (j & 15))) & 0xFFu;
-  if (four == (four & 3u) * 0x55u) {
-    const float *row = p.cos_sin + static_cast<int64_t>(row_of(j)) * p.r + j;
-    *reinterpret_cast<float4 *>(cos) = __ldg(reinterpret_cast<const float4 *>(row));
-    *reinterpret_cast<float4 *>(sin) = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float *row = p.cos_sin + static_cast<int64_t>(row_of(j + e)) * p.r + j + e;
-      cos[e] = __ldg(row);
-      sin[e] = __ldg(row + p.r / 2);
-    }
-  }
-}
-
 __device__ __forceinline__ void load_item(const RopeParams &p, int item, int pos, Item &x) {
   x.rotates = item < p.r / 16;
   if (!x.rotates) return;
@@ -132,18 +112,24 @@ __device__ __forceinline__ void load_item(const RopeParams &p, int item, int pos
     *reinterpret_cast<float4 *>(x.sin + 4 * i) = __ldg(sin_row + i);
   }
 }
+// The table row of axis a.
+__device__ __forceinline__ int row_of(const AxisRows &at, int a) {
+  int pos = at.pos[0];
+#pragma unroll
+  for (int i = 1; i < PA_MAX_AXES; ++i) pos = a == i ? at.pos[i] : pos;
+  return pos;
+}
 __device__ __forceinline__ void load_item(const RopeParams &p, int item, const AxisRows &at, Item &x) {
   x.rotates = item < p.r / 16;
   if (!x.rotates) return;
-  auto row_of = [&](int j) {
-    const int a = axis_of(p, j);
-    int pos = at.pos[0];
+  const uint32_t axes = (p.axes[item >> 1] >> (16 * (item & 1))) & 0xFFFFu;        // of the eight pairs
+  if (axes == (axes & 3u) * 0x5555u) return load_item(p, item, row_of(at, axes & 3), x);
 #pragma unroll
-    for (int i = 1; i < PA_MAX_AXES; ++i) pos = a == i ? at.pos[i] : pos;
-    return pos;
-  };
-#pragma unroll
-  for (int i = 0; i < 2; ++i) load_angles(p, 8 * item + 4 * i, row_of, x.cos + 4 * i, x.sin + 4 * i);
+  for (int e = 0; e < 8; ++e) {
+    const float *row = p.cos_sin + static_cast<int64_t>(row_of(at, axes >> (2 * e) & 3)) * p.r + 8 * item + e;
+    x.cos[e] = __ldg(row);
+    x.sin[e] = __ldg(row + p.r / 2);
+  }
 }
 
 template <bool kInterleaved>
@@ -366,6 +352,17 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
         const bool upper = !kInterleaved && lane * 4 >= p.r / 2;
         const int j = kInterleaved ? lane * 2 : lane * 4 - (upper ? p.r / 2 : 0);
         const int peer = (upper ? lane - p.r / 8 : lane + p.r / 8) & 31;
+        // several axes: the first pair's positions, and whether the lane's other pairs share them
+        const int32_t *positions = p.positions;
+        [[maybe_unused]] bool alike = true;
+        if constexpr (kAxes) {
+          if (turns) {
+            const int axis = axis_of(p, j);
+            positions += static_cast<int64_t>(axis) * p.T;
+#pragma unroll
+            for (int e = 1; e < (kInterleaved ? 2 : 4); ++e) alike = alike && axis_of(p, j + e) == axis;
+          }
+        }
         float s = *scale;
         ByReciprocal over(1.f);
         uint32_t held = 0;                               // rows whose codes are in shared memory
@@ -381,22 +378,20 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
             if (i0 + i >= n) break;
             if (!is_v) {
               const float v[4] = {bf16_lo(x[i].x), bf16_hi(x[i].x), bf16_lo(x[i].y), bf16_hi(x[i].y)};
-              // the table row of pair a, and its place from pair j on
-              auto row_of = [&](int a) {
-                if constexpr (kAxes)
-                  return p.positions[static_cast<int64_t>(axis_of(p, a)) * p.T + members[i0 + i]];
-                else
-                  return p.positions[members[i0 + i]];
+              const float *row = p.cos_sin + static_cast<int64_t>(positions[members[i0 + i]]) * p.r + j;
+              // (several axes) the same for pair j + e
+              auto other_row = [&](int e) {
+                const int64_t axis = axis_of(p, j + e);
+                return p.cos_sin + static_cast<int64_t>(p.positions[axis * p.T + members[i0 + i]]) * p.r + j + e;
               };
-              const float *row = p.cos_sin + static_cast<int64_t>(row_of(kAxes && !turns ? 0 : j)) * p.r + j;
               if constexpr (kInterleaved) {
                 if (turns) {
                   float2 c, sn;
-                  if (!kAxes || axis_of(p, j) == axis_of(p, j + 1)) {
+                  if (!kAxes || alike) {
                     c = __ldg(reinterpret_cast<const float2 *>(row));
                     sn = __ldg(reinterpret_cast<const float2 *>(row + p.r / 2));
                   } else {
-                    const float *next = p.cos_sin + static_cast<int64_t>(row_of(j + 1)) * p.r + j + 1;
+                    const float *next = other_row(1);
                     c = make_float2(__ldg(row), __ldg(next));
                     sn = make_float2(__ldg(row + p.r / 2), __ldg(next + p.r / 2));
                   }
@@ -409,13 +404,18 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
                 const float w[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
                 if (turns) {
                   alignas(16) float cc[4], ss[4];
-                  if constexpr (kAxes) {
-                    load_angles(p, j, row_of, cc, ss);
-                  } else {
+                  if (!kAxes || alike) {
                     const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
                     const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
                     cc[0] = c.x, cc[1] = c.y, cc[2] = c.z, cc[3] = c.w;
                     ss[0] = sn.x, ss[1] = sn.y, ss[2] = sn.z, ss[3] = sn.w;
+                  } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                      const float *own = other_row(e);
+                      cc[e] = __ldg(own);
+                      ss[e] = __ldg(own + p.r / 2);
+                    }
                   }
                   float y[4];                            // a cos - b sin, or b cos + a sin
 #pragma unroll
