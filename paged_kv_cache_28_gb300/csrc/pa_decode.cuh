@@ -1277,118 +1277,6 @@ __global__ void __launch_bounds__(C::THREADS, C::MIN_BLOCKS)
       lane);
 }
 
-// One CTA per (b, kvh) pair; threads over (head, 4 consecutive d).  The pieces of a
-// pair are visited eight at a time with their loads issued together.  The decode
-// leaves the number of KV heads per unit (1, or 2 for paired 4-bit heads) after
-// the tile prefix: head kvh's partials are then rows (kvh % 2) G .. of unit kvh / 2.
-// Out: float, or uint16_t for bf16.
-__device__ __forceinline__ void put4(float *dst, float4 v) { *reinterpret_cast<float4 *>(dst) = v; }
-__device__ __forceinline__ void put4(uint16_t *dst, float4 v) {
-  *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-}
-template <class Out>
-__global__ void __launch_bounds__(256) merge_kernel(Out *out, const int32_t *prefix,
-                                                    const float *o_part, const float *lse_part,
-                                                    int B, int Hq, int Hkv, int G, int D,
-                                                    int num_splits) {
-  pdl_trigger();
-  pdl_wait();
-  const int pair = blockIdx.x;
-  const int b = pair / Hkv, kvh = pair - b * Hkv;
-  const int heads = prefix[B + 1] == 2 ? 2 : 1;
-  const int unit = kvh / heads, row0 = (kvh - unit * heads) * G;
-  const int Hu = Hkv / heads, Gu = G * heads;      // units per sequence, rows per unit
-  const int start_b = prefix[b];
-  const int nt = (prefix[b + 1] - start_b) / Hu;
-  const int total = prefix[B];
-  const int W = max(1, (total + num_splits - 1) / num_splits);
-  Out *o = out + (static_cast<size_t>(b) * Hq + kvh * G) * D;
-  const int D4 = D / 4;
-  // a cascaded sequence adds the partials of its shared prefix (cascade workspace);
-  // a unit finished inside one segment was joined with them there
-  const uint64_t cws = (static_cast<uint64_t>(static_cast<uint32_t>(prefix[B + 3])) << 32) |
-                       static_cast<uint32_t>(prefix[B + 2]);
-  const float *clse = nullptr, *co = nullptr;
-  const int cpieces = cascade_partials(cws, B, Hq, Hkv, G, D, b, kvh, clse, co);
-  if (nt == 0 && cpieces == 0) {
-    for (int e = threadIdx.x; e < G * D4; e += blockDim.x)
-      put4(o + 4 * e, make_float4(0.f, 0.f, 0.f, 0.f));
-    return;
-  }
-  const int start = start_b + unit * nt, end = start + nt;
-  // split pieces p0..p1 (none when the cascade covers the whole sequence)
-  int p0 = nt > 0 ? start / W : 0, p1 = nt > 0 ? (end - 1) / W : -1;
-  const bool inplace = nt > 0 && p0 == p1;         // finished inside one segment
-  if (inplace && cpieces == 0) return;
-  // a cascaded unit finished in place left its (o, lse) in the unit slots
-  const float *ulse = nullptr, *uo = nullptr;
-  if (inplace) {
-    const CascadeLayout cl = cascade_layout(B, Hq, D);
-    const uint8_t *cw = reinterpret_cast<const uint8_t *>(cws);
-    const size_t row = static_cast<size_t>(b) * Hq + kvh * G;
-    ulse = reinterpret_cast<const float *>(cw + cl.ulse) + row;
-    uo = reinterpret_cast<const float *>(cw + cl.uo) + row * D;
-    p1 = p0 - 1;                                   // no split pieces
-  }
-  // one pass: each batch of up to U pieces' (lse, o) is loaded together, then folded into
-  // a running maximum M with num and den rescaled when it rises
-  constexpr int U = 8;
-  for (int e = threadIdx.x; e < G * D4; e += blockDim.x) {
-    const int g = e / D4, d4 = e - g * D4, gu = row0 + g;
-    auto slot = [&](int s) { return static_cast<size_t>(s) * 2 + (s == p0 ? 1 : 0); };
-    float M = -INFINITY, den = 0.f;
-    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto fold = [&](float l, float4 x) {           // one piece; l = -inf adds nothing
-      if (l > M) {
-        const float r = expf(M - l);               // 0 while M is -inf
-        num = make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
-        den *= r;
-        M = l;
-      }
-      const float w = l == -INFINITY ? 0.f : expf(l - M);
-      num.x += w * x.x;
-      num.y += w * x.y;
-      num.z += w * x.z;
-      num.w += w * x.w;
-      den += w;
-    };
-    if (ulse) fold(ulse[g], reinterpret_cast<const float4 *>(uo + g * D)[d4]);
-    for (int c = 0; c < cpieces; ++c)              // the cascade's pieces of the prefix
-      fold(clse[c * G + g], reinterpret_cast<const float4 *>(co + (c * G + g) * D)[d4]);
-    for (int s0 = p0; s0 <= p1; s0 += U) {
-      float l[U];
-      float4 x[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool ok = s0 + u <= p1;
-        l[u] = ok ? __ldg(lse_part + slot(s0 + u) * Gu + gu) : -INFINITY;
-        x[u] = ok ? __ldg(reinterpret_cast<const float4 *>(o_part + (slot(s0 + u) * Gu + gu) * D) + d4)
-                  : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-      float bm = l[0];
-#pragma unroll
-      for (int u = 1; u < U; ++u) bm = fmaxf(bm, l[u]);
-      if (bm > M) {                                // raise M once per batch
-        const float r = expf(M - bm);
-        num = make_float4(num.x * r, num.y * r, num.z * r, num.w * r);
-        den *= r;
-        M = bm;
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float w = l[u] == -INFINITY ? 0.f : expf(l[u] - M);
-        num.x += w * x[u].x;
-        num.y += w * x[u].y;
-        num.z += w * x[u].z;
-        num.w += w * x[u].w;
-        den += w;
-      }
-    }
-    const float inv = 1.f / den;
-    put4(o + 4 * e, make_float4(num.x * inv, num.y * inv, num.z * inv, num.w * inv));
-  }
-}
-
 // ----------------------------------------------------------------------------
 // host side of the split decode
 // ----------------------------------------------------------------------------
@@ -1491,25 +1379,5 @@ static int kind_of(const pa_shape &s, int heads) {
   PA_DISPATCH(128, 2, kKindInt4, FN, __VA_ARGS__)     \
   PA_DISPATCH(128, 2, kKindInt4x2, FN, __VA_ARGS__)   \
   PA_DISPATCH(128, 2, kKindFp8x2, FN, __VA_ARGS__)
-
-// Joins the pieces that a split decode left in its workspace.
-template <class Out>
-static pa_status launch_merge(const pa_shape &s, Out *out, const void *workspace, int num_splits,
-                              cudaStream_t stream) {
-  const WorkspaceLayout w = splitkv_layout(s, num_splits);
-  const uint8_t *ws = static_cast<const uint8_t *>(workspace);
-  const int G = s.Hq / s.Hkv;
-  // a CTA per (sequence, KV head); with thousands of them (large batches, where most
-  // units finished inside one segment and exit at once) smaller CTAs keep more resident
-  const int cap = s.B * s.Hkv >= 2048 ? 128 : 256;
-  const int threads = min(cap, max(32, ((G * s.D / 4) + 31) / 32 * 32));
-  return launch_pdl(merge_kernel<Out>, dim3(s.B * s.Hkv), dim3(threads), 0, stream, out,
-                    reinterpret_cast<const int32_t *>(ws + w.prefix),
-                    reinterpret_cast<const float *>(ws + w.o_part),
-                    reinterpret_cast<const float *>(ws + w.lse), s.B, s.Hq, s.Hkv, G, s.D,
-                    num_splits) == cudaSuccess
-             ? PA_OK
-             : PA_ERR_CUDA;
-}
 
 }  // namespace pa
