@@ -43,6 +43,15 @@
 // products, 981 us; a warp each, taking turns, 872; P announced at half of the keys instead of at
 // three quarters, 835; a piece left in shared memory instead of in the softmax's registers and
 // loads issued in a short loop, 800.
+//
+// Changed scores (pa_extend_scored) cost the softmax instructions, and it was their fetching more than
+// their number: unrolled over a tile's 128 columns as the plain softmax is, four capped prompts of
+// 1,210 to 2,400 tokens took 662 us, two threads a row 711, two forms of the polynomial side by side
+// 832; in loops over 64 columns that read a tile twice 597, with four coefficients where the scores are
+// small 561 (plain scores: 387).  The chunk with a cap takes 1.21 ms, 945 TFLOP/s: 13 fp32
+// operations a score (at 2 cycles a pair), of them the polynomial 8.  With a distance bias it takes
+// 0.84 ms, within 6 % of plain scores: tiles run last to first, so that the reference maximum is
+// found at once (before: 1.29 ms), and the bias is one addition a pair.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -83,10 +92,10 @@ struct AttendParams {
   const float *slopes;                  // [Hq], with kBias
   const int32_t *prefix_lens;           // [B], or null
   float cap2;                           // cap log2(e), with kCap
-  // A capped score times log2(e) as an odd polynomial of the score (bf16 pools) or of c times it, where
-  // c |score| is at most `reach`.
-  float2 tanh[6];
-  float reach;
+  // A capped score times log2(e) as an odd polynomial of the score (bf16 pools) or of c times it: four
+  // coefficients while c |score| is at most reach4, six up to reach6.
+  float2 tanh4[4], tanh6[6];
+  float reach4, reach6;
 };
 
 // ------------------------------------------------------------------ units of work
@@ -658,7 +667,8 @@ struct AttendCfg {
   // A piece's key tiles last to first: where scores fall with distance the first tile then holds the
   // largest, and the reference maximum hardly ever moves again.
   static constexpr bool REVERSE = BIAS;
-  // Loops over 32 columns instead of 64.
+  // Loops over 32 columns instead of 64: prefixes over an E4M3 cache, cap 30, 360 us against 369; four
+  // tokens 14.3 against 16.4; but four capped prompts 617 against 597.
   static constexpr bool NARROW = QUANT || !SHARED;
   static constexpr int HALVES = D / 64;                 // 128-byte column chunks of a bf16 row
   static constexpr int TILE = kKeys * D * 2;            // bytes of a Q, K or V tile
@@ -1095,7 +1105,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               slow = (x.prefix > 0 && key0 + kKeys - 1 > x.pos + tok0) ||
                      __any_sync(0xffffffffu, fabsf(slope) > 2.f);
             float top = -INFINITY;
-            [[maybe_unused]] uint32_t far = 0;           // bit b: block b has scores past the polynomial's reach
+            // bit b: block b has scores past the shorter polynomial's reach; bit 8 + b: past the longer's
+            [[maybe_unused]] uint32_t far = 0;
             // whether column e of block b is hidden from this row
             auto hidden = [&](int b, int e) { return static_cast<unsigned>(32 * b + e - first) >= seen; };
             if (!slow) {
@@ -1125,8 +1136,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                   mx[j / 16] = fmaxf(y[0], y[1]) * (j ? f.y : f.x);
                   if constexpr (C::CAP) peak = fmaxf(peak, fmaxf(a[0], a[1]) * (j ? f.y : f.x));
                 }
-                if constexpr (C::CAP)
-                  far |= __any_sync(0xffffffffu, live && peak > p.reach) ? 1u << b : 0u;
+                if constexpr (C::CAP) {
+                  if (__any_sync(0xffffffffu, live && peak > p.reach4))
+                    far |= (__any_sync(0xffffffffu, live && peak > p.reach6) ? 0x100u : 1u) << b;
+                }
                 float y = fmaxf(mx[0], mx[1]);
                 if constexpr (C::BIAS) {                 // no more than the largest bias on top
                   if constexpr (C::CAP) y = y == -INFINITY ? y : p.cap2 * tanh_any(y);
@@ -1234,8 +1247,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (page == kEarly / 16 - 1) announce_early();
               }
             } else {
-              // The weights of block j.
-              auto weights = [&](const uint32_t *s, int j, float2 f, auto masked, auto past_reach) {
+              // The weights of block j; length: the polynomial's, 0 where no polynomial does.
+              auto weights = [&](const uint32_t *s, int j, float2 f, auto masked, auto length) {
                 float2 v = make_float2(0.f, 0.f);
                 if constexpr (C::QUANT) v = lds_f32x2(sc + 32 + 8 * j);
                 uint32_t packed[16];
@@ -1254,14 +1267,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     float2 y = as_pair(s, 2 * e);
                     if constexpr (!C::CAP) {
                       y = fma2(y, make_float2(c1, c1), shift);
-                    } else if constexpr (decltype(past_reach)::value) {
+                    } else if constexpr (decltype(length)::value == 0) {
                       const float2 t = make_float2(tanh_any(y.x * c1), tanh_any(y.y * c1));
                       y = fma2(t, make_float2(p.cap2, p.cap2), shift);
                     } else {
+                      constexpr int N = decltype(length)::value;
+                      const float2 *k = N == 6 ? p.tanh6 : p.tanh4;
                       const float2 t = C::QUANT ? mul2(y, make_float2(c1, c1)) : y, u = mul2(t, t);
-                      y = fma2(u, p.tanh[5], p.tanh[4]);
+                      y = fma2(u, k[N - 1], k[N - 2]);
 #pragma unroll
-                      for (int i = 3; i >= 0; --i) y = fma2(u, y, p.tanh[i]);
+                      for (int i = N - 3; i >= 0; --i) y = fma2(u, y, k[i]);
                       y = fma2(t, y, shift);
                     }
                     if constexpr (C::BIAS) shift = add2(shift, step);
@@ -1280,10 +1295,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 tc_st16(tS + 16 * j, packed);
               };
               auto of_block = [&](const uint32_t *s, int j, float2 f, auto masked) {
-                if (C::CAP && (far >> j & 1))
-                  weights(s, j, f, masked, std::true_type{});
-                else
-                  weights(s, j, f, masked, std::false_type{});
+                if (C::CAP && (far >> j & 0x101)) {
+                  if (far >> j & 0x100)
+                    weights(s, j, f, masked, std::integral_constant<int, 0>{});
+                  else
+                    weights(s, j, f, masked, std::integral_constant<int, 6>{});
+                } else {
+                  weights(s, j, f, masked, std::integral_constant<int, 4>{});
+                }
               };
               auto narrow_loop = [&](auto masked) {
                 uint32_t s[32];

@@ -19,17 +19,19 @@ pa_status run_attend_scored(const ScoredCall &x) {
     p.cap2 = x.score.softcap * kLog2e;
     // tanh's coefficients; on bf16 pools with c^(2 i + 1) in them, as far as fp32 holds that: all six
     // for c >= 2^-11 (heads of 128: caps up to 180), four for scores up to half the cap to 2^-16 (caps
-    // up to 5,800), two for scores up to a fiftieth of it below.  Scores beyond, and caps below 3.5e-4,
-    // take the slow form.
+    // up to 5,800), two for scores up to a fiftieth of it below.  Scores beyond, and all those of caps
+    // below 3.5e-4, go through the exponential.
     const double c = x.s.kv_dtype == PA_KV_BF16 ? p.c : 1.0;
     const double six[6] = {kTanh0, kTanh1, kTanh2, kTanh3, kTanh4, kTanh5};
     const double four[6] = {kTanhHalf0, kTanhHalf1, kTanhHalf2, kTanhHalf3}, two[6] = {1.0, -1.0 / 3};
-    const double *k = c >= 0x1p-11 ? six : c >= 0x1p-16 ? four : two;
-    p.reach = c > 0x1p8 ? -1.f : k == six ? 1.f : k == four ? 0.5f : 0.02f;
+    const double *small = c >= 0x1p-16 ? four : two, *large = c >= 0x1p-11 ? six : small;
+    p.reach4 = c > 0x1p8 ? -1.f : small == four ? 0.5f : 0.02f;
+    p.reach6 = c > 0x1p8 ? -1.f : large == six ? 1.f : p.reach4;
     double power = p.cap2 * c;
     for (int i = 0; i < 6; ++i, power *= c * c) {
-      const float y = static_cast<float>(k[i] * power);
-      p.tanh[i] = make_float2(y, y);
+      const float y = static_cast<float>(large[i] * power), z = static_cast<float>(small[i] * power);
+      p.tanh6[i] = make_float2(y, y);
+      if (i < 4) p.tanh4[i] = make_float2(z, z);
     }
   }
   CUtensorMap maps[3];

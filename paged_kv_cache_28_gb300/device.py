@@ -222,6 +222,64 @@ class DeviceBatch:
                              self.batch.sm_scale, workspace, self.err, stream)
         return out
 
+    # -- changed scores, several position axes, reading back ------------------------
+
+    def rope_axes_and_cache(self, q, k_new, v_new, pair_axis, positions, slot_mapping, cos_sin,
+                            q_out=None, stream=None, interleaved: bool = False) -> torch.Tensor:
+        """rope_and_cache with positions [num_axes, T]; pair_axis: the axis of each of the
+        rotary_dim / 2 pairs."""
+        b = self.batch
+        if q_out is None:
+            with on_stream(stream, self.device):
+                q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+        shape = _lib.make_shape(q.shape[0], b.Hq, b.Hkv, b.D, b.block_size, b.nblocks,
+                                b.max_blocks, self.shape.kv_dtype)
+        _lib.pa_rope_axes_and_cache(shape, pair_axis, cos_sin, positions, q_out, q, k_new, v_new,
+                                    self.k_pool, self.v_pool, self.k_scale, self.v_scale,
+                                    slot_mapping, self.err, stream, interleaved)
+        return q_out
+
+    def extend_scored(self, q, query_offsets, out=None, stream=None, window: int = 0,
+                      softcap: float = 0.0, slopes=None, prefix_lens=None,
+                      workspace=None) -> torch.Tensor:
+        """pa_extend_scored (out and workspace as in extend)."""
+        if workspace is None:
+            workspace = self.attend_workspace(q.shape[0], stream)
+        if out is None:
+            with on_stream(stream, self.device):
+                out = torch.zeros_like(q)
+        _lib.pa_extend_scored(self.shape, out, q, query_offsets, self.k_pool, self.v_pool,
+                              self.k_scale, self.v_scale, self.block_tables, self.seq_lens,
+                              self.batch.sm_scale, workspace, self.err, stream, window, softcap,
+                              slopes, prefix_lens)
+        return out
+
+    def decode_scored(self, out=None, stream=None, window: int = 0, softcap: float = 0.0,
+                      slopes=None, workspace=None) -> torch.Tensor:
+        """pa_decode_scored of the batch's queries, into bf16 [B, Hq, D]; workspace: the caller's,
+        or one for this call alone."""
+        with on_stream(stream, self.device):
+            if workspace is None:
+                nbytes = _lib.pa_decode_workspace_bytes(
+                    self.shape, default_num_segments(self.shape, self.device))
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            if out is None:
+                out = torch.empty_like(self.q)
+        _lib.pa_decode_scored(self.shape, out, self.q, self.k_pool, self.v_pool, self.k_scale,
+                              self.v_scale, self.block_tables, self.seq_lens, self.batch.sm_scale,
+                              workspace, self.err, stream, window, softcap, slopes)
+        return out
+
+    def read_cache(self, offsets, total_tokens: int, starts=None, stream=None):
+        """pa_read_cache: (K, V) [total_tokens, Hkv, D] bf16, zero in the rows of no sequence."""
+        b = self.batch
+        with on_stream(stream, self.device):
+            k, v = (torch.zeros((total_tokens, b.Hkv, b.D), dtype=torch.bfloat16,
+                                device=self.device) for _ in range(2))
+        _lib.pa_read_cache(self.shape, k, v, self.k_pool, self.v_pool, self.k_scale, self.v_scale,
+                           self.block_tables, self.seq_lens, offsets, starts, self.err, stream)
+        return k, v
+
     # -- Quest page selection ------------------------------------------------------
 
     def quest_summary_slots(self) -> torch.Tensor:

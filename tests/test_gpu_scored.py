@@ -492,3 +492,46 @@ def test_a_layer_from_its_prompt_to_its_next_tokens(kind):
         if kind != "bf16":
             bound = bound + t1 * E / 2 * float(vr.abs().max())
         assert ((out[t0:t1].double() - ref).abs() <= bound).all(), (t0, t1)
+
+
+def test_device_batch_on_a_stream_beside_a_busy_one():
+    """DeviceBatch's calls on another stream, whose new tensors are made in its order."""
+    from paged_kv_cache_28_gb300 import workload as wl
+    from paged_kv_cache_28_gb300.device import DeviceBatch, rope_table
+    batch = wl.make("tiny")
+    dev = DeviceBatch(batch, device="cuda")
+    dev.reshape_and_cache()
+    B, Hq = batch.B, batch.Hq
+    rows = torch.arange(B + 1, dtype=torch.int32, device="cuda")
+    offsets = torch.cat([rows[:1] * 0, dev.seq_lens.cumsum(0).int()])
+    total = int(offsets[-1])
+    slopes = torch.linspace(0.01, 0.5, Hq, device="cuda")
+    positions = torch.stack([dev.seq_lens - 1, dev.seq_lens % 7]).int()
+    pair = [j % 2 for j in range(batch.D // 2)]
+    table = rope_table(int(dev.seq_lens.max()) + 1, batch.D)
+    calls = dict(
+        extend=lambda st: dev.extend_scored(dev.q, rows, softcap=9.0, slopes=slopes, stream=st),
+        decode=lambda st: dev.decode_scored(softcap=9.0, slopes=slopes, stream=st),
+        read=lambda st: torch.cat(dev.read_cache(offsets, total, stream=st)),
+        rope=lambda st: dev.rope_axes_and_cache(dev.q, dev.k_new, dev.v_new, pair, positions, dev.slot_mapping,
+                                                table, stream=st))
+    first = dev.k_pool.view(-1, batch.Hkv, batch.D)[int(batch.block_tables[0, 0]) * batch.block_size].clone()
+    want = {k: f(None) for k, f in calls.items()}        # (rope, the last, writes the same tokens anew)
+    assert dev.read_err() == 0
+    assert torch.equal(want["read"][0], first)
+    torch.cuda.synchronize()
+    side, junk = torch.cuda.Stream(), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for stream in (side, side.cuda_stream):
+        for name in ("extend", "decode", "rope"):        # (before rope writes its keys again: the same bits)
+            for i in range(4):
+                junk.fill_(i)                            # the current stream is busy
+            got = calls[name](stream)
+            side.synchronize()
+            if name == "rope":
+                assert torch.equal(got.view(torch.int16), want[name].view(torch.int16))
+            else:
+                assert got.isfinite().all()
+    assert dev.read_err() == 0
+    after = {k: calls[k](None) for k in ("extend", "decode")}
+    for name in after:
+        assert torch.equal(calls[name](side).view(torch.int16), after[name].view(torch.int16))
