@@ -50,7 +50,7 @@
 // 832; in loops over 64 columns that read a tile twice 597, with four coefficients where the scores are
 // small 561 (plain scores: 387).  The chunk with a cap takes 1.21 ms, 945 TFLOP/s: 13 fp32
 // operations a score (at 2 cycles a pair), of them the polynomial 8.  With a distance bias it takes
-// 0.84 ms, within 6 % of plain scores: tiles run last to first, so that the reference maximum is
+// 0.82 ms, within 2 % of plain scores: tiles run last to first, so that the reference maximum is
 // found at once (before: 1.29 ms), and the bias is one addition a pair.
 #pragma once
 
@@ -1094,15 +1094,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // Changed scores.  A tile takes a fast form, where the maximum is taken from the scores and
             // the change is part of the exponents' arithmetic, or a slow one, which first writes the
             // exponents over the scores.  Slow are tiles with a bias and keys ahead of their query (in a
-            // prefix), or with so steep a bias that the fast form's bound on the maximum could be too far
-            // from it.  Both are loops that read the scores twice: unrolled over the tile, with the plain
-            // softmax's registers, the instructions did not come fast enough.
+            // prefix), with so steep a bias that the fast form's bound on the maximum could be too far from
+            // it (62 octaves, at 2 a key), or, without a cap, that some row does not see whole (a masked
+            // loop of its own for these: chunk 840 us against 817, windows of 1,024 keys 148 against 152).
+            // Both are loops that read the scores twice: unrolled over the tile, with the plain softmax's
+            // registers, the instructions did not come fast enough.
             auto as_pair = [](const uint32_t *s, int e) {
               return make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
             };
             bool slow = false;
             if constexpr (C::BIAS)
-              slow = (x.prefix > 0 && key0 + kKeys - 1 > x.pos + tok0) ||
+              slow = (!C::CAP && edge) || (x.prefix > 0 && key0 + kKeys - 1 > x.pos + tok0) ||
                      __any_sync(0xffffffffu, fabsf(slope) > 2.f);
             float top = -INFINITY;
             // bit b: block b has scores past the shorter polynomial's reach; bit 8 + b: past the longer's
@@ -1160,7 +1162,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                   scan(s, j, k_factors(j), masked);
                 }
               };
-              if (edge) {
+              if (C::CAP && edge) {
                 narrow_loop(std::true_type{});
               } else if constexpr (C::NARROW) {
                 narrow_loop(std::false_type{});
@@ -1316,7 +1318,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                   if (j == kEarly / 32 - 1) announce_early();
                 }
               };
-              if (edge) {
+              if (C::CAP && edge) {
                 narrow_loop(std::true_type{});
               } else if constexpr (C::NARROW) {
                 narrow_loop(std::false_type{});

@@ -43,16 +43,23 @@ struct RopeParams {
   uint32_t axes[4];
 };
 
+// How many axes the positions have, and whether pairs 4 i .. 4 i + 3 share theirs, so that their
+// angles lie side by side in the table: a kernel for each.  9,485 tokens into an E4M3 cache take 107 us
+// with one axis, 121 with three in fours, 135 with three in turn.  The bf16 kernels, which load
+// each angle for several heads, take them pair by pair (16,384 tokens: 109 us with one axis, 115 to
+// 119 with three either way).
+constexpr int kOneAxis = 0, kInFours = 1, kAnyPair = 2;
+
 // The rows of the table that a token's pairs turn by: one, or one for each axis.
 struct AxisRows {
   int pos[PA_MAX_AXES];
 };
-template <bool kAxes>
-using Place = std::conditional_t<kAxes, AxisRows, int>;
+template <int kAxes>
+using Place = std::conditional_t<kAxes != kOneAxis, AxisRows, int>;
 
-template <bool kAxes>
+template <int kAxes>
 __device__ __forceinline__ Place<kAxes> load_place(const RopeParams &p, int t) {
-  if constexpr (kAxes) {
+  if constexpr (kAxes != kOneAxis) {
     AxisRows x;
 #pragma unroll
     for (int a = 0; a < PA_MAX_AXES; ++a)
@@ -100,6 +107,7 @@ struct Item {
   float cos[8], sin[8];
 };
 
+template <int kAxes>
 __device__ __forceinline__ void load_item(const RopeParams &p, int item, int pos, Item &x) {
   x.rotates = item < p.r / 16;
   if (!x.rotates) return;
@@ -119,16 +127,22 @@ __device__ __forceinline__ int row_of(const AxisRows &at, int a) {
   for (int i = 1; i < PA_MAX_AXES; ++i) pos = a == i ? at.pos[i] : pos;
   return pos;
 }
+template <int kAxes>
 __device__ __forceinline__ void load_item(const RopeParams &p, int item, const AxisRows &at, Item &x) {
   x.rotates = item < p.r / 16;
   if (!x.rotates) return;
-  const uint32_t axes = (p.axes[item >> 1] >> (16 * (item & 1))) & 0xFFFFu;        // of the eight pairs
-  if (axes == (axes & 3u) * 0x5555u) return load_item(p, item, row_of(at, axes & 3), x);
+  const uint32_t axes = p.axes[item >> 1] >> (16 * (item & 1));        // of the eight pairs, two bits each
+  constexpr int N = kAxes == kInFours ? 4 : 1;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 8; e += N) {
     const float *row = p.cos_sin + static_cast<int64_t>(row_of(at, axes >> (2 * e) & 3)) * p.r + 8 * item + e;
-    x.cos[e] = __ldg(row);
-    x.sin[e] = __ldg(row + p.r / 2);
+    if constexpr (N == 4) {
+      *reinterpret_cast<float4 *>(x.cos + e) = __ldg(reinterpret_cast<const float4 *>(row));
+      *reinterpret_cast<float4 *>(x.sin + e) = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
+    } else {
+      x.cos[e] = __ldg(row);
+      x.sin[e] = __ldg(row + p.r / 2);
+    }
   }
 }
 
@@ -154,7 +168,7 @@ __device__ __forceinline__ void rotate_item(const Item &x, uint4 &a, uint4 &b) {
 // Heads first, first + step, ... < last of token t, counted through the queries, then (bf16
 // pools) the keys and the values; this thread's item of each.  Four heads' loads are in flight
 // at once, the first four's before the token's slot, position and angles are there.
-template <int D, bool kInterleaved, bool kAxes>
+template <int D, bool kInterleaved, int kAxes>
 __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int item, int first, int step,
                                            int last, bool report) {
   constexpr int U = 4;
@@ -178,7 +192,7 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int item,
   const Place<kAxes> at = load_place<kAxes>(p, t);
   if (!token_ok(p, slot, at, report)) return;
   Item x;
-  load_item(p, item, at, x);
+  load_item<kAxes>(p, item, at, x);
   for (int h0 = first; h0 < last; h0 += step * U) {
     if (h0 > first) load(h0);
 #pragma unroll
@@ -198,7 +212,7 @@ __device__ __forceinline__ void rope_heads(const RopeParams &p, int t, int item,
 }
 
 // The queries alone: heads first, first + step, ... of token t (D = 128), two at a time.
-template <bool kInterleaved, bool kAxes>
+template <bool kInterleaved, int kAxes>
 __device__ __forceinline__ void rope_queries(const RopeParams &p, int t, int item, int first, int step) {
   constexpr int D = 128, U = 2;
   const bool split = !kInterleaved && item < p.r / 16;
@@ -220,7 +234,7 @@ __device__ __forceinline__ void rope_queries(const RopeParams &p, int t, int ite
   const Place<kAxes> at = load_place<kAxes>(p, t);
   if (!token_ok(p, slot, at, false)) return;
   Item x;
-  load_item(p, item, at, x);
+  load_item<kAxes>(p, item, at, x);
 #pragma unroll 1
   for (int h = first; h < p.Hq; h += U * step) {
 #pragma unroll
@@ -238,7 +252,7 @@ __device__ __forceinline__ void rope_queries(const RopeParams &p, int t, int ite
 
 // BF16 pools: blockIdx.x is the token; blockIdx.y a share of its heads.  Six CTAs an SM (80 registers)
 // keep the memory busiest: 112, 111, 109, 136 us for 16,384 tokens with 95 registers, 5, 6 and 8 CTAs.
-template <int D, bool kInterleaved, bool kAxes>
+template <int D, bool kInterleaved, int kAxes>
 __global__ void __launch_bounds__(128, 6) rope_bf16_kernel(const RopeParams p) {
   pdl_trigger();
   pdl_wait();
@@ -259,7 +273,7 @@ __global__ void __launch_bounds__(128, 6) rope_bf16_kernel(const RopeParams p) {
 // The scale is absmax times the fp32 reciprocal of the largest code (pa_reshape_and_cache
 // divides: the two differ by one unit in the last place at most); codes are x / scale, rounded,
 // in both.
-template <class Codec, bool kInterleaved, bool kAxes>
+template <class Codec, bool kInterleaved, int kAxes>
 __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, int cache_ctas, int tokens,
                                                             int shares) {
   using Word = typename Codec::Word;
@@ -307,10 +321,24 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
     const int64_t blk = slot >> (p.bs == 16 ? 4 : 5), blk0 = blk * p.bs;
     auto in_block = [&](int u, int64_t o) { return same_block(u, o, blk0); };
     int earlier = 0, later = 0;
+    bool look = true;
+    if constexpr (kAxes != kOneAxis) {
+      // (a token of the block by its slot alone; with several positions each the look at them would
+      // be most of the loop)
+      int any = 0;
 #pragma unroll 8
-    for (int u = tid; u < t - 1; u += 256) earlier |= in_block(u, p.slots[u]);
+      for (int u = tid; u < p.T; u += 256) {
+        const int64_t o = p.slots[u];
+        any |= o >= blk0 && o < blk0 + p.bs && (u < t - 1 || u >= t + 256);
+      }
+      look = __syncthreads_or(any);
+    }
+    if (look) {
 #pragma unroll 8
-    for (int u = t + 256 + tid; u < p.T; u += 256) later |= in_block(u, p.slots[u]);
+      for (int u = tid; u < t - 1; u += 256) earlier |= in_block(u, p.slots[u]);
+#pragma unroll 8
+      for (int u = t + 256 + tid; u < p.T; u += 256) later |= in_block(u, p.slots[u]);
+    }
     const int others = __syncthreads_or(earlier | later);
     if (others && __syncthreads_or(earlier)) continue;
     const int end = others ? p.T : min(p.T, t + 256);
@@ -352,17 +380,10 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
         const bool upper = !kInterleaved && lane * 4 >= p.r / 2;
         const int j = kInterleaved ? lane * 2 : lane * 4 - (upper ? p.r / 2 : 0);
         const int peer = (upper ? lane - p.r / 8 : lane + p.r / 8) & 31;
-        // several axes: the first pair's positions, and whether the lane's other pairs share them
+        // the positions of the lane's first pair
         const int32_t *positions = p.positions;
-        [[maybe_unused]] bool alike = true;
-        if constexpr (kAxes) {
-          if (turns) {
-            const int axis = axis_of(p, j);
-            positions += static_cast<int64_t>(axis) * p.T;
-#pragma unroll
-            for (int e = 1; e < (kInterleaved ? 2 : 4); ++e) alike = alike && axis_of(p, j + e) == axis;
-          }
-        }
+        if constexpr (kAxes != kOneAxis)
+          if (turns) positions += static_cast<int64_t>(axis_of(p, j)) * p.T;
         float s = *scale;
         ByReciprocal over(1.f);
         uint32_t held = 0;                               // rows whose codes are in shared memory
@@ -379,15 +400,15 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
             if (!is_v) {
               const float v[4] = {bf16_lo(x[i].x), bf16_hi(x[i].x), bf16_lo(x[i].y), bf16_hi(x[i].y)};
               const float *row = p.cos_sin + static_cast<int64_t>(positions[members[i0 + i]]) * p.r + j;
-              // (several axes) the same for pair j + e
-              auto other_row = [&](int e) {
+              // the same for pair j + e, where pairs have axes of their own
+              [[maybe_unused]] auto other_row = [&](int e) {
                 const int64_t axis = axis_of(p, j + e);
                 return p.cos_sin + static_cast<int64_t>(p.positions[axis * p.T + members[i0 + i]]) * p.r + j + e;
               };
               if constexpr (kInterleaved) {
                 if (turns) {
                   float2 c, sn;
-                  if (!kAxes || alike) {
+                  if constexpr (kAxes != kAnyPair) {
                     c = __ldg(reinterpret_cast<const float2 *>(row));
                     sn = __ldg(reinterpret_cast<const float2 *>(row + p.r / 2));
                   } else {
@@ -404,7 +425,7 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
                 const float w[4] = {bf16_lo(w0), bf16_hi(w0), bf16_lo(w1), bf16_hi(w1)};
                 if (turns) {
                   alignas(16) float cc[4], ss[4];
-                  if (!kAxes || alike) {
+                  if constexpr (kAxes != kAnyPair) {
                     const float4 c = __ldg(reinterpret_cast<const float4 *>(row));
                     const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + p.r / 2));
                     cc[0] = c.x, cc[1] = c.y, cc[2] = c.z, cc[3] = c.w;
@@ -481,7 +502,7 @@ __global__ void __launch_bounds__(256, 3) rope_quant_kernel(const RopeParams p, 
   }
 }
 
-template <int D, bool I, bool A>
+template <int D, bool I, int A>
 cudaError_t launch_bf16(const RopeParams &p, cudaStream_t stream) {
   // few tokens: their heads go over several CTAs, about two per SM
   constexpr int kHeads = 128 / (D / 16);
@@ -490,7 +511,7 @@ cudaError_t launch_bf16(const RopeParams &p, cudaStream_t stream) {
   return launch_pdl(rope_bf16_kernel<D, I, A>, dim3(p.T, shares), dim3(128), 0, stream, p);
 }
 
-template <class Codec, bool I, bool A>
+template <class Codec, bool I, int A>
 cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
   // a prompt's tokens mostly leave at once, so a CTA looks at several; a batch's stay
   const int tokens = p.T >= 2048 ? 8 : 1;
@@ -505,11 +526,12 @@ cudaError_t launch_quant(const RopeParams &p, cudaStream_t stream) {
                     stream, p, cache_ctas, tokens, shares);
 }
 
-template <bool I, bool A>
+template <bool I, int A>
 cudaError_t launch_kind(const pa_shape &s, const RopeParams &p, cudaStream_t stream) {
   if (s.kv_dtype == PA_KV_FP8_E4M3) return launch_quant<Fp8Codec, I, A>(p, stream);
   if (s.kv_dtype == PA_KV_INT4) return launch_quant<Int4Codec, I, A>(p, stream);
-  return s.D == 128 ? launch_bf16<128, I, A>(p, stream) : launch_bf16<64, I, A>(p, stream);
+  constexpr int B = A == kOneAxis ? kOneAxis : kAnyPair;
+  return s.D == 128 ? launch_bf16<128, I, B>(p, stream) : launch_bf16<64, I, B>(p, stream);
 }
 
 }  // namespace
@@ -546,12 +568,18 @@ pa_status run_rope_and_cache(const pa_shape &s, const pa_rope &rope, const pa_ro
   const bool i = rope.interleaved;
   cudaError_t e;
   if (axes) {
+    bool in_fours = true;
     p.num_axes = axes->num_axes;
-    for (int j = 0; j < rope.rotary_dim / 2; ++j)
+    for (int j = 0; j < rope.rotary_dim / 2; ++j) {
       p.axes[j / 16] |= static_cast<uint32_t>(axes->pair_axis[j]) << (2 * (j % 16));
-    e = i ? launch_kind<true, true>(s, p, stream) : launch_kind<false, true>(s, p, stream);
+      in_fours = in_fours && axes->pair_axis[j] == axes->pair_axis[j & ~3];
+    }
+    if (in_fours)
+      e = i ? launch_kind<true, kInFours>(s, p, stream) : launch_kind<false, kInFours>(s, p, stream);
+    else
+      e = i ? launch_kind<true, kAnyPair>(s, p, stream) : launch_kind<false, kAnyPair>(s, p, stream);
   } else {
-    e = i ? launch_kind<true, false>(s, p, stream) : launch_kind<false, false>(s, p, stream);
+    e = i ? launch_kind<true, kOneAxis>(s, p, stream) : launch_kind<false, kOneAxis>(s, p, stream);
   }
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -389,6 +389,22 @@ def test_same_bits_captured_and_on_two_streams(decode):
                 b.seq_lens -= 1
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
+def test_same_bits_whatever_ran_before(kind):
+    """What an earlier call left in shared memory and beyond a sequence's length is no part of a result:
+    the form that a tile takes may not depend on it."""
+    for change in CHANGES.values():
+        for decode in (False, True):
+            n, L = ([1] * 3, [130, 7, 300]) if decode else ([90, 3, 200], [130, 7, 300])
+            b = Scored(n, L, 2, 8, 128, 16, kind, qmul=1.0, decode=decode, seed=41, **change)
+            other = Scored(n, [x + 77 for x in L], 2, 8, 128, 16, kind, qmul=200.0, decode=decode, seed=42, **change)
+            want = b.run()
+            b.check(want)
+            for _ in range(3):
+                other.run()
+                assert torch.equal(b.run().view(torch.int16), want.view(torch.int16))
+
+
 def test_outputs_on_a_16_byte_boundary():
     for decode in (False, True):
         b = Scored([1] * 2 if decode else [40, 1], [300, 40], 2, 3, 64, 16, "bf16", cap=9.0, decode=decode, seed=33)
