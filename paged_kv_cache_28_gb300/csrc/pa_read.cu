@@ -203,8 +203,8 @@ pa_status run_read_cache(const pa_shape &s, void *k_out, void *v_out, const void
   p.wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31u) == 0;
   // four rows a thread; fewer in small calls, so that there are about two CTAs an SM
   const int per_row = s.Hkv * s.D / 16, step = std::max(1, kThreads / per_row);
-  p.rows = std::max(1, std::min({kMaxRows, 4 * step, (T + 303) / 304}));
-  const dim3 grid((T + p.rows - 1) / p.rows);
+  p.rows = std::max(1, std::min({kMaxRows, 4 * step, T / 304}));
+  const dim3 grid((T - 1) / p.rows + 1);
   cudaError_t e;
   if (s.kv_dtype == PA_KV_FP8_E4M3)
     e = launch_pdl(read_kernel<PA_KV_FP8_E4M3, 128>, grid, dim3(kThreads), 0, stream, p);

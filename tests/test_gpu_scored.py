@@ -242,12 +242,15 @@ def test_slopes_of_any_size_and_sign(slopes, kind, decode):
         Scored(n, [900, 130], 1, 8, 128, 16, kind, slopes=slopes, qmul=1.0, decode=decode, seed=10).check()
 
 
-def test_negative_scale():
-    for decode in (False, True):
-        for change in CHANGES.values():
-            b = Scored([1, 1] if decode else [150, 1], [400, 300], 2, 4, 128, 16, "fp8", decode=decode, seed=11, **change)
-            b.scale = -b.scale
-            b.check()
+@pytest.mark.parametrize("factor", [-1.0, 0.0, 1e-4, 300.0])
+def test_scales_of_any_size_and_sign(factor):
+    for kind in ("bf16", "fp8"):
+        for decode in (False, True):
+            for change in CHANGES.values():
+                b = Scored([1, 1] if decode else [150, 1], [400, 300], 2, 4, 128, 16, kind, decode=decode, seed=11,
+                           **change)
+                b.scale *= factor
+                b.check()
 
 
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "int4"])
