@@ -567,7 +567,8 @@ typedef struct {
  *     out[row][h][:] = sum_j softmax_j(a) V_b[j]
  * over the j that the row sees; a window bounds them below as in pa_extend (p - window < j).  What
  * pa_extend says of its arguments, workspace (pa_attend_workspace_bytes), cached values, errors,
- * rounding and limits holds here; the capped score is off by 2^-20 of itself at most.  A score with
+ * rounding and limits holds here; the capped score is off by 2^-20 of itself at most, and with
+ * slopes weights below 2^-40 of a row's largest may count as 0.  A score with
  * neither cap, slopes nor prefix gives pa_extend's result.
  */
 pa_status pa_extend_scored(const pa_shape *shape, void *out, const void *q,

@@ -71,6 +71,7 @@ namespace {
 constexpr bool kScored = PA_ATTEND_SCORED;
 constexpr int kKeys = 128;              // keys per tile
 constexpr int kRows = 128;              // rows per tile
+constexpr float kLeastScale = -24.f;    // log2 of the smallest V scale that a biased exponent takes whole
 constexpr int kEarly = 64;              // keys whose weights are announced ahead of the rest
 constexpr float kMaxJump = 8.f;         // the reference maximum moves only past this many octaves
 
@@ -1095,17 +1096,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // the change is part of the exponents' arithmetic, or a slow one, which first writes the
             // exponents over the scores.  Slow are tiles with a bias and keys ahead of their query (in a
             // prefix), with so steep a bias that the fast form's bound on the maximum could be too far from
-            // it (62 octaves, at 2 a key), or, without a cap, that some row does not see whole (a masked
-            // loop of its own for these: chunk 840 us against 817, windows of 1,024 keys 148 against 152).
+            // it (62 octaves, at 2 a key), with a page whose V scale is below 2^-24, or, without a cap, that
+            // some row does not see whole (a masked loop of its own for these: chunk 840 us against 817,
+            // windows of 1,024 keys 148 against 152).
             // Both are loops that read the scores twice: unrolled over the tile, with the plain softmax's
             // registers, the instructions did not come fast enough.
             auto as_pair = [](const uint32_t *s, int e) {
               return make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1]));
             };
             bool slow = false;
-            if constexpr (C::BIAS)
+            if constexpr (C::BIAS) {
+              bool mine = fabsf(slope) > 2.f;
+              if constexpr (C::QUANT) mine |= __uint_as_float(lds_u32(sc + 32 + 4 * (lane & 7))) < kLeastScale;
               slow = (!C::CAP && edge) || (x.prefix > 0 && key0 + kKeys - 1 > x.pos + tok0) ||
-                     __any_sync(0xffffffffu, fabsf(slope) > 2.f);
+                     __any_sync(0xffffffffu, mine);
+            }
             float top = -INFINITY;
             // bit b: block b has scores past the shorter polynomial's reach; bit 8 + b: past the longer's
             [[maybe_unused]] uint32_t far = 0;
@@ -1225,13 +1230,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(p_early(t));    // the second product may begin
             };
-            // Code pools: V's scale enters in the exponent, and leaves the sums of its page again.
+            // Code pools: V's scale enters in the exponent, and leaves the sums of its page again.  A biased
+            // row's reference may lie 62 octaves above its largest exponent (from any of its tiles), and a
+            // scale of 0 counts as 100 octaves down: together past 2^-126, where the exponential gives 0 and
+            // the sum would lose the page's weights.  So the exponent takes a scale down to 2^-24 only, and
+            // what is below that, a power of two, multiplies the rounded weights, in the slow form: where
+            // no scale is that small, the vote for it takes E4M3 chunks with a window from 264 to 269 us, the
+            // loops doing it themselves took 283.  Weights down to 2^-40 of
+            // the row's largest count, and a row with a reference has a sum above 0, which a jump asks for.
             if (slow) {
 #pragma unroll 1
               for (int page = 0; page < 8; ++page) {
                 uint32_t o[16], packed[8];
                 tc_ld16(o, tS + 16 * page);
-                const float lv = of_page(sc + 32 + 4 * page, 0.f);
+                float lv = of_page(sc + 32 + 4 * page, 0.f);
+                [[maybe_unused]] float rest = 0.f;
+                if constexpr (C::QUANT) {
+                  rest = fminf(floorf(lv - kLeastScale), 0.f);             // in [-76, 0]
+                  lv -= rest;
+                }
                 const float2 shift = make_float2(neg + lv, neg + lv);
                 float2 mine = make_float2(0.f, 0.f);
                 tc_wait_ld16(o);
@@ -1245,6 +1262,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 const float back = C::QUANT ? ex2(-lv) : 1.f;
                 sum[0] = fma2(mine, make_float2(back, back), sum[0]);
+                if constexpr (C::QUANT) {
+                  const uint32_t by = static_cast<uint32_t>(127 + static_cast<int>(rest)) * 0x00800080u;
+                  if (rest < 0.f) {
+#pragma unroll
+                    for (uint32_t &w : packed) asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(by));
+                  }
+                }
                 tc_st8(tS + 8 * page, packed);           // over columns that are already read
                 if (page == kEarly / 16 - 1) announce_early();
               }
@@ -1481,7 +1505,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       };
       // block id to pool row (and the scales on their way), when it has come
       auto resolve = [&](Chunk &c) {
-        c.ks = c.vs = 0.f;
+        c.ks = 0.f;
+        c.vs = C::BIAS && c.row < 0 ? 1.f : 0.f;         // (a page that no row sees has no small scale)
         if (c.row >= 0) {
           if (c.row < p.nblocks) {
             if constexpr (C::QUANT) {
