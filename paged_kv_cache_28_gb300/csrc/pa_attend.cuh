@@ -1549,8 +1549,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             float *sc = reinterpret_cast<float *>(scales[st][tiles % C::SCALES]);
             if ((lane >> 3) == here) {
               // c times K's scale and log2 of V's, both kept above zero: a zero scale's codes add
-              // nothing, and -inf stays -inf
-              sc[lane & 7] = fmaxf(cur.ks * p.c, 1e-30f);
+              // nothing, and -inf stays -inf (capped scores are hidden after their change, and need
+              // no such care)
+              sc[lane & 7] = C::CAP ? cur.ks * p.c : fmaxf(cur.ks * p.c, 1e-30f);
               sc[8 + (lane & 7)] = __log2f(fmaxf(cur.vs, 1e-30f));
             }
             __syncwarp();

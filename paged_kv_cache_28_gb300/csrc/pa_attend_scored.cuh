@@ -2,6 +2,9 @@
 // that fall with distance, or with a prefix whose tokens all see one another.
 #pragma once
 
+#include <cfloat>
+#include <cmath>
+
 #define PA_ATTEND_SCORED true
 #include "pa_attend.cuh"
 
@@ -15,18 +18,27 @@ pa_status run_attend_scored(const ScoredCall &x) {
   p.slopes = x.score.slopes;
   p.prefix_lens = x.score.prefix_lens;
   if (kScore & kCap) {
-    p.c = fmaxf(fabsf(x.sm_scale / x.score.softcap), 1e-30f);
+    // (0 with sm_scale 0, whatever the products)
+    p.c = fabsf(x.sm_scale / x.score.softcap);
     p.cap2 = x.score.softcap * kLog2e;
-    // tanh's coefficients; on bf16 pools with c^(2 i + 1) in them, as far as fp32 holds that: all six
+    // tanh's coefficients; on bf16 pools with c^(2 i + 1) in them, as far as fp32 holds all of them: six
     // for c >= 2^-11 (heads of 128: caps up to 180), four for scores up to half the cap to 2^-16 (caps
     // up to 5,800), two for scores up to a fiftieth of it below.  Scores beyond, and all those of caps
-    // below 3.5e-4, go through the exponential.
+    // below 3.5e-4 and of a c whose powers leave fp32 (with the usual scales: below 1e-15), go through
+    // the exponential.
     const double c = x.s.kv_dtype == PA_KV_BF16 ? p.c : 1.0;
     const double six[6] = {kTanh0, kTanh1, kTanh2, kTanh3, kTanh4, kTanh5};
     const double four[6] = {kTanhHalf0, kTanhHalf1, kTanhHalf2, kTanhHalf3}, two[6] = {1.0, -1.0 / 3};
-    const double *small = c >= 0x1p-16 ? four : two, *large = c >= 0x1p-11 ? six : small;
-    p.reach4 = c > 0x1p8 ? -1.f : small == four ? 0.5f : 0.02f;
-    p.reach6 = c > 0x1p8 ? -1.f : large == six ? 1.f : p.reach4;
+    auto fits = [&](const double *k) {                   // no coefficient that counts leaves fp32
+      double power = p.cap2 * c;
+      for (int i = 0; i < 6; ++i, power *= c * c)
+        if (k[i] != 0.0 && !(fabs(k[i] * power) >= FLT_MIN && fabs(k[i] * power) <= FLT_MAX)) return false;
+      return c <= 0x1p8;
+    };
+    const double *small = c >= 0x1p-16 && fits(four) ? four : two;
+    const double *large = c >= 0x1p-11 && fits(six) ? six : small;
+    p.reach4 = !fits(small) ? -1.f : small == four ? 0.5f : 0.02f;
+    p.reach6 = large == six ? 1.f : p.reach4;
     double power = p.cap2 * c;
     for (int i = 0; i < 6; ++i, power *= c * c) {
       const float y = static_cast<float>(large[i] * power), z = static_cast<float>(small[i] * power);
