@@ -635,7 +635,7 @@ pa_status pa_rope_axes_and_cache(const pa_shape *shape, const pa_rope *rope,
  * shape->Hq is ignored.  Errors found on the device: a block id outside the pool gives zeros
  * (PA_DEVERR_BLOCK_ID); positions outside [0, seq_lens[b]) give zeros, as do those past the block
  * table, and set PA_DEVERR_SEQ_LEN; a sequence whose offsets fall or leave the rows is skipped
- * (PA_DEVERR_QUERY).
+ * (PA_DEVERR_QUERY; a row that two of the others then share is either's).
  */
 pa_status pa_read_cache(const pa_shape *shape, void *k_out, void *v_out, const void *k_pool,
                         const void *v_pool, const float *k_scale, const float *v_scale,

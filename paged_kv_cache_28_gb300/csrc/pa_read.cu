@@ -45,8 +45,14 @@ __device__ __forceinline__ int pool_row(const ReadParams &p, int b, int t, int f
   return block * p.bs + static_cast<int>(pos & (p.bs - 1));
 }
 
-// The last sequence whose first row is at most t (a warp, all lanes): the bound moves by 32 looks at
-// a time, so that 16,384 sequences take three loads.
+// Whether row t is sequence b's, whose offsets neither fall nor leave the rows.
+__device__ __forceinline__ bool has_row(const ReadParams &p, int b, int t) {
+  const int q0 = p.offsets[b], q1 = p.offsets[b + 1];
+  return q0 >= 0 && q0 <= t && t < q1 && q1 <= p.T;
+}
+
+// The last sequence whose first row is at most t (a warp, all lanes), where no offset falls: the bound
+// moves by 32 looks at a time, so that 16,384 sequences take three loads.
 __device__ __forceinline__ int find_sequence(const int32_t *offsets, int B, int t, int lane) {
   int lo = 0, hi = B;                                    // offsets[lo] <= t, or lo = 0
   while (hi - lo > 1) {
@@ -108,15 +114,32 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const ReadParams p) {
       const int q0 = p.offsets[b], q1 = p.offsets[b + 1];
       if (q0 < 0 || q1 < q0 || q1 > p.T) set_err(p.err, PA_DEVERR_QUERY);
     }
+  bool lost = false;
   for (int r = warp; r < n; r += kThreads / 32) {
     const int t = static_cast<int>(t0) + r;
     const int b = find_sequence(p.offsets, p.B, t, lane);
-    if (lane == 0) {
-      const int first = p.offsets[b];
-      row_of[r] = first >= 0 && first <= t && t < p.offsets[b + 1] ? pool_row(p, b, t, first, p.err) : kLeft;
+    const bool mine = has_row(p, b, t);
+    lost |= !mine;
+    if (lane == 0) row_of[r] = mine ? pool_row(p, b, t, p.offsets[b], p.err) : kLeft;
+  }
+  if (__syncthreads_or(lost)) {                          // a row of no sequence, or the search was misled
+    int falls = 0;
+    for (int b = tid; b < p.B; b += kThreads) falls |= p.offsets[b + 1] < p.offsets[b];
+    if (__syncthreads_or(falls)) {
+      for (int r = warp; r < n; r += kThreads / 32) {
+        if (row_of[r] != kLeft) continue;
+        const int t = static_cast<int>(t0) + r;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+          const uint32_t found = __ballot_sync(0xffffffffu, b0 + lane < p.B && has_row(p, b0 + lane, t));
+          if (!found) continue;
+          const int b = b0 + __ffs(found) - 1;
+          if (lane == 0) row_of[r] = pool_row(p, b, t, p.offsets[b], p.err);
+          break;
+        }
+      }
+      __syncthreads();
     }
   }
-  __syncthreads();
   constexpr int kPieces = D / 16, kBatch = 4;
   const int per_row = p.Hkv * kPieces;
   // a thread keeps to its piece of a row: piece, piece + kThreads, ... of wide rows
