@@ -168,13 +168,23 @@ def _ptr(t):
                      "libpa takes CUDA tensors only")
 
 
-def _array_ptr(name, t, dtype, count, exact=False):
-    """Device pointer of an array that the kernels read `count` elements of, as `dtype` (None -> NULL;
-    plain ints pass through).  exact: no more than that either."""
-    if t is None or isinstance(t, int):
-        return t
-    if str(t.dtype) != dtype or t.numel() < count or (exact and t.numel() != count):
-        raise ValueError(f"{name}: {count} elements of {dtype}, not {t.numel()} of {t.dtype}")
+@functools.lru_cache(maxsize=None)
+def _dtypes():
+    import torch
+    return torch.int32, torch.float32
+
+
+def _array_ptr(name, t, count, floats=False):
+    """Device pointer of an array that the kernels read `count` elements of (None -> NULL; plain ints
+    pass through): int32, with as many elements or more, or (floats) fp32 with so many."""
+    if t is None:
+        return None
+    try:
+        n = t.nbytes
+    except AttributeError:
+        return _ptr(t)
+    if t.dtype is not _dtypes()[floats] or n < 4 * count or (floats and n > 4 * count):
+        raise ValueError(f"{name}: {count} elements of {_dtypes()[floats]}, not {t.numel()} of {t.dtype}")
     return _ptr(t)
 
 
@@ -364,14 +374,14 @@ def pa_extend_scored(shape: pa_shape, out, q, query_offsets, k_pool, v_pool, k_s
                      window: int = 0, softcap: float = 0.0, slopes=None, prefix_lens=None) -> None:
     """pa_extend with scores capped by softcap (0: not), a bias that falls with distance (slopes
     [Hq] fp32) and prefixes that see all of themselves (prefix_lens [B] int32)."""
-    score = pa_score(float(softcap), _array_ptr("slopes", slopes, "torch.float32", shape.Hq, True),
-                     _array_ptr("prefix_lens", prefix_lens, "torch.int32", shape.B))
+    score = pa_score(float(softcap), _array_ptr("slopes", slopes, shape.Hq, True),
+                     _array_ptr("prefix_lens", prefix_lens, shape.B))
     _check("pa_extend_scored", load().pa_extend_scored(
         ctypes.byref(shape), _ptr(out), _ptr(q),
-        _array_ptr("query_offsets", query_offsets, "torch.int32", shape.B + 1), int(q.shape[0]),
+        _array_ptr("query_offsets", query_offsets, shape.B + 1), int(q.shape[0]),
         _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale), _ptr(block_tables),
         _ptr(seq_lens), int(window), ctypes.byref(score), float(sm_scale), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(err_flag), _stream(stream)))
+        workspace.nbytes, _ptr(err_flag), _stream(stream)))
 
 
 def pa_decode_scored(shape: pa_shape, out, q, k_pool, v_pool, k_scale, v_scale, block_tables,
@@ -380,11 +390,11 @@ def pa_decode_scored(shape: pa_shape, out, q, k_pool, v_pool, k_scale, v_scale, 
                      num_segments: int = 0) -> None:
     """One token per sequence with changed scores: q, out [B, Hq, D] bf16; workspace: uint8 tensor
     of pa_decode_workspace_bytes(shape, num_segments or pa_default_num_segments)."""
-    score = pa_score(float(softcap), _array_ptr("slopes", slopes, "torch.float32", shape.Hq, True), None)
+    score = pa_score(float(softcap), _array_ptr("slopes", slopes, shape.Hq, True), None)
     _check("pa_decode_scored", load().pa_decode_scored(
         ctypes.byref(shape), _ptr(out), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
         _ptr(v_scale), _ptr(block_tables), _ptr(seq_lens), int(window), ctypes.byref(score),
-        float(sm_scale), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        float(sm_scale), _ptr(workspace), workspace.nbytes,
         int(num_segments), _ptr(err_flag), _stream(stream)))
 
 
@@ -404,11 +414,12 @@ def pa_rope_axes_and_cache(shape: pa_shape, pair_axis, cos_sin, positions, q_out
     pair_axis = bytes(pair_axis)
     if len(pair_axis) != width // 2 or positions.dim() != 2 or positions.shape[1] != shape.B:
         raise ValueError("pair_axis has rotary_dim / 2 entries, positions is [num_axes, tokens]")
-    positions_ptr = _array_ptr("positions", positions, "torch.int32", positions.numel())
+    if positions.dtype is not _dtypes()[0]:
+        raise ValueError("positions: int32")
     rope = _rope(width, bool(interleaved), rows, qs, ks, vs)
     axes = _rope_axes(int(positions.shape[0]), pair_axis)
     _check("pa_rope_axes_and_cache", lib.pa_rope_axes_and_cache(
-        ctypes.byref(shape), ctypes.byref(rope), ctypes.byref(axes), _ptr(cos_sin), positions_ptr,
+        ctypes.byref(shape), ctypes.byref(rope), ctypes.byref(axes), _ptr(cos_sin), _ptr(positions),
         _ptr(q_out), qp, kp, vp, _ptr(k_pool), _ptr(v_pool), _ptr(k_scale), _ptr(v_scale),
         _ptr(slot_mapping), _ptr(err_flag), _stream(stream)))
 
@@ -418,14 +429,14 @@ def pa_read_cache(shape: pa_shape, k_out, v_out, k_pool, v_pool, k_scale, v_scal
     """k_out, v_out: [total_tokens, Hkv, D] bf16 (either may be None); offsets: [B + 1] int32;
     starts: [B] int32, None: position 0."""
     out = v_out if k_out is None else k_out
-    tokens = 0 if out is None else int(out.shape[0])
-    if k_out is not None and v_out is not None and int(v_out.shape[0]) != tokens:
+    tokens = 0 if out is None else out.shape[0]
+    if k_out is not None and v_out is not None and v_out.shape[0] != tokens:
         raise ValueError("k_out and v_out have the same number of rows")
     _check("pa_read_cache", load().pa_read_cache(
         ctypes.byref(shape), _ptr(k_out), _ptr(v_out), _ptr(k_pool), _ptr(v_pool), _ptr(k_scale),
         _ptr(v_scale), _ptr(block_tables), _ptr(seq_lens),
-        _array_ptr("offsets", offsets, "torch.int32", shape.B + 1), tokens,
-        _array_ptr("starts", starts, "torch.int32", shape.B), _ptr(err_flag), _stream(stream)))
+        _array_ptr("offsets", offsets, shape.B + 1), tokens,
+        _array_ptr("starts", starts, shape.B), _ptr(err_flag), _stream(stream)))
 
 
 def pa_attend_workspace_bytes(shape: pa_shape, total_queries: int, sm_count: int) -> int:
