@@ -48,10 +48,14 @@
 // their number: unrolled over a tile's 128 columns as the plain softmax is, four capped prompts of
 // 1,210 to 2,400 tokens took 662 us, two threads a row 711, two forms of the polynomial side by side
 // 832; in loops over 64 columns that read a tile twice 597, with four coefficients where the scores are
-// small 561 (plain scores: 387).  The chunk with a cap takes 1.21 ms, 945 TFLOP/s: 13 fp32
-// operations a score (at 2 cycles a pair), of them the polynomial 8.  With a distance bias it takes
-// 0.82 ms, within 2 % of plain scores: tiles run last to first, so that the reference maximum is
-// found at once (before: 1.29 ms), and the bias is one addition a pair.
+// small 561 (plain scores: 387).  A capped weight takes 6 packed fp32 operations a pair of scores with
+// four coefficients, 8 with six (the sum's addition among them; code pools one more each), at 2 cycles
+// each, beside 8 cycles of exponentials.  What a cap costs depends on the scores: a block of 32 rows by
+// 32 keys with one past half the cap takes six coefficients, with one past the cap the exponential form,
+// which computes both for every score.  Scores with a standard deviation of 6, prompts / chunk: cap 50
+// 0.56 / 1.20 ms (949 TFLOP/s), cap 30 0.61 / 1.36, cap 20 1.05 / 2.17.  With a distance bias they take
+// 0.41 / 0.82 ms, the chunk 2 to 5 % more than plain scores: tiles run last to first, so that the
+// reference maximum is found at once (before: 1.29 ms), and the bias is one addition a pair.
 #pragma once
 
 #include <cudaTypedefs.h>
@@ -1236,8 +1240,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // the sum would lose the page's weights.  So the exponent takes a scale down to 2^-24 only, and
             // what is below that, a power of two, multiplies the rounded weights, in the slow form: where
             // no scale is that small, the vote for it takes E4M3 chunks with a window from 264 to 269 us, the
-            // loops doing it themselves took 283.  Weights down to 2^-40 of
-            // the row's largest count, and a row with a reference has a sum above 0, which a jump asks for.
+            // loops doing it themselves took 283.  Weights down to 2^-40 of the row's largest count, and a
+            // row with a reference has a sum above 0, which a jump asks for.
             if (slow) {
 #pragma unroll 1
               for (int page = 0; page < 8; ++page) {

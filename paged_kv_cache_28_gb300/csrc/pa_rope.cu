@@ -44,10 +44,10 @@ struct RopeParams {
 };
 
 // How many axes the positions have, and whether pairs 4 i .. 4 i + 3 share theirs, so that their
-// angles lie side by side in the table: a kernel for each.  9,485 tokens into an E4M3 cache take 107 us
-// with one axis, 121 with three in fours, 135 with three in turn.  The bf16 kernels, which load
-// each angle for several heads, take them pair by pair (16,384 tokens: 109 us with one axis, 115 to
-// 119 with three either way).
+// angles lie side by side in the table: a kernel for each.  8,726 tokens into an E4M3 cache take 102 us
+// with one axis, 115 with three in fours, 130 with three in turn.  The bf16 kernels, which load
+// each angle for several heads, take them pair by pair (16,384 tokens: 104 us with one axis, 109 to
+// 113 with three either way).
 constexpr int kOneAxis = 0, kInFours = 1, kAnyPair = 2;
 
 // The rows of the table that a token's pairs turn by: one, or one for each axis.
