@@ -19,7 +19,7 @@ pa_status run_attend_scored(const ScoredCall &x) {
   p.prefix_lens = x.score.prefix_lens;
   if (kScore & kCap) {
     // (0 with sm_scale 0, whatever the products)
-    p.c = fabsf(x.sm_scale / x.score.softcap);
+    p.c = fabsf(scale_over_cap(x.sm_scale, x.score.softcap));
     p.cap2 = x.score.softcap * kLog2e;
     // tanh's coefficients; on bf16 pools with c^(2 i + 1) in them, as far as fp32 holds all of them: six
     // for c >= 2^-11 (heads of 128: caps up to 180), four for scores up to half the cap to 2^-16 (caps

@@ -118,7 +118,7 @@ pa_status run_decode_scored(const pa_shape &s, void *out, const void *q, const v
                          err);
   p.window = window;
   if (score.softcap > 0.f) {
-    p.sl2 = sm_scale / score.softcap;
+    p.sl2 = scale_over_cap(sm_scale, score.softcap);
     p.cap2 = score.softcap * kLog2e;
   }
   p.slopes = score.slopes;

@@ -1,6 +1,8 @@
 // pa_score.cuh -- the capped score of pa_extend_scored and pa_decode_scored.
 #pragma once
 
+#include <cmath>
+
 #include "pa_common.cuh"
 
 namespace pa {
@@ -29,6 +31,12 @@ __device__ __forceinline__ float tanh_within_1(float t) {
 __device__ __forceinline__ float tanh_any(float t) {
   const float far = 1.f - __fdividef(2.f, 1.f + ex2(t * (2.f * kLog2e)));
   return fabsf(t) <= 1.f ? tanh_within_1(t) : far;
+}
+
+// What a product is multiplied by under a cap, kept where its own products with a pool's scales are finite, so
+// that a product of 0 scores 0; a score that this bounds lies far past its cap (products above 1e-19).
+inline float scale_over_cap(float sm_scale, float softcap) {
+  return fminf(fmaxf(sm_scale / softcap, -1e20f), 1e20f);
 }
 
 // A slope in the log2 domain, kept where its product with any distance is finite: a key that is
